@@ -394,6 +394,98 @@ gptq_status gptq_dequant_gemm(const uint32_t* packed, int64_t m, int64_t n, int6
                               int group_size, const int32_t* g_idx, const uint16_t* X, int64_t batch,
                               int64_t ldx, float* Y, int64_t ldy, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled weights (MXFP4), a second low-bit format next to the integer
+ * codes above (Wiki "GPTQ", "Technical Approach": a low-bit grid whose groups
+ * have their own scaling factor; here the grid is a 4-bit floating-point one
+ * and the factor a power of two, which the matrix cores of gfx950 take as
+ * stored).
+ *   codes   4-bit e2m1: bit 3 the sign, bits 0-2 the magnitude 0, 0.5, 1, 1.5,
+ *           2, 3, 4, 6; stored in gptq_pack's 4-bit layout (the code of column
+ *           k occupies bits [4k, 4k + 4) of its row of uint32 words;
+ *           ceil(n/8) words to a row).
+ *   scales  one e8m0 byte for every 32 consecutive columns of a row
+ *           (ceil(n/32) bytes to a row; the last block may be shorter): the
+ *           factor 2^(byte - 127); byte 255 is NaN.
+ * Sizes for all calls: 0 <= n <= 2^20, others return GPTQ_ERR_UNSUPPORTED.
+ * Rows may start at any element-aligned address.
+ * ---------------------------------------------------------------------- */
+#define GPTQ_MX_MAX_ROWS 1048576     /* rows of W and of X in a product */
+#define GPTQ_MX_MAX_EXPERTS 65536
+
+/* Round-to-nearest quantization of W (weights, or activations on their way
+ * into gptq_mx_scaled_gemm) in blocks of 32 columns:
+ *   byte = max(floor(log2 max|w|) - 2, -127) + 127,
+ *   code = the e2m1 value nearest to w / 2^(byte - 127), ties to the even
+ *          code, magnitudes above 6 to 6 (blocks whose largest |w| lies in
+ *          (6, 8) / 4 of its power of two saturate there).
+ * A block of zeros gets byte 127; a block that holds a NaN or an infinity gets
+ * byte 255 and codes 0 (all its values are NaN).
+ *   W       device, m x n, element type w_dtype, leading dimension ldw >= n.
+ *   packed  device, m x ld_packed uint32 output, ld_packed >= ceil(n/8); unused
+ *           bits of a row's last word are 0, words beyond it are not written.
+ *   scales  device, m x ld_scales uint8 output, ld_scales >= ceil(n/32).
+ *   Wq      device, m x n output (ldwq >= n) of the quantized values in
+ *           w_dtype (exact), or NULL.  Must not overlap W.
+ * m < 2^31. */
+gptq_status gptq_mx_quantize(const void* W, int w_dtype, int64_t m, int64_t n, int64_t ldw,
+                             uint32_t* packed, int64_t ld_packed, uint8_t* scales, int64_t ld_scales,
+                             void* Wq, int64_t ldwq, void* stream);
+
+/* Y[b, r] = sum_k What[r, k] X[b, k] for microscaled weights What (m x n) and
+ * 16-bit activations, any batch >= 0.
+ *   packed, scales  device, as gptq_mx_quantize writes them (codes past column
+ *                   n in a row's last word are ignored).
+ *   X       device, batch x n (ldx >= n), x_dtype GPTQ_F16 or GPTQ_BF16.
+ *   Y       device, batch x m output (ldy >= m), y_dtype GPTQ_F32, GPTQ_F16 or
+ *           GPTQ_BF16.  Must not overlap the inputs.
+ *   ws      device workspace of gptq_mx_gemm_ws_bytes(m, n, batch, 1) bytes
+ *           (NULL allowed when that is 0), in use until the call's work on
+ *           `stream` is done: calls that may run at the same time (two streams,
+ *           two captured graphs) need one each.
+ * Products are exact in float32 and accumulation is float32, in an order that
+ * depends on the sizes alone (the same call gives the same bits): the error
+ * before the one rounding to y_dtype is at most (n/32 + 80) 2^-23
+ * sum_k |What[r, k] X[b, k]|, unless that sum passes float32's range.  A weight
+ * value outside float32's range counts as infinite.  Non-finite weights or X make the outputs that they enter
+ * non-finite.  With n = 0, Y is 0. */
+size_t gptq_mx_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, int64_t experts);
+gptq_status gptq_mx_gemm(const uint32_t* packed, int64_t m, int64_t n, int64_t ld_packed,
+                         const uint8_t* scales, int64_t ld_scales, const void* X, int x_dtype,
+                         int64_t batch, int64_t ldx, void* Y, int y_dtype, int64_t ldy,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* The same product grouped by expert: rows offsets[e] .. offsets[e+1] - 1 of X
+ * are multiplied with expert e's weights,
+ *   Y[t, r] = sum_k What_e[r, k] X[t, k],  offsets[e] <= t < offsets[e+1].
+ *   packed, scales  device, `experts` matrices of m rows; expert e's first row
+ *                   is at packed + e * stride_packed, scales + e *
+ *                   stride_scales (strides >= m * leading dimension).
+ *   X       device, `rows` rows sorted by expert; Y likewise.
+ *   offsets device, experts + 1 int32, ascending.  Experts without rows are
+ *           fine; rows of Y outside [offsets[0], offsets[experts]) are left as
+ *           they were.  Offsets are read on the device and confined to
+ *           [0, rows] there; offsets that descend leave it undefined which rows
+ *           are computed, and nothing outside Y is written.
+ *   ws      gptq_mx_gemm_ws_bytes(m, n, rows, experts) bytes, as above.
+ * experts <= GPTQ_MX_MAX_EXPERTS. */
+gptq_status gptq_mx_gemm_grouped(const uint32_t* packed, int64_t experts, int64_t m, int64_t n,
+                                 int64_t ld_packed, int64_t stride_packed, const uint8_t* scales,
+                                 int64_t ld_scales, int64_t stride_scales, const void* X, int x_dtype,
+                                 int64_t rows, int64_t ldx, const int32_t* offsets, void* Y, int y_dtype,
+                                 int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* Y = Xhat What^T with both operands microscaled (X quantized by
+ * gptq_mx_quantize): the scaled 4-bit matrix instructions, float32
+ * accumulation, the error bound of gptq_mx_gemm.
+ *   x_packed, x_scales  device, batch rows of ceil(n/8) words (ld_xpacked) and
+ *                       ceil(n/32) bytes (ld_xscales). */
+gptq_status gptq_mx_scaled_gemm(const uint32_t* packed, int64_t m, int64_t n, int64_t ld_packed,
+                                const uint8_t* scales, int64_t ld_scales, const uint32_t* x_packed,
+                                int64_t batch, int64_t ld_xpacked, const uint8_t* x_scales,
+                                int64_t ld_xscales, void* Y, int y_dtype, int64_t ldy,
+                                void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

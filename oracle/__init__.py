@@ -37,4 +37,15 @@ from .gptq_oracle import (  # noqa: F401
     lora_refine,
     gptq_layer,
 )
+from .mx_oracle import (  # noqa: F401,E402
+    MX_BLOCK,
+    MX_VALUES,
+    mx_block_byte,
+    mx_blocks,
+    mx_dequantize,
+    mx_matmul,
+    mx_matmul_bound,
+    mx_nearest_code,
+    mx_quantize,
+)
 from . import decoder_oracle  # noqa: F401,E402

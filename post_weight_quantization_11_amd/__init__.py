@@ -18,11 +18,17 @@ from ._lib import (  # noqa: F401
     gptq_lowrank_basis,
     gptq_lowrank_compensation,
     gptq_lowrank_hessian,
+    gptq_mx_gemm,
+    gptq_mx_gemm_grouped,
+    gptq_mx_quantize,
+    gptq_mx_scaled_gemm,
     gptq_pack,
     gptq_prepare_hinv,
     gptq_quantize_layer,
     gptq_quantize_linear,
     gptq_refine_codes,
     load,
+    mx_scales,
+    mx_words,
     packed_words,
 )

@@ -44,10 +44,16 @@ EXPORTS = (
     "gptq_lowrank_compensation",
     "gptq_refine_ws_bytes",
     "gptq_refine_codes",
+    "gptq_mx_quantize",
+    "gptq_mx_gemm_ws_bytes",
+    "gptq_mx_gemm",
+    "gptq_mx_gemm_grouped",
+    "gptq_mx_scaled_gemm",
 )
 
 GEMV_MAX_BATCH = 8   # X rows per pass of the VALU product kernel
 LOWRANK_MAX_RANK = 64
+MX_BLOCK = 32        # columns that share a scale of a microscaled matrix
 
 _lib = None
 
@@ -115,6 +121,17 @@ def load(path: str = LIB_PATH):
     lib.gptq_refine_codes.restype = C
     lib.gptq_refine_codes.argtypes = [vp, C, i64, i64, i64, vp, i64, vp, vp, i64, i64, vp, vp, C, vp, C, C, vp, vp,
                                       vp, sz, vp]
+    lib.gptq_mx_quantize.restype = C
+    lib.gptq_mx_quantize.argtypes = [vp, C, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.gptq_mx_gemm_ws_bytes.restype = sz
+    lib.gptq_mx_gemm_ws_bytes.argtypes = [i64, i64, i64, i64]
+    lib.gptq_mx_gemm.restype = C
+    lib.gptq_mx_gemm.argtypes = [vp, i64, i64, i64, vp, i64, vp, C, i64, i64, vp, C, i64, vp, sz, vp]
+    lib.gptq_mx_gemm_grouped.restype = C
+    lib.gptq_mx_gemm_grouped.argtypes = [vp, i64, i64, i64, i64, i64, vp, i64, i64, vp, C, i64, i64, vp, vp, C, i64,
+                                         vp, sz, vp]
+    lib.gptq_mx_scaled_gemm.restype = C
+    lib.gptq_mx_scaled_gemm.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, C, i64, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -352,6 +369,207 @@ def gptq_dequant_gemm(packed, scales, zeros, X, n: int, bits: int, group_size: i
                                int(G), int(group_size), _ptr(g_idx), _ptr(X), batch, X.stride(0), _ptr(Y),
                                Y.stride(0), _stream(stream))
     _check(rc, "gptq_dequant_gemm")
+    return Y
+
+
+# ---------------------------------------------------------------------------
+# Microscaled weights (MXFP4).
+# ---------------------------------------------------------------------------
+class _on_device:
+    """Makes a tensor's device current and, when one is given, `stream`: the
+    outputs and the workspace a call allocates then belong to the stream that
+    uses them.  Enters as the stream's handle."""
+
+    def __init__(self, t, stream):
+        torch = _torch()
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+            self._ctx = torch.cuda.stream(stream)
+        elif t.device.index != torch.cuda.current_device():
+            self._ctx = torch.cuda.device(t.device)
+        else:
+            self._ctx = None
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _mx_tensor(t, name: str, dtype, shape, device):
+    """A device tensor of the given type and shape whose last axis is dense."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+
+
+def _ld(t, axis: int = 0):
+    """Leading dimension (the stride of a single row means nothing)."""
+    return t.stride(axis) if t.shape[axis] > 1 else t.shape[-1]
+
+
+def _mx_output(Y, y_dtype, shape, like):
+    torch = _torch()
+    if Y is None:
+        return torch.empty(shape, dtype=torch.float32 if y_dtype is None else y_dtype, device=like.device)
+    _mx_tensor(Y, "Y", Y.dtype if y_dtype is None else y_dtype, shape, like.device)
+    return Y
+
+
+def _mx_workspace(ws, m: int, n: int, rows: int, experts: int, device):
+    if ws is not None:
+        if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous on {device}")
+        return ws, ws.numel() * ws.element_size()
+    ws = _workspace(load().gptq_mx_gemm_ws_bytes(m, n, rows, experts), device)
+    return ws, 0 if ws is None else ws.numel()
+
+
+def _mx_x(X):
+    torch = _torch()
+    _rows_check(X)
+    if X.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("X must be float16 or bfloat16")
+
+
+def _y_code(Y) -> int:
+    try:
+        return _dtype_code(Y)
+    except KeyError:
+        raise ValueError("Y must be float32, float16 or bfloat16") from None
+
+
+def mx_words(n: int) -> int:
+    """Packed words of a microscaled row of n columns."""
+    return -(-n // 8)
+
+
+def mx_scales(n: int) -> int:
+    """Scale bytes of a microscaled row of n columns."""
+    return -(-n // MX_BLOCK)
+
+
+def gptq_mx_quantize(W, want_wq: bool = False, out=None, stream=None):
+    """Rounds W (m x n, or a stack experts x m x n; float32, float16 or
+    bfloat16) to microscaled 4-bit floats in blocks of 32 columns.
+
+    Returns dict(packed (... x m x ceil(n/8) int32 words: bit patterns of
+    uint32, the code of column k at bits [4k, 4k + 4) of its row), scales
+    (... x m x ceil(n/32) uint8, 2^(byte - 127)), Wq (W's shape and dtype, the
+    quantized values) or None).  `out` may hold those tensors."""
+    torch = _torch()
+    lib = load()
+    if not W.is_cuda or W.dim() not in (2, 3) or (W.shape[-1] > 1 and W.stride(-1) != 1):
+        raise ValueError("W must be a 2-D or 3-D device tensor with unit column stride")
+    if W.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError("W must be float32, float16 or bfloat16")
+    lead, n = W.shape[:-1], W.shape[-1]
+    with _on_device(W, stream) as st:
+        if out is None:
+            out = dict(packed=torch.empty((*lead, mx_words(n)), dtype=torch.int32, device=W.device),
+                       scales=torch.empty((*lead, mx_scales(n)), dtype=torch.uint8, device=W.device),
+                       Wq=torch.empty(W.shape, dtype=W.dtype, device=W.device) if want_wq else None)
+        else:
+            out.setdefault("Wq", None)
+            _mx_tensor(out["packed"], "packed", torch.int32, (*lead, mx_words(n)), W.device)
+            _mx_tensor(out["scales"], "scales", torch.uint8, (*lead, mx_scales(n)), W.device)
+            if out["Wq"] is not None:
+                _mx_tensor(out["Wq"], "Wq", W.dtype, W.shape, W.device)
+        dense = []
+        for t in (W, out["packed"], out["scales"], out["Wq"]):
+            if t is not None and t.dim() == 3:
+                if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) != t.shape[1] * _ld(t, 1):
+                    raise ValueError("stacked matrices must follow one another row by row")
+                t = t.as_strided((t.shape[0] * t.shape[1], t.shape[2]), (_ld(t, 1), 1))
+            dense.append(t)
+        w, packed, scales, wq = dense
+        rc = lib.gptq_mx_quantize(_ptr(w), _dtype_code(w), w.shape[0], n, _ld(w), _ptr(packed), _ld(packed),
+                                  _ptr(scales), _ld(scales), _ptr(wq), 0 if wq is None else _ld(wq), st)
+    _check(rc, "gptq_mx_quantize")
+    return out
+
+
+def gptq_mx_gemm(packed, scales, X, Y=None, y_dtype=None, ws=None, stream=None):
+    """Y (batch x m; float32, or y_dtype) = X W^T with microscaled weights
+    (packed m x ceil(n/8) int32 words, scales m x ceil(n/32) uint8, as
+    gptq_mx_quantize returns them) and X batch x n float16 or bfloat16 (any
+    leading dimension)."""
+    torch = _torch()
+    lib = load()
+    _mx_x(X)
+    batch, n = X.shape
+    m = packed.shape[0]
+    _mx_tensor(packed, "packed", torch.int32, (m, mx_words(n)), X.device)
+    _mx_tensor(scales, "scales", torch.uint8, (m, mx_scales(n)), X.device)
+    with _on_device(X, stream) as st:
+        Y = _mx_output(Y, y_dtype, (batch, m), X)
+        yc = _y_code(Y)
+        ws, ws_bytes = _mx_workspace(ws, m, n, batch, 1, X.device)
+        rc = lib.gptq_mx_gemm(_ptr(packed), m, n, _ld(packed), _ptr(scales), _ld(scales), _ptr(X), _dtype_code(X),
+                              batch, _ld(X), _ptr(Y), yc, _ld(Y), _ptr(ws), ws_bytes, st)
+    _check(rc, "gptq_mx_gemm")
+    return Y
+
+
+def gptq_mx_gemm_grouped(packed, scales, X, offsets, Y=None, y_dtype=None, ws=None, stream=None):
+    """Rows offsets[e] .. offsets[e+1] - 1 of X (rows x n, sorted by expert)
+    times expert e's weights: packed experts x m x ceil(n/8) int32, scales
+    experts x m x ceil(n/32) uint8, offsets experts + 1 int32 (on the device;
+    not read on the host).  Returns Y (rows x m); rows of Y that belong to no
+    expert are left as they were (unset when Y is allocated here)."""
+    torch = _torch()
+    lib = load()
+    _mx_x(X)
+    rows, n = X.shape
+    if packed.dim() != 3:
+        raise ValueError("packed must be experts x m x words")
+    experts, m = packed.shape[:2]
+    _mx_tensor(packed, "packed", torch.int32, (experts, m, mx_words(n)), X.device)
+    _mx_tensor(scales, "scales", torch.uint8, (experts, m, mx_scales(n)), X.device)
+    _mx_tensor(offsets, "offsets", torch.int32, (experts + 1,), X.device)
+    with _on_device(X, stream) as st:
+        Y = _mx_output(Y, y_dtype, (rows, m), X)
+        yc = _y_code(Y)
+        ws, ws_bytes = _mx_workspace(ws, m, n, rows, experts, X.device)
+        rc = lib.gptq_mx_gemm_grouped(_ptr(packed), experts, m, n, _ld(packed, 1), packed.stride(0), _ptr(scales),
+                                      _ld(scales, 1), scales.stride(0), _ptr(X), _dtype_code(X), rows, _ld(X),
+                                      _ptr(offsets), _ptr(Y), yc, _ld(Y), _ptr(ws), ws_bytes, st)
+    _check(rc, "gptq_mx_gemm_grouped")
+    return Y
+
+
+def gptq_mx_scaled_gemm(packed, scales, x_packed, x_scales, n: int, Y=None, y_dtype=None, ws=None, stream=None):
+    """Y (batch x m; float32, or y_dtype) = X^ W^T with both operands
+    microscaled: gptq_mx_quantize's packed and scales of the weights (m rows)
+    and of X (batch rows), n columns each."""
+    torch = _torch()
+    lib = load()
+    n = int(n)
+    m, batch = packed.shape[0], x_packed.shape[0]
+    if not packed.is_cuda:
+        raise ValueError("packed must be a device tensor")
+    _mx_tensor(packed, "packed", torch.int32, (m, mx_words(n)), packed.device)
+    _mx_tensor(scales, "scales", torch.uint8, (m, mx_scales(n)), packed.device)
+    _mx_tensor(x_packed, "x_packed", torch.int32, (batch, mx_words(n)), packed.device)
+    _mx_tensor(x_scales, "x_scales", torch.uint8, (batch, mx_scales(n)), packed.device)
+    with _on_device(packed, stream) as st:
+        Y = _mx_output(Y, y_dtype, (batch, m), packed)
+        yc = _y_code(Y)
+        ws, ws_bytes = _mx_workspace(ws, m, n, batch, 1, packed.device)
+        rc = lib.gptq_mx_scaled_gemm(_ptr(packed), m, n, _ld(packed), _ptr(scales), _ld(scales), _ptr(x_packed),
+                                     batch, _ld(x_packed), _ptr(x_scales), _ld(x_scales), _ptr(Y), yc, _ld(Y),
+                                     _ptr(ws), ws_bytes, st)
+    _check(rc, "gptq_mx_scaled_gemm")
     return Y
 
 

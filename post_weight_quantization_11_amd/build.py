@@ -36,6 +36,7 @@ EXTRA_FLAGS = {
     "lowrank.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "prepare.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "mx_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -1,0 +1,585 @@
+"""Microscaled operators on the GPU against the float64 oracle.
+
+Quantization is exact: bytes, codes and dequantized values must be equal.
+Products: the terms are exact in float32, so the error before the rounding to
+Y's type is at most oracle.mx_matmul_bound (n/32 + 80 additions of one unit
+2^-23 of sum |terms|); a 16-bit Y adds half a unit of its type (2^-8 relative
+for bfloat16, 2^-11 for float16, at least 2^-25 absolute there)."""
+import numpy as np
+import pytest
+
+import oracle
+from tests.gpu_util import log
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def g(gpu_lib):
+    import post_weight_quantization_11_amd as g
+    return g
+
+
+def _dt(name):
+    import torch
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[name]
+
+
+def _rng(*seed):
+    return np.random.Generator(np.random.PCG64(np.random.SeedSequence(list(seed))))
+
+
+def _to(a, dtype, cols=None):
+    """Device tensor of `dtype` (and its float64 values); `cols`: leading dimension."""
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(_dt(dtype))
+    if cols is not None:
+        buf = torch.full((t.shape[0], cols), float("nan"), dtype=t.dtype)
+        buf[:, :t.shape[1]] = t
+        d = buf.cuda()[:, :t.shape[1]]
+    else:
+        d = t.cuda()
+    return d, t.double().numpy()
+
+
+def _weights(rng, m, n, lo=110, hi=125):
+    """Random codes and scale bytes in [lo, hi]."""
+    return rng.integers(0, 16, size=(m, n)), rng.integers(lo, hi + 1, size=(m, oracle.mx_blocks(n)))
+
+
+def _packed(codes, scale, words=None, bytes_=None):
+    """Device tensors of packed codes and bytes; words, bytes_: leading
+    dimensions, the padding filled with ones."""
+    import torch
+    p = oracle.pack_codes(codes, 4).astype(np.uint32)
+    nw = -(-codes.shape[1] // 8)
+    pb = np.full((p.shape[0], words or nw), 0xFFFFFFFF, dtype=np.uint32)
+    pb[:, :nw] = p[:, :nw]
+    sb = np.full((p.shape[0], bytes_ or scale.shape[1]), 255, dtype=np.uint8)
+    sb[:, :scale.shape[1]] = scale
+    return (torch.from_numpy(pb.view(np.int32)).cuda()[:, :nw],
+            torch.from_numpy(sb).cuda()[:, :scale.shape[1]])
+
+
+def _tol(n, mags, want, out):
+    t = oracle.mx_matmul_bound(n, mags)
+    if out == "bf16":
+        t = t + 2.0 ** -8 * (np.abs(want) + t)
+    elif out == "f16":
+        t = t + np.maximum(2.0 ** -11 * (np.abs(want) + t), 2.0 ** -25)
+    return t
+
+
+def _check(Y, want, mags, n, out, what):
+    got = Y.double().cpu().numpy()
+    assert got.shape == want.shape
+    tol = _tol(n, mags, want, out)
+    # The bound is float32's without overflow: a partial sum can be as large as
+    # the sum of the magnitudes, so where that passes float32's largest value
+    # (2^128 (1 - 2^-24)) an infinity or, from two of them, a NaN is the
+    # float32 result.  Those entries must be few and are left out.
+    over = mags + tol > float(np.finfo(np.float32).max)
+    assert np.mean(over) < 0.5
+    with np.errstate(invalid="ignore"):
+        err = np.where(over, 0.0, np.abs(got - want))
+    log(f"  {what}: max |err| / tol {float(np.max(err / np.maximum(tol, 1e-300), initial=0.0)):.3e}")
+    assert np.all(err <= tol)
+
+
+# ---------------------------------------------------------------------------
+# Quantization.
+# ---------------------------------------------------------------------------
+def _unpack(q, n):
+    words = q["packed"].cpu().numpy().view(np.uint32)
+    return oracle.unpack_codes(words, n, 4).astype(np.int64), q["scales"].cpu().numpy().astype(np.int64)
+
+
+def _check_quantized(q, W64, n, dtype):
+    codes, scale = oracle.mx_quantize(W64)
+    gc, gs = _unpack(q, n)
+    assert np.array_equal(gs, scale)
+    assert np.array_equal(gc, codes)
+    words = q["packed"].cpu().numpy().view(np.uint32)
+    if n % 8:
+        assert not np.any(words[:, -1] >> np.uint32(4 * (n % 8)))
+    if q["Wq"] is not None:
+        v = oracle.mx_dequantize(codes, scale)
+        got = q["Wq"].double().cpu().numpy()
+        assert np.array_equal(np.isnan(got), np.isnan(v))
+        assert np.array_equal(got[~np.isnan(v)], v[~np.isnan(v)])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n,ld", [(1, 1, None), (3, 31, None), (2, 32, None), (5, 33, None), (256, 256, None),
+                                    (17, 1000, None), (9, 1031, 1037), (300, 64, 72), (1, 20001, None)])
+def test_quantize_matches_oracle(g, dtype, m, n, ld):
+    rng = _rng(m, n, 1)
+    W, W64 = _to(rng.standard_normal((m, n)) * 0.02 * np.exp(rng.standard_normal((m, 1))), dtype, ld)
+    for want_wq in (False, True):
+        _check_quantized(g.gptq_mx_quantize(W, want_wq=want_wq), W64, n, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_quantize_every_binade_ties_and_special_blocks(g, dtype):
+    import torch
+    # One block per power of two of the type's range, its values the grid
+    # points, the midpoints, one step of the type to either side of each, and
+    # the largest value below the next power; then zeros, signed zeros, NaN,
+    # infinities and the smallest subnormal.
+    t = _dt(dtype)
+    info = torch.finfo(t)
+    lo = {"f32": -149, "f16": -24, "bf16": -133}[dtype]
+    hi = {"f32": 127, "f16": 15, "bf16": 127}[dtype]
+    base = np.array([0.0, 0.25, 0.5, 0.75, 1.0, 1.25, 1.5, 1.75, 2.0, 2.5, 3.0, 3.5, 4.0, 5.0, 6.0, 7.0])
+    step = float(info.eps)
+    near = np.concatenate([base, base[1:] * (1 - step / 2), [4.0]])          # 32 values below 8
+    near2 = np.concatenate([base[:15], base[1:14] * (1 + step), [-5.0, -3.5, -0.25, 4.0]])
+    rows = []
+    for e in range(lo, hi - 1):
+        for v in (near, near2):
+            rows.append(np.ldexp(v, e))
+    rows += [np.zeros(32), np.full(32, -0.0), np.r_[np.nan, np.ones(31)], np.r_[np.ones(31), np.inf],
+             np.r_[-np.inf, np.zeros(31)], np.r_[np.ldexp(1.0, lo), np.zeros(31)], np.full(32, float(info.max))]
+    with np.errstate(over="ignore"):
+        a64 = np.stack(rows)
+        W = torch.from_numpy(a64).to(t)
+    q = g.gptq_mx_quantize(W.cuda(), want_wq=True)
+    _check_quantized(q, W.double().numpy(), 32, dtype)
+
+
+def test_quantize_writes_only_its_elements(g):
+    import torch
+    rng = _rng(3)
+    W, W64 = _to(rng.standard_normal((5, 45)), "bf16", 50)
+    packed = torch.full((5, 9), -1, dtype=torch.int32, device="cuda")
+    scales = torch.full((5, 5), 9, dtype=torch.uint8, device="cuda")
+    wq = torch.full((5, 47), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = dict(packed=packed[:, :6], scales=scales[:, :2], Wq=wq[:, :45])
+    _check_quantized(g.gptq_mx_quantize(W, out=out), W64, 45, "bf16")
+    assert (packed[:, 6:] == -1).all() and (scales[:, 2:] == 9).all() and (wq[:, 45:] == 3.0).all()
+
+
+def test_quantize_stack_of_experts(g):
+    import torch
+    rng = _rng(4)
+    W, W64 = _to(rng.standard_normal((6 * 10, 70)), "f16")
+    q = g.gptq_mx_quantize(W.view(6, 10, 70), want_wq=True)
+    assert q["packed"].shape == (6, 10, 9) and q["scales"].shape == (6, 10, 3) and q["Wq"].shape == (6, 10, 70)
+    _check_quantized({k: v.reshape(60, -1) for k, v in q.items()}, W64, 70, "f16")
+    with pytest.raises(ValueError):
+        g.gptq_mx_quantize(W.view(6, 10, 70)[::2])          # matrices apart from one another
+    with pytest.raises(ValueError):
+        g.gptq_mx_quantize(W.t())
+    with pytest.raises(ValueError):
+        g.gptq_mx_quantize(W.double())
+    for shape in ((0, 70), (5, 0)):
+        q = g.gptq_mx_quantize(torch.empty(shape, device="cuda"))
+        assert q["packed"].numel() == 0 and q["scales"].numel() == 0
+
+
+def test_quantize_many_rows(g):
+    # More rows than one grid dimension of 65535 workgroups would take.
+    import torch
+    W = torch.randn((700001, 33), device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).bfloat16()
+    q = g.gptq_mx_quantize(W, want_wq=True)
+    at = torch.tensor([0, 1, 65535, 65536, 349999, 700000], device="cuda")
+    sub = {k: q[k][at] for k in q}
+    _check_quantized(sub, W[at].double().cpu().numpy(), 33, "bf16")
+
+
+# ---------------------------------------------------------------------------
+# Products with 16-bit X.
+# ---------------------------------------------------------------------------
+GEMM = [
+    # m, n, batch
+    (1, 1, 1), (16, 128, 1), (17, 33, 2), (40, 7, 3), (70, 1000, 5), (33, 31, 16), (64, 4096, 1), (100, 2049, 17),
+    (256, 256, 64), (130, 640, 33), (515, 515, 130), (300, 1031, 259), (1040, 256, 7), (48, 8200, 40),
+    (272, 1056, 520),
+]
+
+
+@pytest.mark.parametrize("m,n,batch", GEMM)
+@pytest.mark.parametrize("dtype,out", [("f16", "f32"), ("bf16", "f32"), ("f16", "f16"), ("bf16", "bf16")])
+def test_gemm_matches_oracle(g, m, n, batch, dtype, out):
+    rng = _rng(m, n, batch)
+    codes, scale = _weights(rng, m, n)
+    X, X64 = _to(rng.standard_normal((batch, n)), dtype)
+    packed, scales = _packed(codes, scale)
+    Y = g.gptq_mx_gemm(packed, scales, X, y_dtype=_dt(out))
+    assert Y.dtype == _dt(out)
+    want, mags = oracle.mx_matmul(codes, scale, X64)
+    _check(Y, want, mags, n, out, f"gemm {batch}x{m}x{n} {dtype}->{out}")
+
+
+@pytest.mark.parametrize("m,n,batch", [(37, 70, 3), (300, 515, 70), (530, 999, 300), (64, 512, 20)])
+def test_gemm_strided_operands_and_padding(g, m, n, batch):
+    # Leading dimensions of their own, padding that must not be read (NaN in X,
+    # ones in the packed words, NaN scales) or written.
+    import torch
+    rng = _rng(m, n, batch, 7)
+    codes, scale = _weights(rng, m, n)
+    X, X64 = _to(rng.standard_normal((batch, n)), "bf16", n + 3)
+    packed, scales = _packed(codes, scale, words=-(-n // 8) + 3, bytes_=oracle.mx_blocks(n) + 1)
+    buf = torch.full((batch, m + 5), 4.0, device="cuda")
+    Y = g.gptq_mx_gemm(packed, scales, X, Y=buf[:, :m])
+    want, mags = oracle.mx_matmul(codes, scale, X64)
+    _check(Y, want, mags, n, "f32", f"strided gemm {batch}x{m}x{n}")
+    assert (buf[:, m:] == 4.0).all()
+
+
+def test_gemm_ignores_codes_past_the_last_column(g):
+    import torch
+    rng = _rng(11)
+    m, n, batch = 35, 45, 6
+    codes, scale = _weights(rng, m, n)
+    X, X64 = _to(rng.standard_normal((batch, n)), "f16")
+    packed, scales = _packed(codes, scale)
+    packed = packed.clone()
+    packed[:, -1] |= torch.tensor(0xFFF00000 - (1 << 32), dtype=torch.int32, device="cuda")   # codes 45 .. 47
+    want, mags = oracle.mx_matmul(codes, scale, X64)
+    _check(g.gptq_mx_gemm(packed, scales, X), want, mags, n, "f32", "garbage codes past n")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,batch", [(40, 300, 4), (200, 320, 100), (280, 330, 300)])
+def test_gemm_wide_scales(g, dtype, m, n, batch):
+    # Scale bytes over the whole finite range of float32's values, mixed
+    # within rows: rows whose terms span hundreds of binades.
+    rng = _rng(13, m)
+    codes = rng.integers(0, 16, size=(m, n))
+    nb = oracle.mx_blocks(n)
+    scale = rng.integers(0, 225, size=(m, nb))
+    scale[:8] = rng.integers(100, 145, size=(8, nb))
+    scale[8] = 104
+    scale[9] = 140
+    scale[10, ::2] = 103
+    scale[11, ::2] = 141
+    X, X64 = _to(rng.standard_normal((batch, n)), dtype)
+    packed, scales = _packed(codes, scale)
+    want, mags = oracle.mx_matmul(codes, scale, X64)
+    # Sums of float32 subnormals round absolutely: n / 32 + 80 steps of 2^-149.
+    Y = g.gptq_mx_gemm(packed, scales, X).double().cpu().numpy()
+    tol = oracle.mx_matmul_bound(n, mags) + (n / 32 + 80) * 2.0 ** -149
+    assert np.all(np.abs(Y - want) <= tol)
+
+
+@pytest.mark.parametrize("batch", [1, 40, 260])
+def test_gemm_nan_scales_zero_blocks_and_non_finite_x(g, batch):
+    rng = _rng(17, batch)
+    m, n = 150, 200
+    codes, scale = _weights(rng, m, n)
+    scale[3, 2] = 255                             # a NaN block: row 3 of W
+    codes[5, :32] = 0
+    scale[5, 0] = 0                               # zeros under the smallest factor
+    x = rng.standard_normal((batch, n))
+    packed, scales = _packed(codes, scale)
+    for dtype in ("f16", "bf16"):
+        X, X64 = _to(x, dtype)
+        Y = g.gptq_mx_gemm(packed, scales, X).double().cpu().numpy()
+        assert np.isnan(Y[:, 3]).all()
+        keep = np.arange(m) != 3
+        scale_ok = np.where(scale == 255, 127, scale)
+        want, mags = oracle.mx_matmul(codes, scale_ok, X64)
+        assert np.all((np.abs(Y - want) <= oracle.mx_matmul_bound(n, mags))[:, keep])
+        # A NaN row of X stays in its row of Y.
+        X[0, 7] = float("nan")
+        Z = g.gptq_mx_gemm(packed, scales, X).double().cpu().numpy()
+        assert np.isnan(Z[0]).all()
+        assert np.array_equal(Z[1:][:, keep], Y[1:][:, keep])
+
+
+def test_gemm_same_bits_every_time(g):
+    import torch
+    rng = _rng(19)
+    for m, n, batch in [(100, 4000, 3), (500, 2000, 90), (256, 1024, 700)]:
+        codes, scale = _weights(rng, m, n)
+        packed, scales = _packed(codes, scale)
+        X, _ = _to(rng.standard_normal((batch, n)), "f16")
+        first = g.gptq_mx_gemm(packed, scales, X)
+        for _ in range(3):
+            assert torch.equal(first, g.gptq_mx_gemm(packed, scales, X))
+
+
+def test_gemm_empty(g):
+    import torch
+    packed = torch.empty((0, 8), dtype=torch.int32, device="cuda")
+    scales = torch.empty((0, 2), dtype=torch.uint8, device="cuda")
+    X = torch.ones((3, 64), dtype=torch.float16, device="cuda")
+    assert g.gptq_mx_gemm(packed, scales, X).shape == (3, 0)
+    p0, s0 = torch.zeros((5, 8), dtype=torch.int32, device="cuda"), torch.zeros((5, 2), dtype=torch.uint8, device="cuda")
+    assert g.gptq_mx_gemm(p0, s0, X[:0]).shape == (0, 5)
+    Y = g.gptq_mx_gemm(p0[:, :0], s0[:, :0], X[:, :0], Y=torch.full((3, 5), 2.0, device="cuda"))
+    assert (Y == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# Grouped by expert.
+# ---------------------------------------------------------------------------
+def _grouped_oracle(codes, scale, X64, off, Y0, m):
+    want, mags = Y0.copy(), np.zeros_like(Y0)
+    for e in range(len(off) - 1):
+        a, b = off[e], off[e + 1]
+        if a < b:
+            want[a:b], mags[a:b] = oracle.mx_matmul(codes[e * m:(e + 1) * m], scale[e * m:(e + 1) * m], X64[a:b])
+    return want, mags
+
+
+GROUPED = [
+    # experts, m, n, offsets, rows
+    (1, 33, 70, [0, 5], 5),
+    (3, 40, 100, [0, 0, 7, 7], 7),                       # the first and the last without rows
+    (4, 50, 128, [0, 1, 2, 3, 4], 4),                    # one row each
+    (5, 64, 260, [2, 4, 30, 30, 95, 99], 110),           # rows before and behind that belong to none
+    (2, 130, 515, [0, 300, 301], 301),
+    (70, 20, 64, list(range(0, 71 * 3, 3)), 213),        # more experts than lanes of a wave
+    (130, 16, 40, [0] * 100 + [9] * 30 + [12], 12),
+    (3, 260, 1024, [0, 17, 17, 600], 600),
+    (8, 300, 999, [0, 16, 32, 33, 34, 200, 460, 461, 777], 777),
+]
+
+
+@pytest.mark.parametrize("experts,m,n,off,rows", GROUPED)
+@pytest.mark.parametrize("dtype,out", [("f16", "f32"), ("bf16", "bf16")])
+def test_grouped_matches_oracle(g, experts, m, n, off, rows, dtype, out):
+    import torch
+    rng = _rng(experts, m, n, rows)
+    codes, scale = _weights(rng, experts * m, n)
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((rows, n)), dtype)
+    Y = torch.full((rows, m), 7.0, device="cuda", dtype=_dt(out))
+    got = g.gptq_mx_gemm_grouped(packed.view(experts, m, -1), scales.view(experts, m, -1), X,
+                                 torch.tensor(off, dtype=torch.int32, device="cuda"), Y=Y)
+    assert got is Y
+    want, mags = _grouped_oracle(codes, scale, X64, off, np.full((rows, m), 7.0), m)
+    _check(Y, want, mags, n, out, f"grouped {experts} x {m}x{n}, {rows} rows, {dtype}->{out}")
+
+
+def test_grouped_strided_experts(g):
+    import torch
+    rng = _rng(23)
+    E, m, n, rows = 3, 40, 70, 30
+    codes, scale = _weights(rng, E * m, n)
+    packed, scales = _packed(codes, scale)
+    P = torch.full((E, m + 2, 11), -1, dtype=torch.int32, device="cuda")
+    S = torch.full((E, m + 3, 4), 255, dtype=torch.uint8, device="cuda")
+    P[:, :m, :9] = packed.view(E, m, 9)
+    S[:, :m, :3] = scales.view(E, m, 3)
+    off = [0, 11, 12, 30]
+    X, X64 = _to(rng.standard_normal((rows, n)), "f16", 75)
+    Y = torch.zeros((rows, m + 1), device="cuda")
+    g.gptq_mx_gemm_grouped(P[:, :m, :9], S[:, :m, :3], X, torch.tensor(off, dtype=torch.int32, device="cuda"),
+                           Y=Y[:, :m])
+    want, mags = _grouped_oracle(codes, scale, X64, off, np.zeros((rows, m)), m)
+    _check(Y[:, :m], want, mags, n, "f32", "strided experts")
+    assert (Y[:, m] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [12, 300])
+def test_grouped_offsets_beyond_the_rows_are_confined(g, rows):
+    # Offsets below 0 and above the row count mean the rows there are; the
+    # rows around Y's (one buffer) stay.
+    import torch
+    rng = _rng(29, rows)
+    E, m, n = 3, 24, 96
+    codes, scale = _weights(rng, E * m, n)
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((rows, n)), "bf16")
+    buf = torch.full((rows + 20, m), 5.0, device="cuda")
+    off = torch.tensor([-(1 << 31), 4, 9, (1 << 31) - 1], dtype=torch.int32, device="cuda")
+    g.gptq_mx_gemm_grouped(packed.view(E, m, -1), scales.view(E, m, -1), X, off, Y=buf[10:10 + rows])
+    want, mags = _grouped_oracle(codes, scale, X64, [0, 4, 9, rows], np.zeros((rows, m)), m)
+    _check(buf[10:10 + rows], want, mags, n, "f32", f"confined offsets, {rows} rows")
+    assert (buf[:10] == 5.0).all() and (buf[10 + rows:] == 5.0).all()
+
+
+def test_grouped_empty(g):
+    import torch
+    X = torch.ones((4, 64), dtype=torch.float16, device="cuda")
+    P, S = torch.zeros((2, 8, 8), dtype=torch.int32, device="cuda"), torch.zeros((2, 8, 2), dtype=torch.uint8, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    Y = torch.full((4, 8), 3.0, device="cuda")
+    g.gptq_mx_gemm_grouped(P, S, X, off, Y=Y)                               # no rows in any expert
+    assert (Y == 3.0).all()
+    g.gptq_mx_gemm_grouped(P[:0], S[:0], X, off[:1], Y=Y)                   # no experts
+    assert (Y == 3.0).all()
+    assert g.gptq_mx_gemm_grouped(P, S, X[:0], off).shape == (0, 8)
+    off[1:] = 4
+    g.gptq_mx_gemm_grouped(P[:, :, :0], S[:, :, :0], X[:, :0], off, Y=Y)    # no columns: empty sums
+    assert (Y == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# Both operands microscaled.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("m,n,batch", GEMM)
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+def test_scaled_gemm_matches_oracle(g, m, n, batch, out):
+    rng = _rng(m, n, batch, 31)
+    codes, scale = _weights(rng, m, n)
+    xc, xs = _weights(rng, batch, n, 118, 130)
+    packed, scales = _packed(codes, scale)
+    xp, xsc = _packed(xc, xs)
+    Y = g.gptq_mx_scaled_gemm(packed, scales, xp, xsc, n, y_dtype=_dt(out))
+    want, mags = oracle.mx_matmul(codes, scale, oracle.mx_dequantize(xc, xs))
+    _check(Y, want, mags, n, out, f"scaled gemm {batch}x{m}x{n} ->{out}")
+
+
+@pytest.mark.parametrize("m,n,batch", [(37, 70, 3), (300, 515, 70), (530, 999, 300)])
+def test_scaled_gemm_strided(g, m, n, batch):
+    import torch
+    rng = _rng(m, n, batch, 37)
+    codes, scale = _weights(rng, m, n, 60, 190)
+    xc, xs = _weights(rng, batch, n, 60, 190)
+    nw, nb = -(-n // 8), oracle.mx_blocks(n)
+    packed, scales = _packed(codes, scale, nw + 2, nb + 3)
+    xp, xsc = _packed(xc, xs, nw + 1, nb + 1)
+    buf = torch.full((batch, m + 3), 4.0, device="cuda")
+    Y = g.gptq_mx_scaled_gemm(packed, scales, xp, xsc, n, Y=buf[:, :m])
+    want, mags = oracle.mx_matmul(codes, scale, oracle.mx_dequantize(xc, xs))
+    _check(Y, want, mags, n, "f32", f"strided scaled gemm {batch}x{m}x{n}")
+    assert (buf[:, m:] == 4.0).all()
+
+
+@pytest.mark.parametrize("batch", [2, 300])
+def test_scaled_gemm_nan_blocks(g, batch):
+    rng = _rng(41, batch)
+    m, n = 140, 300
+    codes, scale = _weights(rng, m, n)
+    xc, xs = _weights(rng, batch, n)
+    scale[4, 1], xs[1, 9] = 255, 255
+    packed, scales = _packed(codes, scale)
+    xp, xsc = _packed(xc, xs)
+    Y = g.gptq_mx_scaled_gemm(packed, scales, xp, xsc, n).double().cpu().numpy()
+    bad = np.zeros((batch, m), dtype=bool)
+    bad[:, 4] = True
+    bad[1] = True
+    assert np.array_equal(np.isnan(Y), bad)
+    scale[4, 1], xs[1, 9] = 127, 127
+    want, mags = oracle.mx_matmul(codes, scale, oracle.mx_dequantize(xc, xs))
+    assert np.all((np.abs(Y - want) <= oracle.mx_matmul_bound(n, mags))[~bad])
+
+
+# ---------------------------------------------------------------------------
+# The operators together, on streams and in graphs.
+# ---------------------------------------------------------------------------
+def test_expert_layer_end_to_end(g):
+    """Experts quantized as one stack, their rows multiplied in one grouped
+    call and expert by expert, then the same rows with both operands
+    microscaled: all against the oracle on the quantized values."""
+    import torch
+    rng = _rng(43)
+    E, m, n = 6, 96, 320
+    off = [0, 5, 5, 40, 41, 100, 130]
+    W, W64 = _to(rng.standard_normal((E * m, n)) * 0.02, "bf16")
+    X, X64 = _to(rng.standard_normal((off[-1], n)), "bf16")
+    q = g.gptq_mx_quantize(W.view(E, m, n), want_wq=True)
+    Y = g.gptq_mx_gemm_grouped(q["packed"], q["scales"], X, torch.tensor(off, dtype=torch.int32, device="cuda"))
+    codes, scale = oracle.mx_quantize(W64)
+    want, mags = _grouped_oracle(codes, scale, X64, off, np.zeros((off[-1], m)), m)
+    _check(Y, want, mags, n, "f32", "grouped")
+    Wq = q["Wq"].double().cpu().numpy()
+    x = g.gptq_mx_quantize(X)
+    xd = oracle.mx_dequantize(*oracle.mx_quantize(X64))
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        assert np.array_equal(Wq[e], oracle.mx_dequantize(codes, scale)[e * m:(e + 1) * m])
+        if a < b:
+            _check(g.gptq_mx_gemm(q["packed"][e], q["scales"][e], X[a:b]), want[a:b], mags[a:b], n, "f32", f"expert {e}")
+            w, mg = oracle.mx_matmul(codes[e * m:(e + 1) * m], scale[e * m:(e + 1) * m], xd[a:b])
+            _check(g.gptq_mx_scaled_gemm(q["packed"][e], q["scales"][e], x["packed"][a:b], x["scales"][a:b], n), w, mg,
+                   n, "f32", f"expert {e}, microscaled rows")
+
+
+def _layer(rng, m, n, batch):
+    codes, scale = _weights(rng, m, n)
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((batch, n)), "f16")
+    return codes, scale, packed, scales, X, X64
+
+
+@pytest.mark.parametrize("batch", [2, 77, 300])
+def test_side_stream(g, batch):
+    import torch
+    rng = _rng(47, batch)
+    m, n = 600, 1000
+    codes, scale, packed, scales, X, X64 = _layer(rng, m, n, batch)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    Y = g.gptq_mx_gemm(packed, scales, X, stream=s)
+    q = g.gptq_mx_quantize(X, want_wq=True, stream=s)
+    Z = g.gptq_mx_scaled_gemm(packed, scales, q["packed"], q["scales"], n, stream=s)
+    s.synchronize()
+    want, mags = oracle.mx_matmul(codes, scale, X64)
+    _check(Y, want, mags, n, "f32", "side stream")
+    want, mags = oracle.mx_matmul(codes, scale, oracle.mx_dequantize(*oracle.mx_quantize(X64)))
+    _check(Z, want, mags, n, "f32", "side stream, microscaled")
+
+
+def test_graphs_replayed_in_turn(g):
+    """Two graphs over the operators, replayed several times in turn with new
+    inputs and eager calls between, each replay against the eager result."""
+    import torch
+    rng = _rng(53)
+    E, m, n = 4, 300, 520
+    layers = []
+    for batch in (3, 90):
+        codes, scale, packed, scales, X, _ = _layer(rng, E * m, n, batch)
+        off = torch.tensor([0, 1, 1, batch // 2, batch], dtype=torch.int32, device="cuda")
+        layers.append(dict(P=packed.view(E, m, -1), S=scales.view(E, m, -1), X=X, off=off,
+                           Yg=torch.zeros((batch, m), device="cuda")))
+
+    def step(L):
+        q = g.gptq_mx_quantize(L["X"])
+        a = g.gptq_mx_gemm(L["P"][0], L["S"][0], L["X"])
+        b = g.gptq_mx_scaled_gemm(L["P"][1], L["S"][1], q["packed"], q["scales"], n)
+        c = g.gptq_mx_gemm_grouped(L["P"], L["S"], L["X"], L["off"], Y=L["Yg"])
+        return a, b, c
+
+    graphs = []
+    for L in layers:
+        step(L)
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = step(L)
+        graphs.append((gr, out))
+    for k in range(4):
+        for L, (gr, out) in zip(layers, graphs):
+            L["X"].copy_(torch.randn(L["X"].shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(k)))
+            gr.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in out]
+            for x, y in zip(got, step(L)):
+                assert torch.equal(x, y)
+
+
+def test_binding_refusals(g):
+    import torch
+    dev = "cuda"
+    P, S = torch.zeros((4, 8), dtype=torch.int32, device=dev), torch.zeros((4, 2), dtype=torch.uint8, device=dev)
+    X = torch.zeros((3, 64), dtype=torch.float16, device=dev)
+    off = torch.zeros(2, dtype=torch.int32, device=dev)
+    bad = [
+        lambda: g.gptq_mx_gemm(P, S, X.float()),
+        lambda: g.gptq_mx_gemm(P, S, X[:, :60]),                       # 60 columns: the same words, other scales fit
+        lambda: g.gptq_mx_gemm(P, S[:, :1], X),
+        lambda: g.gptq_mx_gemm(P.float(), S, X),
+        lambda: g.gptq_mx_gemm(P, S.int(), X),
+        lambda: g.gptq_mx_gemm(P, S, X, Y=torch.zeros((3, 5), device=dev)),
+        lambda: g.gptq_mx_gemm(P, S, X, Y=torch.zeros((3, 4), device=dev), y_dtype=torch.float16),
+        lambda: g.gptq_mx_gemm(P, S, X, y_dtype=torch.float64),
+        lambda: g.gptq_mx_gemm(P, S, X.t().contiguous().t()),
+        lambda: g.gptq_mx_gemm(P, S, X, Y=torch.zeros((3, 4))),
+        lambda: g.gptq_mx_gemm_grouped(P[None], S[None], X, off.long()),
+        lambda: g.gptq_mx_gemm_grouped(P[None], S[None], X, off[:1]),
+        lambda: g.gptq_mx_gemm_grouped(P, S, X, off),
+        lambda: g.gptq_mx_scaled_gemm(P, S, P, S, 72),
+        lambda: g.gptq_mx_quantize(X, out=dict(packed=P, scales=S)),
+    ]
+    for i, f in enumerate(bad):
+        if i == 1:
+            continue
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(g.GptqError, match="INVALID_ARG"):
+        g.gptq_mx_gemm(P, S, X[:1].expand(3, 64))                      # rows on top of one another
