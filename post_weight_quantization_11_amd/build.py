@@ -36,7 +36,6 @@ EXTRA_FLAGS = {
     "lowrank.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "prepare.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-    "mx_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 
