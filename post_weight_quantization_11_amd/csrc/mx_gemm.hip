@@ -20,6 +20,12 @@
 namespace gptq {
 namespace {
 
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
+typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
+typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
+
 constexpr int kMx = 3;                       // X operand kinds: GPTQ_F16, GPTQ_BF16, microscaled
 
 struct MxOperands {
@@ -164,162 +170,14 @@ __device__ inline uint32_t load_scale(const uint8_t* srow, int blk, int n) {
   const uint32_t v = srow[min(blk, (n - 1) >> 5)];
   return blk * kMxBlock < n ? v : (uint32_t)kMxScaleOne;
 }
-__device__ inline void load_block(const uint32_t* row, const uint8_t* srow, int blk, int n, u32x4& w,
-                                  uint32_t& byte) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = load_word(row, 4 * blk + i, n);
-  byte = load_scale(srow, blk, n);
+__device__ inline u32x4 load_block(const uint32_t* row, int blk, int n) {
+  return u32x4{load_word(row, 4 * blk, n), load_word(row, 4 * blk + 1, n), load_word(row, 4 * blk + 2, n),
+               load_word(row, 4 * blk + 3, n)};
 }
-
-// Rows of W in tiles of 16; a wave holds RT tiles of W rows and NT tiles of 16
-// rows of X, and takes every KW-th unit of 128 columns; the waves of the
-// workgroup add their sums through LDS in wave order.
-template <int XT, int RT, int NT>
-__global__ __launch_bounds__(512) void mx_rows_kernel(MxOperands p) {
-  constexpr int kXRegs = XT == kMx ? 1 : 4;  // 16-byte registers of X per unit and tile
-  extern __shared__ floatx4 red[];           // [wave][RT][NT][64]
-  const int lane = (int)threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int waves = (int)blockDim.x >> 6;
-  const TokenTile tile = find_tile(p, (int)blockIdx.y, 16 * NT);
-  if (!tile.valid) return;
-  const int r0 = (int)blockIdx.x * 16 * RT;
-  const uint32_t* wrow[RT];
-  const uint8_t* srow[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int64_t r = min(r0 + 16 * rt + c16, p.m - 1);
-    wrow[rt] = p.W + (int64_t)tile.expert * p.w_stride + r * p.ldp;
-    srow[rt] = p.S + (int64_t)tile.expert * p.s_stride + r * p.lds;
-  }
-  const uint16_t* xrow[NT];
-  const uint32_t* xprow[NT];
-  const uint8_t* xsrow[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int64_t t = min(tile.begin + 16 * nt + c16, tile.end - 1);
-    xrow[nt] = static_cast<const uint16_t*>(p.X) + t * p.ldx;
-    xprow[nt] = static_cast<const uint32_t*>(p.X) + t * p.ldx;
-    xsrow[nt] = p.XS + t * p.ldxs;
-  }
-  floatx4 acc[RT][NT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[rt][nt] = floatx4{0.f, 0.f, 0.f, 0.f};
-
-  const int units = (p.n + 127) >> 7;
-  for (int u = wave; u < units; u += waves) {
-    const int blk = 4 * u + q, k0 = blk * kMxBlock;
-    u32x4 w[RT], x[NT][kXRegs];
-    uint32_t wb[RT], xb[NT];
-    if ((u + 1) * 128 <= p.n) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        w[rt] = *reinterpret_cast<const u32x4_a4*>(wrow[rt] + 4 * blk);
-        wb[rt] = srow[rt][blk];
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if constexpr (XT == kMx) {
-          x[nt][0] = *reinterpret_cast<const u32x4_a4*>(xprow[nt] + 4 * blk);
-          xb[nt] = xsrow[nt][blk];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[nt][j] = *reinterpret_cast<const u32x4_a2*>(xrow[nt] + k0 + 8 * j);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) load_block(wrow[rt], srow[rt], blk, p.n, w[rt], wb[rt]);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if constexpr (XT == kMx) {
-          load_block(xprow[nt], xsrow[nt], blk, p.n, x[nt][0], xb[nt]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) x[nt][j][d] = load_pair(xrow[nt], k0 + 8 * j + 2 * d, p.n);
-        }
-      }
-    }
-    if constexpr (XT == kMx) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          acc[rt][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              fp4_operand(x[nt][0]), fp4_operand(w[rt]), acc[rt][nt], 4, 4, 0, (int)xb[nt], 0, (int)wb[rt]);
-    } else {
-      bool exact = true;
-      if constexpr (XT == GPTQ_F16) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) exact = exact && f16_exact(wb[rt]);
-      }
-      if (XT == GPTQ_BF16 || __all(exact)) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const u32x4 wv = widen8<XT>(w[rt][j], mx_scale_operand(wb[rt]));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[rt][nt] = mfma16<XT>(x[nt][j], wv, acc[rt][nt]);
-          }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            u32x4 hi, lo;
-            split8(x[nt][j], hi, lo);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              const u32x4 wv = widen8<GPTQ_BF16>(w[rt][j], mx_scale_operand(wb[rt]));
-              acc[rt][nt] = mfma16<GPTQ_BF16>(hi, wv, acc[rt][nt]);
-              acc[rt][nt] = mfma16<GPTQ_BF16>(lo, wv, acc[rt][nt]);
-            }
-          }
-      }
-    }
-  }
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) red[((wave * RT + rt) * NT + nt) * 64 + lane] = acc[rt][nt];
-  __syncthreads();
-  // Accumulator register i of lane l: X row 4 (l / 16) + i, W row l % 16.
-  for (int o = wave; o < RT * NT; o += waves) {
-    const int rt = o / NT, nt = o % NT;
-    floatx4 v = red[o * 64 + lane];
-    for (int w = 1; w < waves; ++w) v += red[(w * RT * NT + o) * 64 + lane];
-    const int r = r0 + 16 * rt + c16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = tile.begin + 16 * nt + 4 * q + i;
-      if (t < tile.end && r < p.m) store_y(p, (int64_t)t * p.ldy + r, v[i]);
-    }
-  }
+__device__ inline uint32_t load_scales4(const uint8_t* srow, int blk, int n) {
+  return load_scale(srow, blk, n) | load_scale(srow, blk + 1, n) << 8 | load_scale(srow, blk + 2, n) << 16 |
+         load_scale(srow, blk + 3, n) << 24;
 }
-
-// ---------------------------------------------------------------------------
-// Tiled products (many rows of X).  A workgroup owns 32 WR RB rows of W x
-// 32 WC CB rows of X; its WR x WC waves own 32 RB x 32 CB each, in
-// v_mfma_f32_32x32x16 (16-bit X) or v_mfma_scale_f32_32x32x64_f8f6f4
-// (microscaled X).
-//
-// A stage is 128 bytes of every row of X (64 or 256 columns), staged in LDS in
-// two buffers: while a stage is multiplied the next one arrives.  The 16-byte
-// chunk c of local row r lies in slot c ^ (r % 8) of the row's eight, so the
-// reads of one chunk over 32 rows touch all banks evenly.
-//
-// 16-bit X: the codes of W go from memory straight into registers (a row's 32
-// codes of a block are 16 bytes: 1/4 of what X needs) and become operands
-// there; of a stage's two blocks, lane half h takes block h, and step j the
-// codes 8j .. 8j+7 of both.  Microscaled X: W's codes are staged in LDS like
-// X's; step j takes blocks 2j + h.
-// ---------------------------------------------------------------------------
-typedef __attribute__((address_space(3))) void lds_void;
 
 // s_waitcnt immediate (gfx9 encoding): vmcnt <= v, expcnt unconstrained, lgkmcnt = 0.
 constexpr int waitcnt_vm(int v) { return (v & 15) | ((v >> 4) << 14) | (7 << 4); }
@@ -331,6 +189,415 @@ __device__ inline void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Stores a 16 x 16 block: accumulator register i of lane l is X row 4 (l / 16) + i,
+// W row l % 16.
+__device__ inline void store_block16(const MxOperands& p, const TokenTile& tile, int t0, int r0, floatx4 v) {
+  const int lane = (int)threadIdx.x & 63, r = r0 + (lane & 15);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 4 * (lane >> 4) + i;
+    if (t < tile.end && r < p.m) store_y(p, (int64_t)t * p.ldy + r, v[i]);
+  }
+}
+
+// What a wave multiplies in one unit of 128 columns (four blocks): RT x NT
+// tiles of 16 rows.  As loaded, lane quarter q holds block q of its W row; X
+// likewise where it is microscaled.  16-bit X: register j holds columns 32j + 8q
+// .. + 7, so that the four lanes of a row read 64 neighbouring bytes.
+template <int XT, int RT, int NT>
+struct Unit {
+  static constexpr int kX = XT == kMx ? 1 : 4;
+  u32x4 w[RT], x[NT][kX];
+};
+
+// 4 x 4 transpose over the lane quarters: register j of quarter q becomes
+// register q of quarter j, i.e. word q of block j.
+__device__ inline u32x4 transpose_quarters(u32x4 v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v[0], v[1], false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(v[2], v[3], false, false);
+  const auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+  return u32x4{c[0], d[0], c[1], d[1]};
+}
+
+// Whether four scale bytes are exact in float16, tested for 104 .. 135 only:
+// the result is 0 if and only if each byte - 104 is below 32 (a byte below 104
+// sets its own top bits before it can borrow from the next).
+__device__ inline uint32_t f16_inexact4(uint32_t bytes) { return (bytes - 0x68686868u) & 0xE0E0E0E0u; }
+
+// ws, xs: the four scale bytes of the unit of each W (microscaled X) row.
+// SPLIT (float16 X): every product as two bfloat16 ones.  Otherwise `inexact`
+// gathers whether all scales have been exact in float16.
+template <int XT, bool SPLIT, int RT, int NT>
+__device__ inline void multiply_unit(const Unit<XT, RT, NT>& u, const uint32_t (&ws)[RT], const uint32_t (&xs)[NT],
+                                     floatx4 (&acc)[RT][NT], uint32_t& inexact) {
+  if constexpr (XT == kMx) {
+    const int shift = 8 * (((int)threadIdx.x >> 4) & 3);     // this lane's block
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        acc[rt][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            fp4_operand(u.x[nt][0]), fp4_operand(u.w[rt]), acc[rt][nt], 4, 4, 0, (int)(xs[nt] >> shift), 0,
+            (int)(ws[rt] >> shift));
+  } else {
+    u32x4 w[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      w[rt] = transpose_quarters(u.w[rt]);
+      if constexpr (XT == GPTQ_F16 && !SPLIT) inexact |= f16_inexact4(ws[rt]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (!SPLIT) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const u32x4 wv = widen8<XT>(w[rt][j], mx_scale_operand((ws[rt] >> (8 * j)) & 255u));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[rt][nt] = mfma16<XT>(u.x[nt][j], wv, acc[rt][nt]);
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          u32x4 hi, lo;
+          split8(u.x[nt][j], hi, lo);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const u32x4 wv = widen8<GPTQ_BF16>(w[rt][j], mx_scale_operand((ws[rt] >> (8 * j)) & 255u));
+            acc[rt][nt] = mfma16<GPTQ_BF16>(hi, wv, acc[rt][nt]);
+            acc[rt][nt] = mfma16<GPTQ_BF16>(lo, wv, acc[rt][nt]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Few rows of X: the waves of a workgroup share RT tiles of W rows and NT tiles
+// of X rows, take every KW-th quad of units (512 columns), and add their sums
+// through LDS in wave order.  X comes straight from memory.  D units are in
+// flight per wave; a row's sixteen scale bytes of a quad are one load, a quad
+// ahead (one byte a lane and unit cost 30 of 88 us at 49152 x 12288).  Returns
+// false, with nothing stored, if a float16 workgroup met scales that are not
+// exact in float16 (the caller then runs it again with SPLIT).
+template <int XT, int RT, int NT, int D, bool SPLIT>
+__device__ inline bool rows_product(const MxOperands& p, const TokenTile& tile, int r0, floatx4* red) {
+  static_assert(D == 1 || D == 2 || D == 4, "the ring's slots are the same in every quad");
+  constexpr bool MX = XT == kMx;
+  const int lane = (int)threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int waves = (int)blockDim.x >> 6;
+  const uint32_t* wrow[RT];
+  const uint8_t* wsrow[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int64_t r = min(r0 + 16 * rt + c16, p.m - 1);
+    wrow[rt] = p.W + (int64_t)tile.expert * p.w_stride + r * p.ldp;
+    wsrow[rt] = p.S + (int64_t)tile.expert * p.s_stride + r * p.lds;
+  }
+  const char* xrow[NT];
+  const uint8_t* xsrow[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int64_t t = min(tile.begin + 16 * nt + c16, tile.end - 1);
+    xrow[nt] = static_cast<const char*>(p.X) + t * p.ldx * (MX ? 4 : 2);
+    xsrow[nt] = p.XS + t * p.ldxs;
+  }
+  floatx4 acc[RT][NT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[rt][nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+  uint32_t inexact = 0u;
+
+  typedef Unit<XT, RT, NT> U;
+  struct Scales {
+    u32x4 w[RT], x[NT];                      // a quad's sixteen bytes
+  };
+  const int quads = p.n >> 9;                // whole ones
+  // Past the last quad that quad is loaded again (and not used).
+  auto load_unit = [&](int quad, int d, U& u) {
+    const int unit = 4 * min(quad, quads - 1) + d;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) u.w[rt] = *reinterpret_cast<const u32x4_a4*>(wrow[rt] + 16 * unit + 4 * q);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if constexpr (MX) {
+        u.x[nt][0] = *reinterpret_cast<const u32x4_a4*>(xrow[nt] + 64 * unit + 16 * q);
+      } else {
+#pragma unroll
+        for (int j = 0; j < U::kX; ++j)
+          u.x[nt][j] = *reinterpret_cast<const u32x4_a2*>(xrow[nt] + 256 * unit + 64 * j + 16 * q);
+      }
+    }
+  };
+  auto load_scales = [&](int quad, Scales& s) {
+    const int at = 16 * min(quad, quads - 1);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) s.w[rt] = *reinterpret_cast<const u32x4_a1*>(wsrow[rt] + at);
+    if constexpr (MX) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s.x[nt] = *reinterpret_cast<const u32x4_a1*>(xsrow[nt] + at);
+    }
+  };
+  auto multiply = [&](int d, const U& u, const Scales& s) {
+    uint32_t ws[RT], xs[NT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) ws[rt] = s.w[rt][d];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) xs[nt] = MX ? s.x[nt][d] : 0u;
+    multiply_unit<XT, SPLIT>(u, ws, xs, acc, inexact);
+  };
+  if (wave < quads) {
+    U u[D];
+    Scales cur, nxt;
+    load_scales(wave, cur);
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_unit(wave, d, u[d]);
+    for (int quad = wave; quad < quads; quad += waves) {
+      load_scales(quad + waves, nxt);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        multiply(d, u[d % D], cur);
+        load_unit(d + D < 4 ? quad : quad + waves, (d + D) % 4, u[d % D]);
+      }
+      cur = nxt;
+    }
+  }
+  // The columns behind the last whole quad, one unit a wave.
+  const int units = (p.n + 127) >> 7;
+  for (int unit = 4 * quads + (wave + waves - quads % waves) % waves; unit < units; unit += waves) {
+    U u;
+    Scales s;
+    const int blk = 4 * unit + q;
+    const bool all = (unit + 1) * 128 <= p.n;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      if (all) {
+        u.w[rt] = *reinterpret_cast<const u32x4_a4*>(wrow[rt] + 4 * blk);
+        s.w[rt][0] = *reinterpret_cast<const u32_a1*>(wsrow[rt] + 4 * unit);
+      } else {
+        u.w[rt] = load_block(wrow[rt], blk, p.n);
+        s.w[rt][0] = load_scales4(wsrow[rt], 4 * unit, p.n);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if constexpr (MX) {
+        if (all) {
+          u.x[nt][0] = *reinterpret_cast<const u32x4_a4*>(xrow[nt] + 16 * blk);
+          s.x[nt][0] = *reinterpret_cast<const u32_a1*>(xsrow[nt] + 4 * unit);
+        } else {
+          u.x[nt][0] = load_block(reinterpret_cast<const uint32_t*>(xrow[nt]), blk, p.n);
+          s.x[nt][0] = load_scales4(xsrow[nt], 4 * unit, p.n);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < U::kX; ++j) {
+          const int k = 128 * unit + 32 * j + 8 * q;
+          if (all) {
+            u.x[nt][j] = *reinterpret_cast<const u32x4_a2*>(xrow[nt] + 2 * k);
+          } else {
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+              u.x[nt][j][d] = load_pair(reinterpret_cast<const uint16_t*>(xrow[nt]), k + 2 * d, p.n);
+          }
+        }
+      }
+    }
+    multiply(0, u, s);
+  }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) red[((wave * RT + rt) * NT + nt) * 64 + lane] = acc[rt][nt];
+  if constexpr (XT == GPTQ_F16 && !SPLIT) {
+    if (!__syncthreads_and(inexact == 0u)) return false;
+  } else {
+    __syncthreads();
+  }
+  for (int o = wave; o < RT * NT; o += waves) {
+    floatx4 v = red[o * 64 + lane];
+    for (int w = 1; w < waves; ++w) v += red[(w * RT * NT + o) * 64 + lane];
+    store_block16(p, tile, tile.begin + 16 * (o % NT), r0 + 16 * (o / NT), v);
+  }
+  return true;
+}
+
+template <int XT, int RT, int NT, int D>
+__global__ __launch_bounds__(512) void mx_rows_kernel(MxOperands p) {
+  extern __shared__ floatx4 red[];           // [wave][RT][NT][64]
+  const int row_tiles = (p.m + 16 * RT - 1) / (16 * RT);
+  const int slot = (int)(blockIdx.x / row_tiles), r0 = (int)(blockIdx.x % row_tiles) * 16 * RT;
+  const TokenTile tile = find_tile(p, slot, 16 * NT);
+  if (!tile.valid) return;
+  const bool done = rows_product<XT, RT, NT, D, false>(p, tile, r0, red);
+  if constexpr (XT == GPTQ_F16) {
+    if (!done) rows_product<XT, RT, NT, D, true>(p, tile, r0, red);
+  }
+}
+
+// Few rows of 16-bit X, many rows of W: every wave owns RT tiles of W rows for
+// all columns, and the workgroup stages X once for its waves, a quad of units
+// at a time, two in LDS, in the order the matrix instructions take it: the 16
+// bytes of lane (q, row) of step j at place row ^ (4j + q) of the sixteen, so
+// that writing along a row of X and reading a step both touch all banks evenly.
+// XR: rows of X that are staged (the others' places repeat them).  The packed
+// rows stream through registers, a quad ahead.
+template <int XT, int RT, int NT, int XR, bool SPLIT>
+__device__ inline bool stream_product(const MxOperands& p, const TokenTile& tile, int r0, u32x4* xs) {
+  static_assert(XR == 4 || XR == 16 * NT, "a quarter of one tile, or all rows");
+  constexpr int kThreads = 256, kPanel = 4 * 4 * 4 * XR;       // 16-byte chunks of a quad
+  constexpr int kMine = kPanel / kThreads;
+  const int tid = (int)threadIdx.x, lane = tid & 63, q = lane >> 4, c16 = lane & 15;
+  const uint32_t* wrow[RT];
+  const uint8_t* wsrow[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int64_t r = min(r0 + 16 * rt + c16, p.m - 1);
+    wrow[rt] = p.W + (int64_t)tile.expert * p.w_stride + r * p.ldp;
+    wsrow[rt] = p.S + (int64_t)tile.expert * p.s_stride + r * p.lds;
+  }
+  const uint16_t* X = static_cast<const uint16_t*>(p.X) + (int64_t)tile.begin * p.ldx;
+  const int last = tile.end - tile.begin - 1;
+  floatx4 acc[RT][NT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[rt][nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+  uint32_t inexact = 0u;
+  typedef Unit<XT, RT, NT> U;
+  const int quads = p.n >> 9;
+
+  // Thread t stages chunks t, t + 256, ... along the rows of X, 64 to a row.
+  const uint16_t* xat[kMine];
+  int xslot[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int c = tid + i * kThreads, row = c >> 6, at = c & 63, jq = at & 15;
+    xat[i] = X + (int64_t)min(row, last) * p.ldx + at * 8;
+    xslot[i] = ((at >> 4) * 16 + jq) * XR + (row & ~15) + ((row ^ jq) & (XR < 16 ? XR - 1 : 15));
+  }
+  u32x4 xr[kMine];
+  auto fetch_x = [&](int quad) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      xr[i] = *reinterpret_cast<const u32x4_a2*>(xat[i] + min(quad, quads - 1) * 512);
+  };
+  auto put_x = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) xs[buf * kPanel + xslot[i]] = xr[i];
+  };
+  u32x4 w[4][RT], cur[RT], nxt[RT];
+  auto load_w = [&](int quad, int d) {
+    const int unit = 4 * min(quad, quads - 1) + d;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) w[d][rt] = *reinterpret_cast<const u32x4_a4*>(wrow[rt] + 16 * unit + 4 * q);
+  };
+  auto load_scales = [&](int quad, u32x4 (&s)[RT]) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) s[rt] = *reinterpret_cast<const u32x4_a1*>(wsrow[rt] + 16 * min(quad, quads - 1));
+  };
+  const uint32_t no_xs[NT] = {};
+  if (quads > 0) {
+    fetch_x(0);
+    load_scales(0, cur);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) load_w(0, d);
+    put_x(0);
+    lds_barrier();
+    for (int quad = 0; quad < quads; ++quad) {
+      fetch_x(quad + 1);
+      load_scales(quad + 1, nxt);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        U u;
+        uint32_t ws[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          u.w[rt] = w[d][rt];
+          ws[rt] = cur[rt][d];
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            u.x[nt][j] = xs[(quad & 1) * kPanel + (d * 16 + 4 * j + q) * XR + 16 * nt +
+                            ((c16 ^ (4 * j + q)) & (XR < 16 ? XR - 1 : 15))];
+        multiply_unit<XT, SPLIT>(u, ws, no_xs, acc, inexact);
+        load_w(quad + 1, d);
+      }
+      put_x((quad + 1) & 1);
+      lds_barrier();
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) cur[rt] = nxt[rt];
+    }
+  }
+  // The columns behind the last whole quad, X from memory.
+  for (int unit = 4 * quads; unit < (p.n + 127) >> 7; ++unit) {
+    U u;
+    uint32_t ws[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      u.w[rt] = load_block(wrow[rt], 4 * unit + q, p.n);
+      ws[rt] = load_scales4(wsrow[rt], 4 * unit, p.n);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint16_t* x = X + (int64_t)min(16 * nt + c16, last) * p.ldx;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) u.x[nt][j][d] = load_pair(x, 128 * unit + 32 * j + 8 * q + 2 * d, p.n);
+    }
+    multiply_unit<XT, SPLIT>(u, ws, no_xs, acc, inexact);
+  }
+  if constexpr (XT == GPTQ_F16 && !SPLIT) {
+    if (!__syncthreads_and(inexact == 0u)) return false;
+  }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) store_block16(p, tile, tile.begin + 16 * nt, r0 + 16 * rt, acc[rt][nt]);
+  return true;
+}
+
+template <int XT, int RT, int NT, int XR>
+__global__ __launch_bounds__(256) void mx_stream_kernel(MxOperands p) {
+  extern __shared__ u32x4 xs[];              // [2][unit][step][quarter][XR]
+  const int wg_rows = 16 * RT * 4;
+  const int row_wgs = (p.m + wg_rows - 1) / wg_rows;
+  const int slot = (int)(blockIdx.x / row_wgs);
+  const int r0 = (int)(blockIdx.x % row_wgs) * wg_rows +
+                 __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 16 * RT;
+  const TokenTile tile = find_tile(p, slot, 16 * NT);
+  if (!tile.valid) return;
+  const bool done = stream_product<XT, RT, NT, XR, false>(p, tile, r0, xs);
+  if constexpr (XT == GPTQ_F16) {
+    if (!done) stream_product<XT, RT, NT, XR, true>(p, tile, r0, xs);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tiled products (many rows of X).  A workgroup owns 32 WR RB rows of W x
+// 32 WC CB rows of X; its WR x WC waves own 32 RB x 32 CB each, in
+// v_mfma_f32_32x32x16 (16-bit X) or v_mfma_scale_f32_32x32x64_f8f6f4
+// (microscaled X).
+//
+// A panel is 128 bytes of every row of X (64 or 256 columns), a stage one or
+// more panels, staged in LDS in two buffers: while a stage is multiplied the
+// next one arrives.  The 16-byte chunk c of a panel's local row r lies in slot
+// c ^ (r % 8) of the row's eight, so the reads of one chunk over 32 rows touch
+// all banks evenly.
+//
+// 16-bit X: the codes of W go from memory straight into registers (a row's 32
+// codes of a block are 16 bytes: 1/4 of what X needs) and become operands
+// there; of a panel's two blocks, lane half h takes block h, and step j the
+// codes 8j .. 8j+7 of both.  Microscaled X: W's codes are staged in LDS like
+// X's; step j takes blocks 2j + h.
+// ---------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) void lds_void;
+
 template <int XT> __device__ inline floatx16 mfma32(u32x4 a, u32x4 b, floatx16 c);
 template <> __device__ inline floatx16 mfma32<GPTQ_F16>(u32x4 a, u32x4 b, floatx16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(halfx8, a), __builtin_bit_cast(halfx8, b), c, 0, 0,
@@ -341,12 +608,23 @@ template <> __device__ inline floatx16 mfma32<GPTQ_BF16>(u32x4 a, u32x4 b, float
                                                  0, 0);
 }
 
-constexpr int kStageRow = 128;               // bytes of a row in a stage
-typedef uint64_t u64_a1 __attribute__((aligned(1)));
+constexpr int kPanelRow = 128;               // bytes of a row in a panel
+
+// Floats per row of X in a wave's output block: two (one) row blocks of W, and
+// four so that neighbouring rows start in different banks.
+constexpr int out_pitch(int row_blocks) { return (row_blocks % 2 == 0 ? 64 : 32) + 4; }
+
+// LDS of a tile: two buffers of staged rows, later the waves' output blocks.
+// The microscaled scales of eight stages stand behind the buffers.
+template <int XT, int WR, int WC, int RB, int CB, int PB>
+constexpr int tile_lds() {
+  const int rows = 32 * (WC * CB + (XT == kMx ? WR * RB : 0));
+  return std::max(2 * PB * rows * kPanelRow + (XT == kMx ? 8 * rows * 8 : 0), WR * WC * 32 * out_pitch(RB) * 4);
+}
 
 // Work of one launch: tiles of W rows, of X rows, and parts of the columns.
 struct TileGrid {
-  int row_tiles, tok_tiles, splits, stages_per_split;
+  int row_tiles, tok_tiles, splits, cols_per_split;
   float* part;                               // [split][row of X][m] sums, when splits > 1
 };
 
@@ -355,40 +633,49 @@ struct TileGrid {
 // either operand in its L2.
 constexpr int kTokBand = 8;
 
-// One 16-byte chunk of a row: of a whole stage, and of a row's last columns
+// One 16-byte chunk of a row: of a whole panel, and of a row's last columns
 // (zero past its end).
 template <int XT>
-__device__ inline u32x4 load_chunk(const char* row, int stage, int chunk) {
-  const char* at = row + (int64_t)stage * kStageRow + chunk * 16;
+__device__ inline u32x4 load_chunk(const char* row, int panel, int chunk) {
+  const char* at = row + (int64_t)panel * kPanelRow + chunk * 16;
   if constexpr (XT == kMx) return *reinterpret_cast<const u32x4_a4*>(at);
   else return *reinterpret_cast<const u32x4_a2*>(at);
 }
 template <int XT>
-__device__ inline u32x4 load_chunk_tail(const char* row, int stage, int chunk, int n) {
+__device__ inline u32x4 load_chunk_tail(const char* row, int panel, int chunk, int n) {
   u32x4 v;
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
     if constexpr (XT == kMx)
-      v[d] = load_word(reinterpret_cast<const uint32_t*>(row), stage * 32 + chunk * 4 + d, n);
+      v[d] = load_word(reinterpret_cast<const uint32_t*>(row), panel * 32 + chunk * 4 + d, n);
     else
-      v[d] = load_pair(reinterpret_cast<const uint16_t*>(row), stage * 64 + chunk * 8 + 2 * d, n);
+      v[d] = load_pair(reinterpret_cast<const uint16_t*>(row), panel * 64 + chunk * 8 + 2 * d, n);
   }
   return v;
 }
 
-// Scale bytes of the eight blocks of a stage of microscaled columns: byte t of
-// the result belongs to block 2t + h.  Blocks past the row's end have scale 1.
-__device__ inline uint32_t order_scales8(uint64_t v, int h) {
-  return __builtin_amdgcn_perm((uint32_t)(v >> 32), (uint32_t)v, h ? 0x07050301u : 0x06040200u);
+// The scale bytes of the eight blocks of a microscaled stage as the lane halves
+// use them: word h holds blocks h, 2 + h, 4 + h and 6 + h.
+__device__ inline u32x2 order_scales8(uint32_t lo, uint32_t hi) {
+  return u32x2{__builtin_amdgcn_perm(hi, lo, 0x06040200u), __builtin_amdgcn_perm(hi, lo, 0x07050301u)};
 }
-__device__ inline uint32_t load_scales8(const uint8_t* srow, int stage, int h) {
-  return order_scales8(*reinterpret_cast<const u64_a1*>(srow + 8 * stage), h);
-}
+// Those of a partial stage; blocks past the row's end have scale 1.
 __device__ inline uint32_t load_scales8_tail(const uint8_t* srow, int stage, int h, int n) {
-  uint64_t v = 0;
+  uint32_t v = 0u;
 #pragma unroll 1
-  for (int i = 7; i >= 0; --i) v = v << 8 | load_scale(srow, 8 * stage + i, n);
-  return order_scales8(v, h);
+  for (int j = 3; j >= 0; --j) v = v << 8 | load_scale(srow, 8 * stage + 2 * j + h, n);
+  return v;
+}
+
+// Step `step` of a microscaled stage: byte `step` of the scales.
+__device__ inline floatx16 mfma_mx(int step, u32x4 x, uint32_t xs, u32x4 w, uint32_t ws, floatx16 c) {
+  const intx8 a = fp4_operand(x), b = fp4_operand(w);
+  switch (step) {                            // the byte is an immediate
+    case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 0, (int)xs, 0, (int)ws);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 1, (int)xs, 1, (int)ws);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 2, (int)xs, 2, (int)ws);
+    default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 3, (int)xs, 3, (int)ws);
+  }
 }
 
 // The first `left` of eight neighbouring results.
@@ -426,28 +713,41 @@ __device__ inline void store8(void* Y, int64_t at, int left, floatx4 lo, floatx4
   }
 }
 
-// One tile.  DIRECT: 16-byte aligned rows; whole stages of X (and microscaled W)
-// go from memory to LDS without passing through registers.  SPLIT (float16 X):
-// every product as two bfloat16 ones.  Without SPLIT a float16 tile runs as if
-// all its scales were exact in float16 and says at the end whether they were
-// (the same answer in the whole workgroup); if not, nothing is stored and the
-// caller runs it again with SPLIT: trained weights have no such scales, and a
-// branch on them in the main loop made the compiler move the accumulators.
-template <int XT, int WR, int WC, int RB, int CB, bool DIRECT, bool SPLIT>
+// One tile.  PB: panels of 128 bytes per row in a stage.  DIRECT: 16-byte
+// aligned rows; whole stages of X (and microscaled W) go from memory to LDS
+// without passing through registers.  SPLIT (float16 X): every product as two
+// bfloat16 ones.  Without SPLIT a float16 tile runs as if all its scales were
+// exact in float16 and says at the end whether they were (the same answer in
+// the whole workgroup); if not, nothing is stored and the caller runs it again
+// with SPLIT: trained weights have no such scales, and a branch on them in the
+// main loop made the compiler move the accumulators.
+//
+// Pipeline: a step's operands are read from LDS while the step before it
+// multiplies.  The one barrier of a stage stands in its last step, between the
+// two halves of that step's products: every wave then holds the step's
+// operands, so the other buffer is complete (its loads were waited for) and
+// this one is free, and the next stage's first reads overlap the second half.
+template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT, bool SPLIT>
 __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, const TokenTile& tile, int r0, int split,
                                     unsigned char* smem) {
   constexpr bool MX = XT == kMx;
+  static_assert(!MX || PB == 1, "microscaled stages are one panel");
   constexpr int kThreads = 64 * WR * WC, kWaves = WR * WC;
   constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB;
   constexpr int kLdsRows = MX ? BM + BN : BN;                 // X rows first, then W rows
-  constexpr int kPerThread = kLdsRows * 8 / kThreads;         // chunks a thread stages
-  constexpr int kCols = MX ? 256 : 64;                        // columns per stage
+  constexpr int kPanel = kLdsRows * kPanelRow, kBuf = PB * kPanel;
+  constexpr int kPerThread = PB * kLdsRows * 8 / kThreads;    // chunks a thread stages
+  constexpr int kRowStep = kThreads / 8;                      // rows that the threads' chunks cover at once
+  constexpr int kDirect = PB * kLdsRows / (8 * kWaves);       // direct loads a wave issues per stage
+  constexpr int kCols = MX ? 256 : 64 * PB;                   // columns per stage
+  constexpr int kSteps = 4 * PB;
   static_assert(kLdsRows % (8 * kWaves) == 0, "a wave stages eight rows at a time");
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / WC, wc = wave % WC;
   const int stages = (p.n + kCols - 1) / kCols;
-  const int s_lo = split * tg.stages_per_split, s_hi = min(stages, s_lo + tg.stages_per_split);
+  const int per_split = tg.cols_per_split / kCols;
+  const int s_lo = split * per_split, s_hi = min(stages, s_lo + per_split);
   const uint32_t* W = p.W + (int64_t)tile.expert * p.w_stride;
   const uint8_t* S = p.S + (int64_t)tile.expert * p.s_stride;
   const char* X = static_cast<const char*>(p.X);
@@ -463,101 +763,144 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
     return (uint32_t)min(r - BN, p.m - 1 - r0) * (uint32_t)w_pitch;
   };
   auto row_ptr = [&](int r) -> const char* { return (!MX || r < BN ? xbase : wbase) + row_offset(r); };
+  // Chunk i of this thread: panel and local row.
+  auto my_panel = [&](int i) { return i / (kPerThread / PB); };
+  auto my_row = [&](int i) { return (tid >> 3) + i % (kPerThread / PB) * kRowStep; };
+  auto my_slot = [&](int buf, int i) {
+    const int r = my_row(i);
+    return reinterpret_cast<u32x4*>(smem + buf * kBuf + my_panel(i) * kPanel + r * kPanelRow +
+                                    (((tid & 7) ^ (r & 7)) << 4));
+  };
   u32x4 stage_regs[DIRECT ? 1 : kPerThread];
   auto fetch = [&](int st) {                 // by registers: any alignment
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int r = (tid >> 3) + i * (kThreads / 8);
-      stage_regs[DIRECT ? 0 : i] = load_chunk<XT>(row_ptr(r), st, tid & 7);
-    }
+    for (int i = 0; i < kPerThread; ++i)
+      stage_regs[DIRECT ? 0 : i] = load_chunk<XT>(row_ptr(my_row(i)), st * PB + my_panel(i), tid & 7);
   };
   auto put = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int r = (tid >> 3) + i * (kThreads / 8);
-      *reinterpret_cast<u32x4*>(smem + buf * (kLdsRows * kStageRow) + r * kStageRow + (((tid & 7) ^ (r & 7)) << 4)) =
-          stage_regs[DIRECT ? 0 : i];
-    }
+    for (int i = 0; i < kPerThread; ++i) *my_slot(buf, i) = stage_regs[DIRECT ? 0 : i];
   };
   // Directly: a wave's instruction moves eight rows, lane i the chunk that
   // belongs into slot i % 8 of row i / 8.
-  uint32_t direct_offset[DIRECT ? kLdsRows / (8 * kWaves) : 1];
+  uint32_t direct_offset[DIRECT ? kDirect / PB : 1];
   if constexpr (DIRECT) {
 #pragma unroll
-    for (int i = 0; i < kLdsRows / (8 * kWaves); ++i)
+    for (int i = 0; i < kDirect / PB; ++i)
       direct_offset[i] = row_offset((wave + i * kWaves) * 8 + (lane >> 3)) + (((lane & 7) ^ (lane >> 3)) << 4);
   }
-  auto fetch_direct = [&](int st, int buf) {
-#pragma unroll
-    for (int i = 0; i < kLdsRows / (8 * kWaves); ++i) {
-      const uint32_t dst = (uint32_t)reinterpret_cast<uintptr_t>(
-          (lds_void*)(smem + buf * (kLdsRows * kStageRow) + (wave + i * kWaves) * 8 * kStageRow));
-      // BN / 8 is a multiple of the waves or the other way round: one i reads one operand.
-      const char* src = ((wave + i * kWaves) * 8 < BN ? xbase : wbase) + (int64_t)st * kStageRow;
-      // M0 is the LDS destination; the compiler does not track the load, the
-      // pipeline waits for it explicitly.
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst),
-                   "v"(direct_offset[DIRECT ? i : 0]), "s"(src)
-                   : "memory", "m0");
-    }
+  auto fetch_direct = [&](int st, int buf, int i) {
+    const int rows8 = wave + i % (kDirect / PB) * kWaves, panel = i / (kDirect / PB);
+    const uint32_t dst = (uint32_t)reinterpret_cast<uintptr_t>(
+        (lds_void*)(smem + buf * kBuf + panel * kPanel + rows8 * 8 * kPanelRow));
+    const char* src = (!MX || rows8 * 8 < BN ? xbase : wbase) + (int64_t)(st * PB + panel) * kPanelRow;
+    // M0 is the LDS destination; the compiler does not track the load, the
+    // pipeline waits for it explicitly.
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst),
+                 "v"(direct_offset[DIRECT ? i % (kDirect / PB) : 0]), "s"(src)
+                 : "memory", "m0");
   };
   // A partial last stage, element by element, into the first buffer (the loop's
   // last barrier is behind it).
   auto fill_tail = [&](int st) {
 #pragma unroll 1
-    for (int i = 0; i < kPerThread; ++i) {
-      const int r = (tid >> 3) + i * (kThreads / 8);
-      const u32x4 v = load_chunk_tail<XT>(row_ptr(r), st, tid & 7, p.n);
-      *reinterpret_cast<u32x4*>(smem + r * kStageRow + (((tid & 7) ^ (r & 7)) << 4)) = v;
-    }
+    for (int i = 0; i < kPerThread; ++i)
+      *my_slot(0, i) = load_chunk_tail<XT>(row_ptr(my_row(i)), st * PB + my_panel(i), tid & 7, p.n);
   };
 
-  // This lane's rows of W (16-bit X: codes and scales; microscaled: scales) and
-  // of X (microscaled: scales).
-  uint32_t w_at[RB], ws_at[RB], xs_at[CB];
+  // Microscaled: the scale bytes of four stages (a group: 32 bytes of every
+  // local row) are staged together, four lanes to a row, in the order the lanes
+  // use them: [two groups][stage][row][half].  Each stage of a group fetches a
+  // quarter of the rows of the next group, so the loop has no branch (one made
+  // the compiler copy the accumulators).  Loaded by the lanes that use them,
+  // eight bytes a row and stage, the scales cost a third of the kernel's time.
+  constexpr int kQuarter = kLdsRows / 4;
+  constexpr int kScaleLoads = MX ? (kQuarter * 4 + kThreads - 1) / kThreads : 1;
+  uint32_t* scale_lds = reinterpret_cast<uint32_t*>(smem + 2 * kBuf);
+  u32x2 scale_regs[kScaleLoads];
+  const int s_whole = min(s_hi, p.n / kCols);
+  auto scale_row = [&](int quarter, int i) {
+    return quarter * kQuarter + min((tid + i * kThreads) >> 2, kQuarter - 1);
+  };
+  auto fetch_scales = [&](int group, int quarter) {
+    const int st = min(s_lo + 4 * group + (tid & 3), s_whole - 1);
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i) {
+      const int r = scale_row(quarter, i);
+      const uint8_t* row = r < BN ? p.XS + (int64_t)min(tile.begin + r, tile.end - 1) * p.ldxs
+                                  : S + (int64_t)min(r0 + r - BN, p.m - 1) * p.lds;
+      scale_regs[i] = *reinterpret_cast<const u32x2_a1*>(row + 8 * st);
+    }
+  };
+  auto put_scales = [&](int group, int quarter) {
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i)
+      *reinterpret_cast<u32x2*>(scale_lds + ((4 * (group & 1) + (tid & 3)) * kLdsRows + scale_row(quarter, i)) * 2) =
+          order_scales8(scale_regs[i][0], scale_regs[i][1]);
+  };
+
+  // This lane's rows of W (16-bit X: codes and scales).
+  uint32_t w_at[RB], ws_at[RB];
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
     const uint32_t r = (uint32_t)min((wr * RB + rb) * 32 + l32, p.m - 1 - r0);
     w_at[rb] = r * (uint32_t)w_pitch;
     ws_at[rb] = r * (uint32_t)p.lds;
   }
-  const uint8_t* xsbase = p.XS + (int64_t)tile.begin * p.ldxs;
-#pragma unroll
-  for (int cb = 0; cb < CB; ++cb)
-    xs_at[cb] = (uint32_t)min((wc * CB + cb) * 32 + l32, tile.end - 1 - tile.begin) * (uint32_t)p.ldxs;
-
   struct Regs {
-    u32x4 w[RB];                             // codes of this lane's block (16-bit X)
-    uint32_t ws[RB];                         // scale byte, or the stage's four
+    u32x4 w[MX ? 1 : PB][RB];                // codes of this lane's block of each panel (16-bit X)
+    uint32_t ws[(PB + 1) / 2][RB];           // scale bytes of two panels' blocks; microscaled: of the stage's four
     uint32_t xs[CB];
   };
   Regs cur, nxt;
   auto fetch_regs = [&](int st, Regs& g) {
-    if constexpr (MX) {
+    if constexpr (!MX) {
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) g.ws[rb] = load_scales8(sbase + ws_at[rb], st, h);
+      for (int u = 0; u < PB; ++u)
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) g.xs[cb] = load_scales8(xsbase + xs_at[cb], st, h);
-    } else {
-      const uint32_t blk = (uint32_t)(2 * st + h);
+        for (int rb = 0; rb < RB; ++rb) {
+          const uint32_t blk = (uint32_t)(2 * (st * PB + u) + h);
+          g.w[u][rb] = *reinterpret_cast<const u32x4_a4*>(wbase + (w_at[rb] + 16u * blk));
+        }
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        g.w[rb] = *reinterpret_cast<const u32x4_a4*>(wbase + (w_at[rb] + 16u * blk));
-        g.ws[rb] = sbase[ws_at[rb] + blk];
+        const uint8_t* at = sbase + (ws_at[rb] + 2u * PB * st);
+        if constexpr (PB == 1) {
+          g.ws[0][rb] = *reinterpret_cast<const u16_a1*>(at);
+        } else {
+#pragma unroll
+          for (int i = 0; i < PB / 2; ++i) g.ws[i][rb] = reinterpret_cast<const u32_a1*>(at)[i];
+        }
       }
+    }
+  };
+  auto read_scales = [&](int st, Regs& g) {
+    if constexpr (MX) {
+      const uint32_t* at = scale_lds + ((st - s_lo) & 7) * kLdsRows * 2 + l32 * 2 + h;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) g.xs[cb] = at[(wc * CB + cb) * 64];
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) g.ws[0][rb] = at[(BN + (wr * RB + rb) * 32) * 2];
     }
   };
   auto fetch_regs_tail = [&](int st, Regs& g) {
     if constexpr (MX) {
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) g.ws[rb] = load_scales8_tail(sbase + ws_at[rb], st, h, p.n);
+      for (int rb = 0; rb < RB; ++rb)
+        g.ws[0][rb] = load_scales8_tail(S + (int64_t)min(r0 + (wr * RB + rb) * 32 + l32, p.m - 1) * p.lds, st, h, p.n);
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) g.xs[cb] = load_scales8_tail(xsbase + xs_at[cb], st, h, p.n);
+      for (int cb = 0; cb < CB; ++cb)
+        g.xs[cb] = load_scales8_tail(
+            p.XS + (int64_t)min(tile.begin + (wc * CB + cb) * 32 + l32, tile.end - 1) * p.ldxs, st, h, p.n);
     } else {
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-        load_block(reinterpret_cast<const uint32_t*>(wbase + w_at[rb]), sbase + ws_at[rb], 2 * st + h, p.n, g.w[rb],
-                   g.ws[rb]);
+      for (int u = 0; u < PB; ++u)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+          const int blk = 2 * (st * PB + u) + h;
+          g.w[u][rb] = load_block(reinterpret_cast<const uint32_t*>(wbase + w_at[rb]), blk, p.n);
+          if (u % 2 == 0) g.ws[u / 2][rb] = load_scales4(sbase + ws_at[rb], 2 * (st * PB + u), p.n);
+        }
     }
   };
 
@@ -567,106 +910,151 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = floatx16{};
 
-  auto frag = [&](int buf, int row, int chunk) {             // row % 32 == l32
-    return *reinterpret_cast<const u32x4*>(smem + buf * (kLdsRows * kStageRow) + row * kStageRow +
-                                           ((chunk ^ (l32 & 7)) << 4));
+  // The operands of one step that come from LDS.
+  struct Frags {
+    u32x4 x[CB], w[MX ? RB : 1];
   };
-  bool exact = true;                         // this lane's scales so far
-  auto multiply = [&](int buf, const Regs& g) {
+  Frags f[2];
+  // This lane's address of chunk j in the wave's first X row block (and, the
+  // constant w_off further, its first W row block).
+  uint32_t frag_at[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    frag_at[j] = (uint32_t)((wc * CB * 32 + l32) * kPanelRow + (((MX ? 2 * j + h : 4 * h + j) ^ (l32 & 7)) << 4));
+  const uint32_t w_off = (uint32_t)((BN + (wr * RB - wc * CB) * 32) * kPanelRow);
+  auto load_frags = [&](int buf, int step, Frags& o) {
+    const unsigned char* at = smem + buf * kBuf + (MX ? 0 : step / 4) * kPanel + frag_at[step % 4];
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) o.x[cb] = *reinterpret_cast<const u32x4*>(at + cb * 32 * kPanelRow);
     if constexpr (MX) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u32x4 x[CB], w[RB];
+      for (int rb = 0; rb < RB; ++rb) o.w[rb] = *reinterpret_cast<const u32x4*>(at + w_off + rb * 32 * kPanelRow);
+    }
+  };
+  // This lane's scale byte in panel u.
+  auto scale_byte = [&](const Regs& g, int u, int rb) { return (g.ws[u / 2][rb] >> (16 * (u % 2) + 8 * h)) & 255u; };
+  // Products of one step, row blocks [lo, hi).
+  auto products = [&](int step, const Frags& o, const Regs& g, int lo, int hi) {
+    if constexpr (SPLIT) {
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) x[cb] = frag(buf, (wc * CB + cb) * 32 + l32, 2 * j + h);
+      for (int cb = 0; cb < CB; ++cb) {
+        u32x4 top, rest;
+        split8(o.x[cb], top, rest);
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) w[rb] = frag(buf, BN + (wr * RB + rb) * 32 + l32, 2 * j + h);
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-          for (int cb = 0; cb < CB; ++cb) {
-#define GPTQ_MX_STEP(J)                                                                                          \
-  case J:                                                                                                        \
-    acc[rb][cb] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(x[cb]), fp4_operand(w[rb]),        \
-                                                                  acc[rb][cb], 4, 4, J, (int)g.xs[cb], J,        \
-                                                                  (int)g.ws[rb]);                                \
-    break;
-            switch (j) {
-              GPTQ_MX_STEP(0)
-              GPTQ_MX_STEP(1)
-              GPTQ_MX_STEP(2)
-              GPTQ_MX_STEP(3)
-            }
-#undef GPTQ_MX_STEP
-          }
+        for (int rb = lo; rb < hi; ++rb) {
+          const u32x4 wv = widen8<GPTQ_BF16>(g.w[step / 4][rb][step % 4], mx_scale_operand(scale_byte(g, step / 4, rb)));
+          acc[rb][cb] = mfma32<GPTQ_BF16>(top, wv, acc[rb][cb]);
+          acc[rb][cb] = mfma32<GPTQ_BF16>(rest, wv, acc[rb][cb]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-      if constexpr (XT == GPTQ_F16 && !SPLIT) {
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) exact = exact && f16_exact(g.ws[rb]);
-      }
+      for (int rb = lo; rb < hi; ++rb) {
+        if constexpr (MX) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (SPLIT) {
-#pragma unroll
-          for (int cb = 0; cb < CB; ++cb) {
-            u32x4 hi, lo;
-            split8(frag(buf, (wc * CB + cb) * 32 + l32, 4 * h + j), hi, lo);
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-              const u32x4 wv = widen8<GPTQ_BF16>(g.w[rb][j], mx_scale_operand(g.ws[rb]));
-              acc[rb][cb] = mfma32<GPTQ_BF16>(hi, wv, acc[rb][cb]);
-              acc[rb][cb] = mfma32<GPTQ_BF16>(lo, wv, acc[rb][cb]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-          }
+          for (int cb = 0; cb < CB; ++cb)
+            acc[rb][cb] = mfma_mx(step, o.x[cb], g.xs[cb], o.w[rb], g.ws[0][rb], acc[rb][cb]);
         } else {
-          u32x4 x[CB];
+          const u32x4 wv = widen8<XT>(g.w[step / 4][rb][step % 4], mx_scale_operand(scale_byte(g, step / 4, rb)));
 #pragma unroll
-          for (int cb = 0; cb < CB; ++cb) x[cb] = frag(buf, (wc * CB + cb) * 32 + l32, 4 * h + j);
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) {
-            const u32x4 wv = widen8<XT>(g.w[rb][j], mx_scale_operand(g.ws[rb]));
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = mfma32<XT>(x[cb], wv, acc[rb][cb]);
-          }
+          for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = mfma32<XT>(o.x[cb], wv, acc[rb][cb]);
         }
       }
     }
   };
+  // 16-bit X: asks the scheduler for one LDS read and up to two conversions
+  // behind each of `count` products.
+  auto interleave = [&](int count) {
+    if constexpr (!MX && !SPLIT) {
+#pragma unroll
+      for (int i = 0; i < count; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);   // two VALU
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // one load
+      }
+    }
+  };
+  bool exact = true;                         // this lane's scales so far
+  auto check_scales = [&](const Regs& g) {
+    if constexpr (XT == GPTQ_F16 && !SPLIT) {
+#pragma unroll
+      for (int u = 0; u < PB; ++u)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) exact = exact && f16_exact(scale_byte(g, u, rb));
+    }
+  };
 
   // Whole stages first; a partial one at the rows' end is staged alone.
-  const int s_whole = min(s_hi, p.n / kCols);
   if (s_lo < s_whole) {
     if constexpr (DIRECT) {
-      fetch_direct(s_lo, 0);
+#pragma unroll
+      for (int i = 0; i < kDirect; ++i) fetch_direct(s_lo, 0, i);
     } else {
       fetch(s_lo);
       put(0);
     }
     fetch_regs(s_lo, cur);
+    if constexpr (MX) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        fetch_scales(0, q);
+        put_scales(0, q);
+      }
+    }
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     lds_barrier();
+    load_frags(0, 0, f[0]);
+    read_scales(s_lo, cur);
     for (int st = s_lo; st < s_whole; ++st) {
       const int buf = (st - s_lo) & 1;
       // The last stage fetches itself again, into the buffer no one reads any
       // more: no branch around the loads.
       const int next = min(st + 1, s_whole - 1);
-      if constexpr (DIRECT) fetch_direct(next, buf ^ 1);
-      else fetch(next);
+      if constexpr (DIRECT) {
+#pragma unroll
+        for (int i = 0; i < kDirect; ++i) fetch_direct(next, buf ^ 1, i);
+      } else {
+        fetch(next);
+      }
       fetch_regs(next, nxt);
-      multiply(buf, cur);
+      if constexpr (MX) {
+        fetch_scales(((st - s_lo) >> 2) + 1, (st - s_lo) & 3);
+      }
+      check_scales(cur);
+#pragma unroll
+      for (int step = 0; step < kSteps - 1; ++step) {
+        load_frags(buf, step + 1, f[(step + 1) & 1]);
+        products(step, f[step & 1], cur, 0, RB);
+        interleave(RB * CB);
+      }
+      products(kSteps - 1, f[1], cur, 0, RB / 2);
+      interleave(RB / 2 * CB);
       if constexpr (!DIRECT) put(buf ^ 1);
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      if constexpr (MX) {
+        put_scales(((st - s_lo) >> 2) + 1, (st - s_lo) & 3);
+      }
       lds_barrier();
+      load_frags(buf ^ 1, 0, f[0]);
+      read_scales(next, nxt);
+      products(kSteps - 1, f[1], cur, RB / 2, RB);
+      interleave((RB - RB / 2) * CB);
       cur = nxt;
     }
   }
   if (s_whole < s_hi) {
+    lds_barrier();                           // the loop's last reads are done
     fill_tail(s_whole);
     fetch_regs_tail(s_whole, cur);
+    check_scales(cur);
     lds_barrier();
-    multiply(0, cur);
+#pragma unroll
+    for (int step = 0; step < kSteps; ++step) {
+      load_frags(0, step, f[0]);
+      products(step, f[0], cur, 0, RB);
+    }
   }
 
   // Accumulator register i of lane l: X row 8 (i / 4) + 4 (l / 32) + i % 4, W row
@@ -677,8 +1065,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
   } else {
     lds_barrier();
   }
-  constexpr int RP = RB % 2 == 0 ? 2 : 1, kPitch = 32 * RP + 4;
-  static_assert(kWaves * 32 * kPitch * 4 <= 2 * kLdsRows * kStageRow, "the stages' LDS holds every wave's block");
+  constexpr int RP = RB % 2 == 0 ? 2 : 1, kPitch = out_pitch(RB);
   float* my = reinterpret_cast<float*>(smem) + wave * 32 * kPitch;
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb)
@@ -716,8 +1103,9 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
   return true;
 }
 
-template <int XT, int WR, int WC, int RB, int CB, bool DIRECT>
-__global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(MxOperands p, TileGrid tg) {
+// Two waves per SIMD where the accumulators leave room for them.
+template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT>
+__global__ __launch_bounds__(64 * WR * WC, RB * CB <= 8 ? 2 : 1) void mx_tile_kernel(MxOperands p, TileGrid tg) {
   constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   // Workgroup -> (split, tile of X rows, tile of W rows).
@@ -732,9 +1120,9 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(MxOperands p, Til
   const TokenTile tile = find_tile(p, band * kTokBand + rest % in_band, BN);
   if (!tile.valid) return;
   const int r0 = rest / in_band * BM;
-  const bool done = tile_product<XT, WR, WC, RB, CB, DIRECT, false>(p, tg, tile, r0, split, smem);
+  const bool done = tile_product<XT, WR, WC, RB, CB, PB, DIRECT, false>(p, tg, tile, r0, split, smem);
   if constexpr (XT == GPTQ_F16) {
-    if (!done) tile_product<XT, WR, WC, RB, CB, DIRECT, true>(p, tg, tile, r0, split, smem);
+    if (!done) tile_product<XT, WR, WC, RB, CB, PB, DIRECT, true>(p, tg, tile, r0, split, smem);
   }
 }
 
@@ -762,26 +1150,88 @@ int64_t max_tiles(int64_t rows, int64_t experts, bool grouped, int tile) {
 }
 
 // What a product runs on, from its sizes alone.
-struct Plan {
-  int kind;                                  // 0: mx_rows_kernel, else a tile shape
-  int splits, stages_per_split;
-  size_t ws;
+enum Kind {
+  kRows1, kRows2, kRows4, kRows2x2, kRows4x2,              // mx_rows_kernel: tiles of W (x tiles of X)
+  kStream1, kStream3,                                                // mx_stream_kernel: tiles of W
+  kTile128x32, kTile128x64, kTile128x128, kTile256x128, kTile256x256, // W rows x X rows of a tile
 };
+struct Plan {
+  Kind kind;
+  int splits;                                // of the columns, tiles only
+};
+constexpr int kSplitCols = 256;              // a split is a multiple of this
 
-Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool mx) {
-  (void)m; (void)n; (void)experts; (void)grouped; (void)mx;
-  Plan pl{0, 1, 1 << 30, 0};
-  if (rows > 64) pl.kind = 1;
-  return pl;
+// The rules below follow sweeps of all kinds over sizes (times in us, the kind
+// taken first): products small enough for their operands to come through L2
+// run on the row kernels, whose waves split the columns (64 x 4096 x 4096: 11.5
+// against 13.1 on tiles; 64 x 12288 x 12288: 75 against 36), long matrices with
+// few rows of X on the stream kernel (16 x 49152 x 12288: 78 against 93), the
+// rest on tiles, as wide as still gives half the 256 CUs one, their columns
+// split until there are about 384 (16 x 12288 x 12288: 28 with 4 splits, 45
+// with 1).  256 x 256 tiles are the fastest where they fill whole rounds of the
+// CUs (4096 x 8192 x 8192: 437 against 464), 256 x 128 (two to a CU) otherwise
+// (2048 x 11008 x 4096: 179 against 209).
+constexpr int64_t kWantTiles = 384, kMinSplitCols = 512;
+
+Plan tile_plan(int64_t m, int64_t n, int64_t rows, bool mx) {
+  auto tiles = [&](int bm, int bn) { return ceil_div(m, bm) * ceil_div(rows, bn); };
+  if (rows >= 192) {
+    const int64_t t = tiles(256, 256);
+    const int64_t rounds = ceil_div(t, 256) * 256;
+    if (t >= 192 && (mx || t * 10 >= rounds * 9)) return Plan{kTile256x256, 1};
+    if (tiles(256, 128) >= 192 && (!mx || rows >= 1024)) return Plan{kTile256x128, 1};
+  }
+  const Kind kinds[3] = {kTile128x128, kTile128x64, kTile128x32};
+  const int widths[3] = {128, 64, 32};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t t = tiles(128, widths[i]);
+    if (i < 2 && (t < 128 || rows <= widths[i] / 2)) continue;
+    const int64_t most = std::max<int64_t>(1, n / kMinSplitCols);
+    const int64_t splits = t >= 256 ? 1 : std::max<int64_t>(1, (kWantTiles + t / 2) / t);
+    return Plan{kinds[i], (int)std::min(splits, most)};
+  }
+  return Plan{kTile128x32, 1};
 }
 
-template <int XT, int WR, int WC, int RB, int CB>
+Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool mx) {
+  if (grouped) {
+    // By the rows an expert has on average; the workgroups of an expert without
+    // rows do not exist.
+    const int64_t each = rows / experts;
+    if (rows <= 4) return Plan{kRows1, 1};
+    if (each <= 8) return Plan{kRows2, 1};
+    if (each <= 32) return Plan{kTile128x32, 1};
+    if (each <= 96) return Plan{kTile128x64, 1};
+    return Plan{kTile256x128, 1};
+  }
+  const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
+  if (mx) {
+    if (products > 1100000000) return tile_plan(m, n, rows, true);
+    if (outputs <= 65536) return Plan{kRows1, 1};
+    return Plan{rows <= 32 ? kRows2 : kRows2x2, 1};
+  }
+  if (m >= 24576 && rows <= 16) return Plan{rows <= 4 ? kStream1 : kStream3, 1};
+  if (products > 2200000000) return tile_plan(m, n, rows, false);
+  if (outputs <= 65536) return Plan{kRows1, 1};
+  if (rows <= 4) return Plan{kRows2, 1};
+  if (rows <= 16) return Plan{kRows4, 1};
+  if (rows <= 32) return Plan{outputs <= 131072 ? kRows2 : kRows4x2, 1};
+  return Plan{outputs <= 262144 ? kRows4 : kRows4x2, 1};
+}
+
+// Workspace of a plan: the splits' sums.
+size_t plan_ws(const Plan& pl, int64_t m, int64_t rows) {
+  return pl.splits > 1 ? align256((size_t)pl.splits * (size_t)rows * (size_t)m * sizeof(float)) : 0;
+}
+
+template <int XT, int WR, int WC, int RB, int CB, int PB>
 gptq_status launch_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStream_t st) {
   constexpr bool MX = XT == kMx;
   constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB;
-  constexpr int kLds = 2 * (MX ? BM + BN : BN) * kStageRow;
+  constexpr int kLds = tile_lds<XT, WR, WC, RB, CB, PB>();
+  const int64_t cols = round_up(std::max<int64_t>(ceil_div(p.n, pl.splits), 1), kSplitCols);
   TileGrid tg{(int)ceil_div(p.m, BM), (int)max_tiles(p.rows, p.experts, p.offsets != nullptr, BN), pl.splits,
-              pl.stages_per_split, static_cast<float*>(ws)};
+              (int)cols, static_cast<float*>(ws)};
   const int64_t items = (int64_t)tg.row_tiles * tg.tok_tiles * tg.splits;
   if (items > ((int64_t)1 << 30)) return GPTQ_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)round_up(items, kXcds);
@@ -789,7 +1239,8 @@ gptq_status launch_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStrea
   const bool direct = ((reinterpret_cast<uintptr_t>(p.X) | (uint64_t)(p.ldx * xb)) & 15) == 0 &&
                       (!MX || ((reinterpret_cast<uintptr_t>(p.W) | (uint64_t)(p.ldp * 4) | (uint64_t)(p.w_stride * 4)) &
                                15) == 0);
-  auto* k = direct ? mx_tile_kernel<XT, WR, WC, RB, CB, true> : mx_tile_kernel<XT, WR, WC, RB, CB, false>;
+  // By registers, one panel a stage: they have to hold it.
+  auto* k = direct ? mx_tile_kernel<XT, WR, WC, RB, CB, PB, true> : mx_tile_kernel<XT, WR, WC, RB, CB, 1, false>;
   if (kLds > 65536)
     GPTQ_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
   k<<<grid, 64 * WR * WC, kLds, st>>>(p, tg);
@@ -802,22 +1253,54 @@ gptq_status launch_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStrea
   return GPTQ_OK;
 }
 
+template <int XT, int RT, int NT, int D>
+gptq_status launch_rows(const MxOperands& p, int waves, hipStream_t st) {
+  const int64_t grid = ceil_div(p.m, 16 * RT) * max_tiles(p.rows, p.experts, p.offsets != nullptr, 16 * NT);
+  if (grid > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  mx_rows_kernel<XT, RT, NT, D>
+      <<<(unsigned)grid, 64 * waves, waves * RT * NT * 64 * sizeof(floatx4), st>>>(p);
+  GPTQ_TRY_LAUNCH();
+  return GPTQ_OK;
+}
+
+template <int XT, int RT, int NT, int XR>
+gptq_status launch_stream(const MxOperands& p, hipStream_t st) {
+  const int64_t grid = ceil_div(p.m, 64 * RT) * max_tiles(p.rows, p.experts, p.offsets != nullptr, 16 * NT);
+  if (grid > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
+  mx_stream_kernel<XT, RT, NT, XR><<<(unsigned)grid, 256, 2 * 64 * XR * 16, st>>>(p);
+  GPTQ_TRY_LAUNCH();
+  return GPTQ_OK;
+}
+
 template <int XT>
-gptq_status launch(const MxOperands& p, hipStream_t st) {
+gptq_status launch(const MxOperands& p, void* ws, size_t ws_bytes, hipStream_t st) {
   Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, XT == kMx);
   // The tile kernels address the rows of a tile with 32 bits.
   constexpr int64_t kMaxPitch = (int64_t)1 << 22;
   if (p.ldx * (XT == kMx ? 4 : 2) > kMaxPitch || p.ldp * 4 > kMaxPitch || p.lds > kMaxPitch || p.ldxs > kMaxPitch)
-    pl.kind = 0;
-  if (pl.kind != 0) return launch_tiles<XT, 2, 2, 4, 4>(p, pl, nullptr, st);
-  constexpr int kRT = 1, kNT = 1, kWaves = 8;
-  constexpr int64_t kMaxGridY = 65535;
-  const int64_t toks = max_tiles(p.rows, p.experts, p.offsets != nullptr, 16 * kNT);
-  if (toks > kMaxGridY) return GPTQ_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)ceil_div(p.m, 16 * kRT), (unsigned)toks);
-  mx_rows_kernel<XT, kRT, kNT><<<grid, 64 * kWaves, kWaves * kRT * kNT * 64 * sizeof(floatx4), st>>>(p);
-  GPTQ_TRY_LAUNCH();
-  return GPTQ_OK;
+    pl = Plan{kRows2, 1};
+  const size_t need = plan_ws(pl, p.m, p.rows);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return GPTQ_ERR_WORKSPACE;
+  constexpr int P2 = XT == kMx ? 1 : 2, P4 = XT == kMx ? 1 : 4;        // panels per stage
+  switch (pl.kind) {
+    case kTile256x256: return launch_tiles<XT, 4, 2, 2, 4, P2>(p, pl, ws, st);
+    case kTile256x128: return launch_tiles<XT, 4, 1, 2, 4, P2>(p, pl, ws, st);
+    case kTile128x128: return launch_tiles<XT, 4, 1, 1, 4, P2>(p, pl, ws, st);
+    case kTile128x64: return launch_tiles<XT, 4, 1, 1, 2, P4>(p, pl, ws, st);
+    case kTile128x32: return launch_tiles<XT, 4, 1, 1, 1, P4>(p, pl, ws, st);
+    case kRows1: return launch_rows<XT, 1, 1, 4>(p, 8, st);
+    case kRows4: return launch_rows<XT, 4, 1, 2>(p, 8, st);
+    case kRows2x2: return launch_rows<XT, 2, 2, 2>(p, 8, st);
+    case kRows4x2: return launch_rows<XT, 4, 2, 1>(p, 8, st);
+    case kStream1:
+      if constexpr (XT != kMx) return launch_stream<XT, 1, 1, 4>(p, st);
+      break;
+    case kStream3:
+      if constexpr (XT != kMx) return launch_stream<XT, 3, 1, 16>(p, st);
+      break;
+    default: break;
+  }
+  return launch_rows<XT, 2, 1, 2>(p, 8, st);
 }
 
 // Checks shared by the products; `rows` rows of X against `experts` matrices.
@@ -836,8 +1319,13 @@ gptq_status check(int64_t m, int64_t n, int64_t rows, int64_t experts, int64_t l
 using namespace gptq;
 
 extern "C" size_t gptq_mx_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, int64_t experts) {
-  (void)m; (void)n; (void)rows; (void)experts;
-  return 0;
+  if (m <= 0 || n < 0 || rows <= 0 || experts <= 0 || n > kMxMaxCols || m > GPTQ_MX_MAX_ROWS ||
+      rows > GPTQ_MX_MAX_ROWS || experts > GPTQ_MX_MAX_EXPERTS)
+    return 0;
+  // Of one matrix with either kind of X; products grouped by expert need none.
+  if (experts > 1) return 0;
+  return std::max(plan_ws(make_plan(m, n, rows, 1, false, false), m, rows),
+                  plan_ws(make_plan(m, n, rows, 1, false, true), m, rows));
 }
 
 extern "C" gptq_status gptq_mx_gemm_grouped(const uint32_t* packed, int64_t experts, int64_t m, int64_t n,
@@ -853,11 +1341,10 @@ extern "C" gptq_status gptq_mx_gemm_grouped(const uint32_t* packed, int64_t expe
   if (m == 0 || rows == 0 || experts == 0) return GPTQ_OK;
   if (offsets == nullptr || Y == nullptr) return GPTQ_ERR_INVALID_ARG;
   if (n > 0 && (packed == nullptr || scales == nullptr || X == nullptr)) return GPTQ_ERR_INVALID_ARG;
-  (void)ws; (void)ws_bytes;
   const MxOperands p{packed, scales, ld_packed, ld_scales, stride_packed, stride_scales, (int)m, (int)n, X, nullptr,
                      ldx, 0, (int)rows, offsets, (int)experts, Y, ldy, y_dtype};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return x_dtype == GPTQ_F16 ? launch<GPTQ_F16>(p, st) : launch<GPTQ_BF16>(p, st);
+  return x_dtype == GPTQ_F16 ? launch<GPTQ_F16>(p, ws, ws_bytes, st) : launch<GPTQ_BF16>(p, ws, ws_bytes, st);
 }
 
 extern "C" gptq_status gptq_mx_gemm(const uint32_t* packed, int64_t m, int64_t n, int64_t ld_packed,
@@ -871,11 +1358,10 @@ extern "C" gptq_status gptq_mx_gemm(const uint32_t* packed, int64_t m, int64_t n
   if (m == 0 || batch == 0) return GPTQ_OK;
   if (Y == nullptr || (n > 0 && (packed == nullptr || scales == nullptr || X == nullptr)))
     return GPTQ_ERR_INVALID_ARG;
-  (void)ws; (void)ws_bytes;
   const MxOperands p{packed, scales, ld_packed, ld_scales, 0, 0, (int)m, (int)n, X, nullptr,
                      ldx, 0, (int)batch, nullptr, 1, Y, ldy, y_dtype};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return x_dtype == GPTQ_F16 ? launch<GPTQ_F16>(p, st) : launch<GPTQ_BF16>(p, st);
+  return x_dtype == GPTQ_F16 ? launch<GPTQ_F16>(p, ws, ws_bytes, st) : launch<GPTQ_BF16>(p, ws, ws_bytes, st);
 }
 
 extern "C" gptq_status gptq_mx_scaled_gemm(const uint32_t* packed, int64_t m, int64_t n, int64_t ld_packed,
@@ -889,8 +1375,7 @@ extern "C" gptq_status gptq_mx_scaled_gemm(const uint32_t* packed, int64_t m, in
   if (m == 0 || batch == 0) return GPTQ_OK;
   if (Y == nullptr || (n > 0 && (packed == nullptr || scales == nullptr || x_packed == nullptr || x_scales == nullptr)))
     return GPTQ_ERR_INVALID_ARG;
-  (void)ws; (void)ws_bytes;
   const MxOperands p{packed, scales, ld_packed, ld_scales, 0, 0, (int)m, (int)n, x_packed, x_scales,
                      ld_xpacked, ld_xscales, (int)batch, nullptr, 1, Y, ldy, y_dtype};
-  return launch<kMx>(p, static_cast<hipStream_t>(stream));
+  return launch<kMx>(p, ws, ws_bytes, static_cast<hipStream_t>(stream));
 }
