@@ -375,42 +375,37 @@ def gptq_dequant_gemm(packed, scales, zeros, X, n: int, bits: int, group_size: i
 # ---------------------------------------------------------------------------
 # Microscaled weights (MXFP4).
 # ---------------------------------------------------------------------------
-class _on_device:
-    """Makes a tensor's device current and, when one is given, `stream`: the
-    outputs and the workspace a call allocates then belong to the stream that
-    uses them.  Enters as the stream's handle."""
-
-    def __init__(self, t, stream):
-        torch = _torch()
-        if stream is not None:
-            if stream.device != t.device:
-                raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
-            self._ctx = torch.cuda.stream(stream)
-        elif t.device.index != torch.cuda.current_device():
-            self._ctx = torch.cuda.device(t.device)
-        else:
-            self._ctx = None
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+# Host time counts here (a decode product runs about 5 us on the GPU), so the
+# checks below compare without building anything unless they fail.
+def _mx_elsewhere(t, stream):
+    """None when t's device is current and no stream is given; otherwise the
+    context to run the call in: outputs and the workspace that the call
+    allocates then belong to the stream that uses them."""
+    torch = _torch()
+    if not t.is_cuda:
+        raise ValueError("expected device tensors")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    return None if t.device.index == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
 
 
-def _mx_tensor(t, name: str, dtype, shape, device):
+def _mx_stream(t) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _mx_check(t, name: str, dtype, shape, device):
     """A device tensor of the given type and shape whose last axis is dense."""
-    if not t.is_cuda or t.device != device:
+    if t.dtype is dtype and t.shape == shape and t.device == device and (t.stride(-1) == 1 or shape[-1] <= 1):
+        return
+    if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have unit column stride")
+    raise ValueError(f"{name} must have unit column stride")
 
 
 def _ld(t, axis: int = 0):
@@ -419,34 +414,41 @@ def _ld(t, axis: int = 0):
 
 
 def _mx_output(Y, y_dtype, shape, like):
+    """(Y, its type code)."""
     torch = _torch()
     if Y is None:
-        return torch.empty(shape, dtype=torch.float32 if y_dtype is None else y_dtype, device=like.device)
-    _mx_tensor(Y, "Y", Y.dtype if y_dtype is None else y_dtype, shape, like.device)
-    return Y
+        dtype = torch.float32 if y_dtype is None else y_dtype
+    else:
+        dtype = Y.dtype if y_dtype is None else y_dtype
+        _mx_check(Y, "Y", dtype, shape, like.device)
+    code = GPTQ_F32 if dtype is torch.float32 else GPTQ_BF16 if dtype is torch.bfloat16 else \
+        GPTQ_F16 if dtype is torch.float16 else None
+    if code is None:
+        raise ValueError("Y must be float32, float16 or bfloat16")
+    return (torch.empty(shape, dtype=dtype, device=like.device) if Y is None else Y), code
 
 
-def _mx_workspace(ws, m: int, n: int, rows: int, experts: int, device):
-    if ws is not None:
-        if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
-            raise ValueError(f"ws must be contiguous on {device}")
-        return ws, ws.numel() * ws.element_size()
-    ws = _workspace(load().gptq_mx_gemm_ws_bytes(m, n, rows, experts), device)
-    return ws, 0 if ws is None else ws.numel()
+def _mx_workspace(ws, m: int, n: int, rows: int, experts: int, like):
+    """(the workspace that stays alive for the call, its address, its size)."""
+    if ws is None:
+        need = _lib.gptq_mx_gemm_ws_bytes(m, n, rows, experts)
+        if need == 0:
+            return None, None, 0
+        ws = _workspace(need, like.device)
+    elif ws.device != like.device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {like.device}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _mx_x(X):
+def _mx_x(X) -> int:
+    """Type code of 16-bit activations."""
     torch = _torch()
-    _rows_check(X)
-    if X.dtype not in (torch.float16, torch.bfloat16):
+    code = GPTQ_F16 if X.dtype is torch.float16 else GPTQ_BF16 if X.dtype is torch.bfloat16 else None
+    if code is None:
         raise ValueError("X must be float16 or bfloat16")
-
-
-def _y_code(Y) -> int:
-    try:
-        return _dtype_code(Y)
-    except KeyError:
-        raise ValueError("Y must be float32, float16 or bfloat16") from None
+    if X.dim() != 2 or (X.shape[1] > 1 and X.stride(1) != 1):
+        raise ValueError("X must be a 2-D device tensor with unit column stride")
+    return code
 
 
 def mx_words(n: int) -> int:
@@ -469,32 +471,40 @@ def gptq_mx_quantize(W, want_wq: bool = False, out=None, stream=None):
     quantized values) or None).  `out` may hold those tensors."""
     torch = _torch()
     lib = load()
-    if not W.is_cuda or W.dim() not in (2, 3) or (W.shape[-1] > 1 and W.stride(-1) != 1):
+    ctx = _mx_elsewhere(W, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_mx_quantize(W, want_wq, out)
+    if W.dim() not in (2, 3) or (W.shape[-1] > 1 and W.stride(-1) != 1):
         raise ValueError("W must be a 2-D or 3-D device tensor with unit column stride")
     if W.dtype not in (torch.float32, torch.float16, torch.bfloat16):
         raise ValueError("W must be float32, float16 or bfloat16")
-    lead, n = W.shape[:-1], W.shape[-1]
-    with _on_device(W, stream) as st:
-        if out is None:
-            out = dict(packed=torch.empty((*lead, mx_words(n)), dtype=torch.int32, device=W.device),
-                       scales=torch.empty((*lead, mx_scales(n)), dtype=torch.uint8, device=W.device),
-                       Wq=torch.empty(W.shape, dtype=W.dtype, device=W.device) if want_wq else None)
+    lead, n, dev = W.shape[:-1], W.shape[-1], W.device
+    if out is None:
+        packed = torch.empty((*lead, mx_words(n)), dtype=torch.int32, device=dev)
+        scales = torch.empty((*lead, mx_scales(n)), dtype=torch.uint8, device=dev)
+        wq = torch.empty(W.shape, dtype=W.dtype, device=dev) if want_wq else None
+        out = dict(packed=packed, scales=scales, Wq=wq)
+    else:
+        packed, scales, wq = out["packed"], out["scales"], out.setdefault("Wq", None)
+        _mx_check(packed, "packed", torch.int32, (*lead, mx_words(n)), dev)
+        _mx_check(scales, "scales", torch.uint8, (*lead, mx_scales(n)), dev)
+        if wq is not None:
+            _mx_check(wq, "Wq", W.dtype, W.shape, dev)
+    lds = []
+    for t in (W, packed, scales, wq):
+        if t is None:
+            lds.append(0)
+        elif t.dim() == 2:
+            lds.append(_ld(t))
         else:
-            out.setdefault("Wq", None)
-            _mx_tensor(out["packed"], "packed", torch.int32, (*lead, mx_words(n)), W.device)
-            _mx_tensor(out["scales"], "scales", torch.uint8, (*lead, mx_scales(n)), W.device)
-            if out["Wq"] is not None:
-                _mx_tensor(out["Wq"], "Wq", W.dtype, W.shape, W.device)
-        dense = []
-        for t in (W, out["packed"], out["scales"], out["Wq"]):
-            if t is not None and t.dim() == 3:
-                if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) != t.shape[1] * _ld(t, 1):
-                    raise ValueError("stacked matrices must follow one another row by row")
-                t = t.as_strided((t.shape[0] * t.shape[1], t.shape[2]), (_ld(t, 1), 1))
-            dense.append(t)
-        w, packed, scales, wq = dense
-        rc = lib.gptq_mx_quantize(_ptr(w), _dtype_code(w), w.shape[0], n, _ld(w), _ptr(packed), _ld(packed),
-                                  _ptr(scales), _ld(scales), _ptr(wq), 0 if wq is None else _ld(wq), st)
+            ld = _ld(t, 1) if t.shape[1] > 1 else t.stride(0) if t.shape[0] > 1 else t.shape[2]
+            if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) != t.shape[1] * ld:
+                raise ValueError("stacked matrices must follow one another row by row")
+            lds.append(ld)
+    m = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    rc = lib.gptq_mx_quantize(W.data_ptr(), _dtype_code(W), m, n, lds[0], packed.data_ptr(), lds[1],
+                              scales.data_ptr(), lds[2], None if wq is None else wq.data_ptr(), lds[3], _mx_stream(W))
     _check(rc, "gptq_mx_quantize")
     return out
 
@@ -506,17 +516,19 @@ def gptq_mx_gemm(packed, scales, X, Y=None, y_dtype=None, ws=None, stream=None):
     leading dimension)."""
     torch = _torch()
     lib = load()
-    _mx_x(X)
+    ctx = _mx_elsewhere(X, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_mx_gemm(packed, scales, X, Y, y_dtype, ws)
+    xc = _mx_x(X)
     batch, n = X.shape
-    m = packed.shape[0]
-    _mx_tensor(packed, "packed", torch.int32, (m, mx_words(n)), X.device)
-    _mx_tensor(scales, "scales", torch.uint8, (m, mx_scales(n)), X.device)
-    with _on_device(X, stream) as st:
-        Y = _mx_output(Y, y_dtype, (batch, m), X)
-        yc = _y_code(Y)
-        ws, ws_bytes = _mx_workspace(ws, m, n, batch, 1, X.device)
-        rc = lib.gptq_mx_gemm(_ptr(packed), m, n, _ld(packed), _ptr(scales), _ld(scales), _ptr(X), _dtype_code(X),
-                              batch, _ld(X), _ptr(Y), yc, _ld(Y), _ptr(ws), ws_bytes, st)
+    m, dev = packed.shape[0], X.device
+    _mx_check(packed, "packed", torch.int32, (m, mx_words(n)), dev)
+    _mx_check(scales, "scales", torch.uint8, (m, mx_scales(n)), dev)
+    Y, yc = _mx_output(Y, y_dtype, (batch, m), X)
+    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, batch, 1, X)
+    rc = lib.gptq_mx_gemm(packed.data_ptr(), m, n, _ld(packed), scales.data_ptr(), _ld(scales), X.data_ptr(), xc,
+                          batch, _ld(X), Y.data_ptr(), yc, _ld(Y), ws_at, ws_bytes, _mx_stream(X))
     _check(rc, "gptq_mx_gemm")
     return Y
 
@@ -529,21 +541,24 @@ def gptq_mx_gemm_grouped(packed, scales, X, offsets, Y=None, y_dtype=None, ws=No
     expert are left as they were (unset when Y is allocated here)."""
     torch = _torch()
     lib = load()
-    _mx_x(X)
-    rows, n = X.shape
+    ctx = _mx_elsewhere(X, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_mx_gemm_grouped(packed, scales, X, offsets, Y, y_dtype, ws)
+    xc = _mx_x(X)
     if packed.dim() != 3:
         raise ValueError("packed must be experts x m x words")
-    experts, m = packed.shape[:2]
-    _mx_tensor(packed, "packed", torch.int32, (experts, m, mx_words(n)), X.device)
-    _mx_tensor(scales, "scales", torch.uint8, (experts, m, mx_scales(n)), X.device)
-    _mx_tensor(offsets, "offsets", torch.int32, (experts + 1,), X.device)
-    with _on_device(X, stream) as st:
-        Y = _mx_output(Y, y_dtype, (rows, m), X)
-        yc = _y_code(Y)
-        ws, ws_bytes = _mx_workspace(ws, m, n, rows, experts, X.device)
-        rc = lib.gptq_mx_gemm_grouped(_ptr(packed), experts, m, n, _ld(packed, 1), packed.stride(0), _ptr(scales),
-                                      _ld(scales, 1), scales.stride(0), _ptr(X), _dtype_code(X), rows, _ld(X),
-                                      _ptr(offsets), _ptr(Y), yc, _ld(Y), _ptr(ws), ws_bytes, st)
+    rows, n = X.shape
+    experts, m, _ = packed.shape
+    dev = X.device
+    _mx_check(packed, "packed", torch.int32, (experts, m, mx_words(n)), dev)
+    _mx_check(scales, "scales", torch.uint8, (experts, m, mx_scales(n)), dev)
+    _mx_check(offsets, "offsets", torch.int32, (experts + 1,), dev)
+    Y, yc = _mx_output(Y, y_dtype, (rows, m), X)
+    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, rows, experts, X)
+    rc = lib.gptq_mx_gemm_grouped(packed.data_ptr(), experts, m, n, _ld(packed, 1), packed.stride(0),
+                                  scales.data_ptr(), _ld(scales, 1), scales.stride(0), X.data_ptr(), xc, rows, _ld(X),
+                                  offsets.data_ptr(), Y.data_ptr(), yc, _ld(Y), ws_at, ws_bytes, _mx_stream(X))
     _check(rc, "gptq_mx_gemm_grouped")
     return Y
 
@@ -554,21 +569,21 @@ def gptq_mx_scaled_gemm(packed, scales, x_packed, x_scales, n: int, Y=None, y_dt
     and of X (batch rows), n columns each."""
     torch = _torch()
     lib = load()
+    ctx = _mx_elsewhere(packed, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_mx_scaled_gemm(packed, scales, x_packed, x_scales, n, Y, y_dtype, ws)
     n = int(n)
-    m, batch = packed.shape[0], x_packed.shape[0]
-    if not packed.is_cuda:
-        raise ValueError("packed must be a device tensor")
-    _mx_tensor(packed, "packed", torch.int32, (m, mx_words(n)), packed.device)
-    _mx_tensor(scales, "scales", torch.uint8, (m, mx_scales(n)), packed.device)
-    _mx_tensor(x_packed, "x_packed", torch.int32, (batch, mx_words(n)), packed.device)
-    _mx_tensor(x_scales, "x_scales", torch.uint8, (batch, mx_scales(n)), packed.device)
-    with _on_device(packed, stream) as st:
-        Y = _mx_output(Y, y_dtype, (batch, m), packed)
-        yc = _y_code(Y)
-        ws, ws_bytes = _mx_workspace(ws, m, n, batch, 1, packed.device)
-        rc = lib.gptq_mx_scaled_gemm(_ptr(packed), m, n, _ld(packed), _ptr(scales), _ld(scales), _ptr(x_packed),
-                                     batch, _ld(x_packed), _ptr(x_scales), _ld(x_scales), _ptr(Y), yc, _ld(Y),
-                                     _ptr(ws), ws_bytes, st)
+    m, batch, dev = packed.shape[0], x_packed.shape[0], packed.device
+    _mx_check(packed, "packed", torch.int32, (m, mx_words(n)), dev)
+    _mx_check(scales, "scales", torch.uint8, (m, mx_scales(n)), dev)
+    _mx_check(x_packed, "x_packed", torch.int32, (batch, mx_words(n)), dev)
+    _mx_check(x_scales, "x_scales", torch.uint8, (batch, mx_scales(n)), dev)
+    Y, yc = _mx_output(Y, y_dtype, (batch, m), packed)
+    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, batch, 1, packed)
+    rc = lib.gptq_mx_scaled_gemm(packed.data_ptr(), m, n, _ld(packed), scales.data_ptr(), _ld(scales),
+                                 x_packed.data_ptr(), batch, _ld(x_packed), x_scales.data_ptr(), _ld(x_scales),
+                                 Y.data_ptr(), yc, _ld(Y), ws_at, ws_bytes, _mx_stream(packed))
     _check(rc, "gptq_mx_scaled_gemm")
     return Y
 
