@@ -391,64 +391,86 @@ def _mx_elsewhere(t, stream):
     return None if t.device.index == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
 
 
-def _mx_stream(t) -> int:
-    return _torch()._C._cuda_getCurrentRawStream(t.device.index)
+def _mx_rows(t, name: str, dtype, m: int, cols: int, device) -> int:
+    """Leading dimension of an m x cols device tensor of the given type whose
+    columns are dense (the stride of a single row means nothing)."""
+    if t.dtype is dtype and t.shape == (m, cols) and t.device == device:
+        ld, unit = t.stride()
+        if unit == 1 or cols <= 1:
+            return ld if m > 1 else cols
+    _mx_refuse(t, name, dtype, (m, cols), device)
 
 
-def _mx_check(t, name: str, dtype, shape, device):
-    """A device tensor of the given type and shape whose last axis is dense."""
-    if t.dtype is dtype and t.shape == shape and t.device == device and (t.stride(-1) == 1 or shape[-1] <= 1):
-        return
+def _mx_stack(t, name: str, dtype, experts: int, m: int, cols: int, device):
+    """(leading dimension, stride of a matrix) of experts such matrices."""
+    if t.dtype is dtype and t.shape == (experts, m, cols) and t.device == device:
+        stride, ld, unit = t.stride()
+        if unit == 1 or cols <= 1:
+            return (ld if m > 1 else cols), stride
+    _mx_refuse(t, name, dtype, (experts, m, cols), device)
+
+
+def _mx_refuse(t, name: str, dtype, shape, device):
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
+        raise ValueError(f"{name} must have shape {shape}")
     raise ValueError(f"{name} must have unit column stride")
 
 
-def _ld(t, axis: int = 0):
-    """Leading dimension (the stride of a single row means nothing)."""
-    return t.stride(axis) if t.shape[axis] > 1 else t.shape[-1]
-
-
-def _mx_output(Y, y_dtype, shape, like):
-    """(Y, its type code)."""
-    torch = _torch()
-    if Y is None:
-        dtype = torch.float32 if y_dtype is None else y_dtype
-    else:
-        dtype = Y.dtype if y_dtype is None else y_dtype
-        _mx_check(Y, "Y", dtype, shape, like.device)
+def _mx_output(torch, Y, y_dtype, rows: int, m: int, device):
+    """(Y, its type code, its leading dimension)."""
+    dtype = y_dtype or (torch.float32 if Y is None else Y.dtype)
     code = GPTQ_F32 if dtype is torch.float32 else GPTQ_BF16 if dtype is torch.bfloat16 else \
         GPTQ_F16 if dtype is torch.float16 else None
     if code is None:
         raise ValueError("Y must be float32, float16 or bfloat16")
-    return (torch.empty(shape, dtype=dtype, device=like.device) if Y is None else Y), code
+    if Y is None:
+        return torch.empty((rows, m), dtype=dtype, device=device), code, m
+    return Y, code, _mx_rows(Y, "Y", dtype, rows, m, device)
 
 
-def _mx_workspace(ws, m: int, n: int, rows: int, experts: int, like):
+def _mx_workspace(ws, m: int, n: int, rows: int, experts: int, device):
     """(the workspace that stays alive for the call, its address, its size)."""
     if ws is None:
         need = _lib.gptq_mx_gemm_ws_bytes(m, n, rows, experts)
         if need == 0:
             return None, None, 0
-        ws = _workspace(need, like.device)
-    elif ws.device != like.device or not ws.is_contiguous():
-        raise ValueError(f"ws must be contiguous on {like.device}")
+        ws = _workspace(need, device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {device}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _mx_x(X) -> int:
-    """Type code of 16-bit activations."""
-    torch = _torch()
+def _mx_x(torch, X):
+    """(rows, columns, leading dimension, type code) of 16-bit activations."""
     code = GPTQ_F16 if X.dtype is torch.float16 else GPTQ_BF16 if X.dtype is torch.bfloat16 else None
     if code is None:
         raise ValueError("X must be float16 or bfloat16")
-    if X.dim() != 2 or (X.shape[1] > 1 and X.stride(1) != 1):
-        raise ValueError("X must be a 2-D device tensor with unit column stride")
-    return code
+    if X.dim() == 2:
+        rows, n = X.shape
+        ld, unit = X.stride()
+        if unit == 1 or n <= 1:
+            return rows, n, (ld if rows > 1 else n), code
+    raise ValueError("X must be a 2-D device tensor with unit column stride")
+
+
+def _mx_folded(t, name: str, dtype, lead, cols: int, device) -> int:
+    """Leading dimension of a matrix, or of a stack of matrices that follow one
+    another row by row, as one matrix."""
+    if len(lead) == 1:
+        return _mx_rows(t, name, dtype, lead[0], cols, device)
+    experts, m = lead
+    ld, stride = _mx_stack(t, name, dtype, experts, m, cols, device)
+    if experts <= 1 or m == 0:
+        return ld
+    if m == 1:
+        return stride
+    if stride != m * ld:
+        raise ValueError(f"the matrices of {name} must follow one another row by row")
+    return ld
 
 
 def mx_words(n: int) -> int:
@@ -475,37 +497,31 @@ def gptq_mx_quantize(W, want_wq: bool = False, out=None, stream=None):
     if ctx is not None:
         with ctx:
             return gptq_mx_quantize(W, want_wq, out)
-    if W.dim() not in (2, 3) or (W.shape[-1] > 1 and W.stride(-1) != 1):
-        raise ValueError("W must be a 2-D or 3-D device tensor with unit column stride")
+    if W.dim() not in (2, 3):
+        raise ValueError("W must be a 2-D or 3-D device tensor")
     if W.dtype not in (torch.float32, torch.float16, torch.bfloat16):
         raise ValueError("W must be float32, float16 or bfloat16")
-    lead, n, dev = W.shape[:-1], W.shape[-1], W.device
+    *lead, n = W.shape
+    dev = W.device
+    words, blocks = -(-n // 8), -(-n // MX_BLOCK)
     if out is None:
-        packed = torch.empty((*lead, mx_words(n)), dtype=torch.int32, device=dev)
-        scales = torch.empty((*lead, mx_scales(n)), dtype=torch.uint8, device=dev)
+        packed = torch.empty((*lead, words), dtype=torch.int32, device=dev)
+        scales = torch.empty((*lead, blocks), dtype=torch.uint8, device=dev)
         wq = torch.empty(W.shape, dtype=W.dtype, device=dev) if want_wq else None
         out = dict(packed=packed, scales=scales, Wq=wq)
+        ld_packed, ld_scales, ld_wq = words, blocks, n
     else:
         packed, scales, wq = out["packed"], out["scales"], out.setdefault("Wq", None)
-        _mx_check(packed, "packed", torch.int32, (*lead, mx_words(n)), dev)
-        _mx_check(scales, "scales", torch.uint8, (*lead, mx_scales(n)), dev)
-        if wq is not None:
-            _mx_check(wq, "Wq", W.dtype, W.shape, dev)
-    lds = []
-    for t in (W, packed, scales, wq):
-        if t is None:
-            lds.append(0)
-        elif t.dim() == 2:
-            lds.append(_ld(t))
-        else:
-            ld = _ld(t, 1) if t.shape[1] > 1 else t.stride(0) if t.shape[0] > 1 else t.shape[2]
-            if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) != t.shape[1] * ld:
-                raise ValueError("stacked matrices must follow one another row by row")
-            lds.append(ld)
+        ld_packed = _mx_folded(packed, "packed", torch.int32, lead, words, dev)
+        ld_scales = _mx_folded(scales, "scales", torch.uint8, lead, blocks, dev)
+        ld_wq = 0 if wq is None else _mx_folded(wq, "Wq", W.dtype, lead, n, dev)
+    code = GPTQ_F32 if W.dtype is torch.float32 else GPTQ_BF16 if W.dtype is torch.bfloat16 else GPTQ_F16
     m = lead[0] if len(lead) == 1 else lead[0] * lead[1]
-    rc = lib.gptq_mx_quantize(W.data_ptr(), _dtype_code(W), m, n, lds[0], packed.data_ptr(), lds[1],
-                              scales.data_ptr(), lds[2], None if wq is None else wq.data_ptr(), lds[3], _mx_stream(W))
-    _check(rc, "gptq_mx_quantize")
+    rc = lib.gptq_mx_quantize(W.data_ptr(), code, m, n, _mx_folded(W, "W", W.dtype, lead, n, dev), packed.data_ptr(),
+                              ld_packed, scales.data_ptr(), ld_scales, None if wq is None else wq.data_ptr(), ld_wq,
+                              torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "gptq_mx_quantize")
     return out
 
 
@@ -520,16 +536,16 @@ def gptq_mx_gemm(packed, scales, X, Y=None, y_dtype=None, ws=None, stream=None):
     if ctx is not None:
         with ctx:
             return gptq_mx_gemm(packed, scales, X, Y, y_dtype, ws)
-    xc = _mx_x(X)
-    batch, n = X.shape
+    batch, n, ldx, xc = _mx_x(torch, X)
     m, dev = packed.shape[0], X.device
-    _mx_check(packed, "packed", torch.int32, (m, mx_words(n)), dev)
-    _mx_check(scales, "scales", torch.uint8, (m, mx_scales(n)), dev)
-    Y, yc = _mx_output(Y, y_dtype, (batch, m), X)
-    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, batch, 1, X)
-    rc = lib.gptq_mx_gemm(packed.data_ptr(), m, n, _ld(packed), scales.data_ptr(), _ld(scales), X.data_ptr(), xc,
-                          batch, _ld(X), Y.data_ptr(), yc, _ld(Y), ws_at, ws_bytes, _mx_stream(X))
-    _check(rc, "gptq_mx_gemm")
+    ldp = _mx_rows(packed, "packed", torch.int32, m, -(-n // 8), dev)
+    lds = _mx_rows(scales, "scales", torch.uint8, m, -(-n // MX_BLOCK), dev)
+    Y, yc, ldy = _mx_output(torch, Y, y_dtype, batch, m, dev)
+    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, batch, 1, dev)
+    rc = lib.gptq_mx_gemm(packed.data_ptr(), m, n, ldp, scales.data_ptr(), lds, X.data_ptr(), xc, batch, ldx,
+                          Y.data_ptr(), yc, ldy, ws_at, ws_bytes, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "gptq_mx_gemm")
     return Y
 
 
@@ -545,21 +561,23 @@ def gptq_mx_gemm_grouped(packed, scales, X, offsets, Y=None, y_dtype=None, ws=No
     if ctx is not None:
         with ctx:
             return gptq_mx_gemm_grouped(packed, scales, X, offsets, Y, y_dtype, ws)
-    xc = _mx_x(X)
+    rows, n, ldx, xc = _mx_x(torch, X)
     if packed.dim() != 3:
         raise ValueError("packed must be experts x m x words")
-    rows, n = X.shape
     experts, m, _ = packed.shape
     dev = X.device
-    _mx_check(packed, "packed", torch.int32, (experts, m, mx_words(n)), dev)
-    _mx_check(scales, "scales", torch.uint8, (experts, m, mx_scales(n)), dev)
-    _mx_check(offsets, "offsets", torch.int32, (experts + 1,), dev)
-    Y, yc = _mx_output(Y, y_dtype, (rows, m), X)
-    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, rows, experts, X)
-    rc = lib.gptq_mx_gemm_grouped(packed.data_ptr(), experts, m, n, _ld(packed, 1), packed.stride(0),
-                                  scales.data_ptr(), _ld(scales, 1), scales.stride(0), X.data_ptr(), xc, rows, _ld(X),
-                                  offsets.data_ptr(), Y.data_ptr(), yc, _ld(Y), ws_at, ws_bytes, _mx_stream(X))
-    _check(rc, "gptq_mx_gemm_grouped")
+    ldp, stride_p = _mx_stack(packed, "packed", torch.int32, experts, m, -(-n // 8), dev)
+    lds, stride_s = _mx_stack(scales, "scales", torch.uint8, experts, m, -(-n // MX_BLOCK), dev)
+    if offsets.dtype is not torch.int32 or offsets.shape != (experts + 1,) or offsets.device != dev or \
+            not offsets.is_contiguous():
+        raise ValueError(f"offsets must be {experts + 1} contiguous int32 on {dev}")
+    Y, yc, ldy = _mx_output(torch, Y, y_dtype, rows, m, dev)
+    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, rows, experts, dev)
+    rc = lib.gptq_mx_gemm_grouped(packed.data_ptr(), experts, m, n, ldp, stride_p, scales.data_ptr(), lds, stride_s,
+                                  X.data_ptr(), xc, rows, ldx, offsets.data_ptr(), Y.data_ptr(), yc, ldy, ws_at,
+                                  ws_bytes, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "gptq_mx_gemm_grouped")
     return Y
 
 
@@ -575,16 +593,18 @@ def gptq_mx_scaled_gemm(packed, scales, x_packed, x_scales, n: int, Y=None, y_dt
             return gptq_mx_scaled_gemm(packed, scales, x_packed, x_scales, n, Y, y_dtype, ws)
     n = int(n)
     m, batch, dev = packed.shape[0], x_packed.shape[0], packed.device
-    _mx_check(packed, "packed", torch.int32, (m, mx_words(n)), dev)
-    _mx_check(scales, "scales", torch.uint8, (m, mx_scales(n)), dev)
-    _mx_check(x_packed, "x_packed", torch.int32, (batch, mx_words(n)), dev)
-    _mx_check(x_scales, "x_scales", torch.uint8, (batch, mx_scales(n)), dev)
-    Y, yc = _mx_output(Y, y_dtype, (batch, m), packed)
-    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, batch, 1, packed)
-    rc = lib.gptq_mx_scaled_gemm(packed.data_ptr(), m, n, _ld(packed), scales.data_ptr(), _ld(scales),
-                                 x_packed.data_ptr(), batch, _ld(x_packed), x_scales.data_ptr(), _ld(x_scales),
-                                 Y.data_ptr(), yc, _ld(Y), ws_at, ws_bytes, _mx_stream(packed))
-    _check(rc, "gptq_mx_scaled_gemm")
+    words, blocks = -(-n // 8), -(-n // MX_BLOCK)
+    ldp = _mx_rows(packed, "packed", torch.int32, m, words, dev)
+    lds = _mx_rows(scales, "scales", torch.uint8, m, blocks, dev)
+    ldxp = _mx_rows(x_packed, "x_packed", torch.int32, batch, words, dev)
+    ldxs = _mx_rows(x_scales, "x_scales", torch.uint8, batch, blocks, dev)
+    Y, yc, ldy = _mx_output(torch, Y, y_dtype, batch, m, dev)
+    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, batch, 1, dev)
+    rc = lib.gptq_mx_scaled_gemm(packed.data_ptr(), m, n, ldp, scales.data_ptr(), lds, x_packed.data_ptr(), batch,
+                                 ldxp, x_scales.data_ptr(), ldxs, Y.data_ptr(), yc, ldy, ws_at, ws_bytes,
+                                 torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "gptq_mx_scaled_gemm")
     return Y
 
 

@@ -153,30 +153,71 @@ __device__ inline void split8(u32x4 x, u32x4& hi, u32x4& lo) {
   }
 }
 
-// Guarded loads of a row's last columns: every address is clamped to the row
-// and what lies past its end is replaced (n >= 1), without branches.
-__device__ inline uint32_t load_word(const uint32_t* row, int k, int n) {
-  const int nw = (n + 7) >> 3;
-  uint32_t v = row[min(k, nw - 1)];
-  const int left = n - 8 * k;                // columns that this word holds
-  if (left < 8) v &= (1u << (4 * max(left, 0))) - 1u;
+// Guarded loads of a row's last columns (n >= 1).  Where the row is long enough,
+// one load that ends at the row's end, shifted down to the columns asked for, so
+// that all of them are in flight together; what lies past the end is replaced.
+// Eight columns of 16-bit X from column k, zeros past the end.
+__device__ inline u32x4 load_x8_tail(const uint16_t* row, int k, int n) {
+  if (n >= 8) {
+    const int at = min(k, n - 8), s = k - at;
+    const u32x4 v = *reinterpret_cast<const u32x4_a2*>(row + at);
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    if (s & 4) {
+      lo = hi;
+      hi = 0;
+    }
+    const int bits = 16 * (s & 3);
+    lo = lo >> bits | hi << 1 << (63 - bits);
+    hi >>= bits;
+    if (s >= 8) lo = hi = 0;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
+  u32x4 v;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const int c = k + 2 * d;
+    const uint32_t lo = row[min(c, n - 1)], hi = row[min(c + 1, n - 1)];
+    v[d] = (c < n ? lo : 0u) | (c + 1 < n ? hi << 16 : 0u);
+  }
   return v;
 }
-__device__ inline uint32_t load_pair(const uint16_t* row, int k, int n) {
-  const uint32_t lo = row[min(k, n - 1)], hi = row[min(k + 1, n - 1)];
-  return (k < n ? lo : 0u) | (k + 1 < n ? hi << 16 : 0u);
+// Four words of codes from word k; codes past column n are 0.
+__device__ inline u32x4 load_w4_tail(const uint32_t* row, int k, int n) {
+  const int nw = (n + 7) >> 3;
+  u32x4 v;
+  if (nw >= 4) {
+    const int at = min(k, nw - 4), s = k - at;
+    const u32x4 l = *reinterpret_cast<const u32x4_a4*>(row + at);
+    v[0] = s == 0 ? l[0] : s == 1 ? l[1] : s == 2 ? l[2] : l[3];
+    v[1] = s == 0 ? l[1] : s == 1 ? l[2] : l[3];
+    v[2] = s == 0 ? l[2] : l[3];
+    v[3] = l[3];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = row[min(k + i, nw - 1)];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int left = n - 8 * (k + i);        // columns that this word holds
+    if (left < 8) v[i] &= (1u << (4 * max(left, 0))) - 1u;
+  }
+  return v;
 }
-__device__ inline uint32_t load_scale(const uint8_t* srow, int blk, int n) {
-  const uint32_t v = srow[min(blk, (n - 1) >> 5)];
-  return blk * kMxBlock < n ? v : (uint32_t)kMxScaleOne;
-}
-__device__ inline u32x4 load_block(const uint32_t* row, int blk, int n) {
-  return u32x4{load_word(row, 4 * blk, n), load_word(row, 4 * blk + 1, n), load_word(row, 4 * blk + 2, n),
-               load_word(row, 4 * blk + 3, n)};
-}
+// Scale bytes of four blocks; blocks past the row's end have scale 1.
 __device__ inline uint32_t load_scales4(const uint8_t* srow, int blk, int n) {
-  return load_scale(srow, blk, n) | load_scale(srow, blk + 1, n) << 8 | load_scale(srow, blk + 2, n) << 16 |
-         load_scale(srow, blk + 3, n) << 24;
+  const int nb = (n + kMxBlock - 1) >> 5;
+  uint32_t v = 0u;
+  if (nb >= 4) {
+    const int at = min(blk, nb - 4);
+    v = *reinterpret_cast<const u32_a1*>(srow + at) >> (8 * min(blk - at, 3));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v |= (uint32_t)srow[min(blk + i, nb - 1)] << (8 * i);
+  }
+  const int left = nb - blk;                 // blocks there are
+  if (left >= 4) return v;
+  const uint32_t there = (1u << (8 * max(left, 0))) - 1u;
+  return (v & there) | (kMxScaleOne * 0x01010101u & ~there);
 }
 
 // s_waitcnt immediate (gfx9 encoding): vmcnt <= v, expcnt unconstrained, lgkmcnt = 0.
@@ -377,7 +418,7 @@ __device__ inline bool rows_product(const MxOperands& p, const TokenTile& tile, 
         u.w[rt] = *reinterpret_cast<const u32x4_a4*>(wrow[rt] + 4 * blk);
         s.w[rt][0] = *reinterpret_cast<const u32_a1*>(wsrow[rt] + 4 * unit);
       } else {
-        u.w[rt] = load_block(wrow[rt], blk, p.n);
+        u.w[rt] = load_w4_tail(wrow[rt], 4 * blk, p.n);
         s.w[rt][0] = load_scales4(wsrow[rt], 4 * unit, p.n);
       }
     }
@@ -388,20 +429,17 @@ __device__ inline bool rows_product(const MxOperands& p, const TokenTile& tile, 
           u.x[nt][0] = *reinterpret_cast<const u32x4_a4*>(xrow[nt] + 16 * blk);
           s.x[nt][0] = *reinterpret_cast<const u32_a1*>(xsrow[nt] + 4 * unit);
         } else {
-          u.x[nt][0] = load_block(reinterpret_cast<const uint32_t*>(xrow[nt]), blk, p.n);
+          u.x[nt][0] = load_w4_tail(reinterpret_cast<const uint32_t*>(xrow[nt]), 4 * blk, p.n);
           s.x[nt][0] = load_scales4(xsrow[nt], 4 * unit, p.n);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < U::kX; ++j) {
           const int k = 128 * unit + 32 * j + 8 * q;
-          if (all) {
+          if (all)
             u.x[nt][j] = *reinterpret_cast<const u32x4_a2*>(xrow[nt] + 2 * k);
-          } else {
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-              u.x[nt][j][d] = load_pair(reinterpret_cast<const uint16_t*>(xrow[nt]), k + 2 * d, p.n);
-          }
+          else
+            u.x[nt][j] = load_x8_tail(reinterpret_cast<const uint16_t*>(xrow[nt]), k, p.n);
         }
       }
     }
@@ -539,16 +577,14 @@ __device__ inline bool stream_product(const MxOperands& p, const TokenTile& tile
     uint32_t ws[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      u.w[rt] = load_block(wrow[rt], 4 * unit + q, p.n);
+      u.w[rt] = load_w4_tail(wrow[rt], 16 * unit + 4 * q, p.n);
       ws[rt] = load_scales4(wsrow[rt], 4 * unit, p.n);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const uint16_t* x = X + (int64_t)min(16 * nt + c16, last) * p.ldx;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int d = 0; d < 4; ++d) u.x[nt][j][d] = load_pair(x, 128 * unit + 32 * j + 8 * q + 2 * d, p.n);
+      for (int j = 0; j < 4; ++j) u.x[nt][j] = load_x8_tail(x, 128 * unit + 32 * j + 8 * q, p.n);
     }
     multiply_unit<XT, SPLIT>(u, ws, no_xs, acc, inexact);
   }
@@ -643,15 +679,8 @@ __device__ inline u32x4 load_chunk(const char* row, int panel, int chunk) {
 }
 template <int XT>
 __device__ inline u32x4 load_chunk_tail(const char* row, int panel, int chunk, int n) {
-  u32x4 v;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    if constexpr (XT == kMx)
-      v[d] = load_word(reinterpret_cast<const uint32_t*>(row), panel * 32 + chunk * 4 + d, n);
-    else
-      v[d] = load_pair(reinterpret_cast<const uint16_t*>(row), panel * 64 + chunk * 8 + 2 * d, n);
-  }
-  return v;
+  if constexpr (XT == kMx) return load_w4_tail(reinterpret_cast<const uint32_t*>(row), panel * 32 + chunk * 4, n);
+  else return load_x8_tail(reinterpret_cast<const uint16_t*>(row), panel * 64 + chunk * 8, n);
 }
 
 // The scale bytes of the eight blocks of a microscaled stage as the lane halves
@@ -659,12 +688,8 @@ __device__ inline u32x4 load_chunk_tail(const char* row, int panel, int chunk, i
 __device__ inline u32x2 order_scales8(uint32_t lo, uint32_t hi) {
   return u32x2{__builtin_amdgcn_perm(hi, lo, 0x06040200u), __builtin_amdgcn_perm(hi, lo, 0x07050301u)};
 }
-// Those of a partial stage; blocks past the row's end have scale 1.
 __device__ inline uint32_t load_scales8_tail(const uint8_t* srow, int stage, int h, int n) {
-  uint32_t v = 0u;
-#pragma unroll 1
-  for (int j = 3; j >= 0; --j) v = v << 8 | load_scale(srow, 8 * stage + 2 * j + h, n);
-  return v;
+  return order_scales8(load_scales4(srow, 8 * stage, n), load_scales4(srow, 8 * stage + 4, n))[h];
 }
 
 // Step `step` of a microscaled stage: byte `step` of the scales.
@@ -803,7 +828,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
   // A partial last stage, element by element, into the first buffer (the loop's
   // last barrier is behind it).
   auto fill_tail = [&](int st) {
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < kPerThread; ++i)
       *my_slot(0, i) = load_chunk_tail<XT>(row_ptr(my_row(i)), st * PB + my_panel(i), tid & 7, p.n);
   };
@@ -898,7 +923,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
           const int blk = 2 * (st * PB + u) + h;
-          g.w[u][rb] = load_block(reinterpret_cast<const uint32_t*>(wbase + w_at[rb]), blk, p.n);
+          g.w[u][rb] = load_w4_tail(reinterpret_cast<const uint32_t*>(wbase + w_at[rb]), 4 * blk, p.n);
           if (u % 2 == 0) g.ws[u / 2][rb] = load_scales4(sbase + ws_at[rb], 2 * (st * PB + u), p.n);
         }
     }
@@ -972,7 +997,6 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
         __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);   // two VALU
-        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // one load
       }
     }
   };
@@ -1022,6 +1046,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
       if constexpr (MX) {
         fetch_scales(((st - s_lo) >> 2) + 1, (st - s_lo) & 3);
       }
+      __builtin_amdgcn_sched_barrier(0);     // the loads are issued before the products
       check_scales(cur);
 #pragma unroll
       for (int step = 0; step < kSteps - 1; ++step) {
@@ -1239,8 +1264,9 @@ gptq_status launch_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStrea
   const bool direct = ((reinterpret_cast<uintptr_t>(p.X) | (uint64_t)(p.ldx * xb)) & 15) == 0 &&
                       (!MX || ((reinterpret_cast<uintptr_t>(p.W) | (uint64_t)(p.ldp * 4) | (uint64_t)(p.w_stride * 4)) &
                                15) == 0);
-  // By registers, one panel a stage: they have to hold it.
-  auto* k = direct ? mx_tile_kernel<XT, WR, WC, RB, CB, PB, true> : mx_tile_kernel<XT, WR, WC, RB, CB, 1, false>;
+  // By registers, a stage of the large tiles is one panel: they have to hold it.
+  constexpr int PR = RB * CB > 4 ? 1 : PB;
+  auto* k = direct ? mx_tile_kernel<XT, WR, WC, RB, CB, PB, true> : mx_tile_kernel<XT, WR, WC, RB, CB, PR, false>;
   if (kLds > 65536)
     GPTQ_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
   k<<<grid, 64 * WR * WC, kLds, st>>>(p, tg);
