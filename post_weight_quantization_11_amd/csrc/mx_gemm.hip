@@ -25,6 +25,7 @@ typedef uint16_t u16_a1 __attribute__((aligned(1)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
+typedef floatx4 floatx4_a4 __attribute__((aligned(4)));
 
 constexpr int kMx = 3;                       // X operand kinds: GPTQ_F16, GPTQ_BF16, microscaled
 
@@ -623,8 +624,9 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxOperands p) {
 // A panel is 128 bytes of every row of X (64 or 256 columns), a stage one or
 // more panels, staged in LDS in two buffers: while a stage is multiplied the
 // next one arrives.  The 16-byte chunk c of a panel's local row r lies in slot
-// c ^ (r % 8) of the row's eight, so the reads of one chunk over 32 rows touch
-// all banks evenly.
+// c ^ r % 8 ^ r / 8 % 2 of the row's eight: sixteen neighbouring rows' chunks c
+// cover all 64 banks (with c ^ r % 8 alone rows r and r + 8 share theirs, which
+// doubled the cycles LDS was busy).
 //
 // 16-bit X: the codes of W go from memory straight into registers (a row's 32
 // codes of a block are 16 bytes: 1/4 of what X needs) and become operands
@@ -645,6 +647,7 @@ template <> __device__ inline floatx16 mfma32<GPTQ_BF16>(u32x4 a, u32x4 b, float
 }
 
 constexpr int kPanelRow = 128;               // bytes of a row in a panel
+__device__ inline int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
 // Floats per row of X in a wave's output block: two (one) row blocks of W, and
 // four so that neighbouring rows start in different banks.
@@ -709,7 +712,6 @@ __device__ inline void store8(void* Y, int64_t at, int left, floatx4 lo, floatx4
   if constexpr (YT == GPTQ_F32) {
     float* y = static_cast<float*>(Y) + at;
     if (left >= 8) {
-      typedef floatx4 floatx4_a4 __attribute__((aligned(4)));
       reinterpret_cast<floatx4_a4*>(y)[0] = lo;
       reinterpret_cast<floatx4_a4*>(y)[1] = hi;
       return;
@@ -736,6 +738,53 @@ __device__ inline void store8(void* Y, int64_t at, int left, floatx4 lo, floatx4
     for (int i = 0; i < 7; ++i)
       if (i < left) y[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
   }
+}
+
+// Stores a workgroup's sums.  Accumulator register i of lane l: X row 8 (i / 4) +
+// 4 (l / 32) + i % 4, W row l % 32.  Each wave passes its sums through LDS of its
+// own (the stages are no longer read), 32 rows of X x 64 (32) rows of W at a
+// time, so that a lane stores eight neighbouring ones.
+template <int WR, int WC, int RB, int CB>
+__device__ inline void store_tile(const MxOperands& p, const TileGrid& tg, const TokenTile& tile, int r0, int split,
+                                  const floatx16 (&acc)[RB][CB], unsigned char* smem) {
+  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / WC, wc = wave % WC;
+  constexpr int RP = RB % 2 == 0 ? 2 : 1, kPitch = out_pitch(RB);
+  float* my = reinterpret_cast<float*>(smem) + wave * 32 * kPitch;
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+    for (int r2 = 0; r2 < RB; r2 += RP) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int b = 0; b < RP; ++b)
+          my[(8 * (i >> 2) + 4 * h + (i & 3)) * kPitch + 32 * b + l32] = acc[r2 + b][cb][i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+      constexpr int kLanes = 4 * RP;         // lanes that share a row of X
+      const int xr = lane / kLanes, c = lane % kLanes * 8;
+      const int r = r0 + (wr * RB + r2) * 32 + c;
+#pragma unroll 1
+      for (int k = 0; k < 32; k += 64 / kLanes) {
+        const int x = tile.begin + (wc * CB + cb) * 32 + k + xr;
+        const floatx4 lo = *reinterpret_cast<const floatx4*>(my + (k + xr) * kPitch + c);
+        const floatx4 hi = *reinterpret_cast<const floatx4*>(my + (k + xr) * kPitch + c + 4);
+        if (x < tile.end && r < p.m) {
+          if (tg.splits > 1)
+            store8<GPTQ_F32>(tg.part, ((int64_t)split * p.rows + x) * p.m + r, p.m - r, lo, hi);
+          else if (p.y_dtype == GPTQ_F32)
+            store8<GPTQ_F32>(p.Y, (int64_t)x * p.ldy + r, p.m - r, lo, hi);
+          else if (p.y_dtype == GPTQ_F16)
+            store8<GPTQ_F16>(p.Y, (int64_t)x * p.ldy + r, p.m - r, lo, hi);
+          else
+            store8<GPTQ_BF16>(p.Y, (int64_t)x * p.ldy + r, p.m - r, lo, hi);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+    }
 }
 
 // One tile.  PB: panels of 128 bytes per row in a stage.  DIRECT: 16-byte
@@ -794,7 +843,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
   auto my_slot = [&](int buf, int i) {
     const int r = my_row(i);
     return reinterpret_cast<u32x4*>(smem + buf * kBuf + my_panel(i) * kPanel + r * kPanelRow +
-                                    (((tid & 7) ^ (r & 7)) << 4));
+                                    (((tid & 7) ^ swizzle(r)) << 4));
   };
   u32x4 stage_regs[DIRECT ? 1 : kPerThread];
   auto fetch = [&](int st) {                 // by registers: any alignment
@@ -807,12 +856,15 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
     for (int i = 0; i < kPerThread; ++i) *my_slot(buf, i) = stage_regs[DIRECT ? 0 : i];
   };
   // Directly: a wave's instruction moves eight rows, lane i the chunk that
-  // belongs into slot i % 8 of row i / 8.
+  // belongs into slot i % 8 of row i / 8.  (Eight-row groups alternate between
+  // the waves, so a wave's are all even or all odd.)
+  static_assert(kWaves % 2 == 0, "a wave's eight-row groups have one parity");
   uint32_t direct_offset[DIRECT ? kDirect / PB : 1];
   if constexpr (DIRECT) {
 #pragma unroll
     for (int i = 0; i < kDirect / PB; ++i)
-      direct_offset[i] = row_offset((wave + i * kWaves) * 8 + (lane >> 3)) + (((lane & 7) ^ (lane >> 3)) << 4);
+      direct_offset[i] =
+          row_offset((wave + i * kWaves) * 8 + (lane >> 3)) + (((lane & 7) ^ swizzle(wave * 8 + (lane >> 3))) << 4);
   }
   auto fetch_direct = [&](int st, int buf, int i) {
     const int rows8 = wave + i % (kDirect / PB) * kWaves, panel = i / (kDirect / PB);
@@ -945,7 +997,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
   uint32_t frag_at[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    frag_at[j] = (uint32_t)((wc * CB * 32 + l32) * kPanelRow + (((MX ? 2 * j + h : 4 * h + j) ^ (l32 & 7)) << 4));
+    frag_at[j] = (uint32_t)((wc * CB * 32 + l32) * kPanelRow + (((MX ? 2 * j + h : 4 * h + j) ^ swizzle(l32)) << 4));
   const uint32_t w_off = (uint32_t)((BN + (wr * RB - wc * CB) * 32) * kPanelRow);
   auto load_frags = [&](int buf, int step, Frags& o) {
     const unsigned char* at = smem + buf * kBuf + (MX ? 0 : step / 4) * kPanel + frag_at[step % 4];
@@ -1069,7 +1121,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
       cur = nxt;
     }
   }
-  if (s_whole < s_hi) {
+  if (s_lo <= s_whole && s_whole < s_hi) {
     lds_barrier();                           // the loop's last reads are done
     fill_tail(s_whole);
     fetch_regs_tail(s_whole, cur);
@@ -1082,90 +1134,287 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
     }
   }
 
-  // Accumulator register i of lane l: X row 8 (i / 4) + 4 (l / 32) + i % 4, W row
-  // l % 32.  Each wave passes its sums through LDS of its own, 32 rows of X x
-  // 64 (32) rows of W at a time, so that a lane stores eight neighbouring ones.
   if constexpr (XT == GPTQ_F16 && !SPLIT) {
     if (!__syncthreads_and(exact)) return false;
   } else {
     lds_barrier();
   }
-  constexpr int RP = RB % 2 == 0 ? 2 : 1, kPitch = out_pitch(RB);
-  float* my = reinterpret_cast<float*>(smem) + wave * 32 * kPitch;
-#pragma unroll
-  for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-    for (int r2 = 0; r2 < RB; r2 += RP) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int b = 0; b < RP; ++b)
-          my[(8 * (i >> 2) + 4 * h + (i & 3)) * kPitch + 32 * b + l32] = acc[r2 + b][cb][i];
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-      __builtin_amdgcn_wave_barrier();
-      constexpr int kLanes = 4 * RP;         // lanes that share a row of X
-      const int xr = lane / kLanes, c = lane % kLanes * 8;
-      const int r = r0 + (wr * RB + r2) * 32 + c;
-#pragma unroll 1
-      for (int k = 0; k < 32; k += 64 / kLanes) {
-        const int x = tile.begin + (wc * CB + cb) * 32 + k + xr;
-        const floatx4 lo = *reinterpret_cast<const floatx4*>(my + (k + xr) * kPitch + c);
-        const floatx4 hi = *reinterpret_cast<const floatx4*>(my + (k + xr) * kPitch + c + 4);
-        if (x < tile.end && r < p.m) {
-          if (tg.splits > 1)
-            store8<GPTQ_F32>(tg.part, ((int64_t)split * p.rows + x) * p.m + r, p.m - r, lo, hi);
-          else if (p.y_dtype == GPTQ_F32)
-            store8<GPTQ_F32>(p.Y, (int64_t)x * p.ldy + r, p.m - r, lo, hi);
-          else if (p.y_dtype == GPTQ_F16)
-            store8<GPTQ_F16>(p.Y, (int64_t)x * p.ldy + r, p.m - r, lo, hi);
-          else
-            store8<GPTQ_BF16>(p.Y, (int64_t)x * p.ldy + r, p.m - r, lo, hi);
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-      __builtin_amdgcn_wave_barrier();
-    }
+  store_tile<WR, WC, RB, CB>(p, tg, tile, r0, split, acc, smem);
   return true;
+}
+
+// One large tile of 16-bit X with 16-byte aligned rows of both operands.  As
+// tile_product, but the codes of W are staged in LDS too, a super-stage of 256
+// columns (128 bytes of a row: whole cache lines) at a time, and its scale bytes
+// with them: loaded into registers by the lanes that use them, 32 bytes of a row
+// at a time, codes and scales took 59 and 56 of 433 us at 4096 x 8192 x 8192.  A
+// stage of X is one panel (64 columns); each of the four stages of a super-stage
+// fetches a quarter of the next one's W.
+template <int XT, int WR, int WC, int RB, int CB>
+constexpr int big_tile_lds() {
+  const int x = 32 * WC * CB, w = 32 * WR * RB;
+  return std::max(2 * (x + w) * kPanelRow + 2 * w * 8, WR * WC * 32 * out_pitch(RB) * 4);
+}
+
+template <int XT, int WR, int WC, int RB, int CB, bool SPLIT>
+__device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg, const TokenTile& tile, int r0,
+                                        int split, unsigned char* smem) {
+  constexpr int kThreads = 64 * WR * WC, kWaves = WR * WC;
+  constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB;
+  constexpr int kX = BN * kPanelRow, kW = BM * kPanelRow;     // bytes of a buffer
+  constexpr int kXLoads = BN / (8 * kWaves), kWLoads = BM / (32 * kWaves);   // a wave's per stage
+  static_assert(BN % (8 * kWaves) == 0 && BM % (32 * kWaves) == 0 && kThreads % BM == 0, "every wave loads whole rows");
+  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / WC, wc = wave % WC;
+  unsigned char* xs = smem;                  // [2][BN][128]
+  unsigned char* wsm = smem + 2 * kX;        // [2][BM][128]
+  uint32_t* ssm = reinterpret_cast<uint32_t*>(smem + 2 * kX + 2 * kW);       // [2][BM][half]
+  const int64_t x_pitch = p.ldx * 2, w_pitch = p.ldp * 4;
+  const char* xbase = static_cast<const char*>(p.X) + (int64_t)tile.begin * x_pitch;
+  const char* wbase = reinterpret_cast<const char*>(p.W + (int64_t)tile.expert * p.w_stride + (int64_t)r0 * p.ldp);
+  const uint8_t* sbase = p.S + (int64_t)tile.expert * p.s_stride + (int64_t)r0 * p.lds;
+  auto x_row = [&](int r) { return (uint32_t)min(r, tile.end - 1 - tile.begin) * (uint32_t)x_pitch; };
+  auto w_row = [&](int r) { return (uint32_t)min(r, p.m - 1 - r0) * (uint32_t)w_pitch; };
+
+  // Supers [lo, hi) of this split; whole ones below `whole`.
+  const int per_split = tg.cols_per_split / 256;
+  const int lo = split * per_split, hi = min((p.n + 255) / 256, lo + per_split), whole = min(hi, p.n / 256);
+  const uint32_t chunk_at = ((lane & 7) ^ swizzle(wave * 8 + (lane >> 3))) << 4;   // source chunk of the lane's slot
+  uint32_t x_at[kXLoads], w_at[4 * kWLoads];
+#pragma unroll
+  for (int i = 0; i < kXLoads; ++i) x_at[i] = x_row((wave + i * kWaves) * 8 + (lane >> 3)) + chunk_at;
+#pragma unroll
+  for (int i = 0; i < 4 * kWLoads; ++i) w_at[i] = w_row((wave + i * kWaves) * 8 + (lane >> 3)) + chunk_at;
+  auto direct = [&](unsigned char* dst, const char* src, uint32_t offset) {
+    // As in tile_product: M0 is the LDS destination, waited for explicitly.
+    const uint32_t d = (uint32_t)reinterpret_cast<uintptr_t>((lds_void*)dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(d), "v"(offset), "s"(src)
+                 : "memory", "m0");
+  };
+  auto fetch_x = [&](int panel, int buf) {
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i)
+      direct(xs + buf * kX + (wave + i * kWaves) * 8 * kPanelRow, xbase + (int64_t)panel * kPanelRow, x_at[i]);
+  };
+  auto fetch_w = [&](int super, int quarter) {
+#pragma unroll
+    for (int i = quarter * kWLoads; i < (quarter + 1) * kWLoads; ++i)
+      direct(wsm + (super & 1) * kW + (wave + i * kWaves) * 8 * kPanelRow,
+             wbase + (int64_t)min(super, whole - 1) * kPanelRow, w_at[i]);
+  };
+  // Scale bytes of a super-stage: thread t those of row t % BM (the threads
+  // beyond BM write the same values).
+  const int srow = tid % BM;
+  const uint8_t* sptr = sbase + (int64_t)min(srow, p.m - 1 - r0) * p.lds;
+  u32x2 sreg;
+  auto fetch_s = [&](int super) { sreg = *reinterpret_cast<const u32x2_a1*>(sptr + 8 * min(super, whole - 1)); };
+  auto put_s = [&](int super) {
+    *reinterpret_cast<u32x2*>(ssm + ((super & 1) * BM + srow) * 2) = order_scales8(sreg[0], sreg[1]);
+  };
+
+  floatx16 acc[RB][CB];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = floatx16{};
+  uint32_t frag_x[4], frag_w[4];             // this lane's addresses of step j, of stage u's codes
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    frag_x[j] = (uint32_t)((wc * CB * 32 + l32) * kPanelRow + (((4 * h + j) ^ swizzle(l32)) << 4));
+    frag_w[j] = (uint32_t)((wr * RB * 32 + l32) * kPanelRow + (((2 * j + h) ^ swizzle(l32)) << 4));
+  }
+  u32x4 x[2][CB], w[2][RB];
+  uint32_t sc[RB], exact = 0u;
+  auto load_x = [&](int buf, int step, u32x4 (&o)[CB]) {
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+      o[cb] = *reinterpret_cast<const u32x4*>(xs + buf * kX + frag_x[step] + cb * 32 * kPanelRow);
+  };
+  auto load_w = [&](int super, int u, u32x4 (&o)[RB]) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+      o[rb] = *reinterpret_cast<const u32x4*>(wsm + (super & 1) * kW + frag_w[u] + rb * 32 * kPanelRow);
+  };
+  auto load_s = [&](int super) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      sc[rb] = ssm[((super & 1) * BM + (wr * RB + rb) * 32 + l32) * 2 + h];
+      if constexpr (XT == GPTQ_F16 && !SPLIT) exact |= f16_inexact4(sc[rb]);
+    }
+  };
+  // Products of step j of stage u, row blocks [from, to).
+  auto products = [&](int u, int j, const u32x4 (&xf)[CB], const u32x4 (&wf)[RB], int from, int to) {
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+        u32x4 top, rest;
+        split8(xf[cb], top, rest);
+#pragma unroll
+        for (int rb = from; rb < to; ++rb) {
+          const u32x4 wv = widen8<GPTQ_BF16>(wf[rb][j], mx_scale_operand((sc[rb] >> (8 * u)) & 255u));
+          acc[rb][cb] = mfma32<GPTQ_BF16>(top, wv, acc[rb][cb]);
+          acc[rb][cb] = mfma32<GPTQ_BF16>(rest, wv, acc[rb][cb]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int rb = from; rb < to; ++rb) {
+        const u32x4 wv = widen8<XT>(wf[rb][j], mx_scale_operand((sc[rb] >> (8 * u)) & 255u));
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = mfma32<XT>(xf[cb], wv, acc[rb][cb]);
+      }
+#pragma unroll
+      for (int i = 0; i < (to - from) * CB; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+        __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);   // one VALU
+      }
+    }
+  };
+
+  if (lo < whole) {
+    fetch_x(4 * lo, 0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) fetch_w(lo, u);
+    fetch_s(lo);
+    put_s(lo);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    lds_barrier();
+    load_x(0, 0, x[0]);
+    load_w(lo, 0, w[0]);
+    load_s(lo);
+    for (int super = lo; super < whole; ++super) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        // Past the last panel that panel is fetched again, for no one.
+        fetch_x(min(4 * super + u + 1, 4 * whole - 1), (u + 1) & 1);
+        fetch_w(super + 1, u);
+        if (u == 0) fetch_s(super + 1);
+        __builtin_amdgcn_sched_barrier(0);   // the loads are issued before the products
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          load_x(u & 1, j + 1, x[(j + 1) & 1]);
+          products(u, j, x[j & 1], w[u & 1], 0, RB);
+        }
+        products(u, 3, x[1], w[u & 1], 0, RB / 2);
+        if (u == 3) put_s(super + 1);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        lds_barrier();
+        load_x((u + 1) & 1, 0, x[0]);
+        load_w(super + (u == 3), (u + 1) & 3, w[(u + 1) & 1]);
+        products(u, 3, x[1], w[u & 1], RB / 2, RB);
+        if (u == 3) load_s(super + 1);
+      }
+    }
+  }
+  // The columns behind the last whole super-stage, a panel at a time.
+  if (lo <= whole && whole < hi) {
+#pragma unroll 1
+    for (int panel = 4 * whole; panel < (p.n + 63) / 64; ++panel) {
+      lds_barrier();
+#pragma unroll
+      for (int i = 0; i < BN * 8 / kThreads; ++i) {
+        const int r = (tid >> 3) + i * (kThreads / 8);
+        *reinterpret_cast<u32x4*>(xs + r * kPanelRow + (((tid & 7) ^ swizzle(r)) << 4)) =
+            load_x8_tail(reinterpret_cast<const uint16_t*>(xbase + x_row(r)), panel * 64 + (tid & 7) * 8, p.n);
+      }
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        const int r = (wr * RB + rb) * 32 + l32;
+        w[0][rb] = load_w4_tail(reinterpret_cast<const uint32_t*>(wbase + w_row(r)), 8 * panel + 4 * h, p.n);
+        sc[rb] = (load_scales4(sbase + (int64_t)min(r, p.m - 1 - r0) * p.lds, 2 * panel, p.n) >> (8 * h)) & 255u;
+        if constexpr (XT == GPTQ_F16 && !SPLIT) exact |= f16_inexact4(sc[rb] * 0x01010101u);
+      }
+      lds_barrier();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        load_x(0, j, x[0]);
+        products(0, j, x[0], w[0], 0, RB);
+      }
+    }
+  }
+  if constexpr (XT == GPTQ_F16 && !SPLIT) {
+    if (!__syncthreads_and(exact == 0u)) return false;
+  } else {
+    lds_barrier();
+  }
+  store_tile<WR, WC, RB, CB>(p, tg, tile, r0, split, acc, smem);
+  return true;
+}
+
+// Workgroup -> (split, tile of X rows, tile of W rows); false: none.
+__device__ inline bool tile_of_workgroup(const MxOperands& p, const TileGrid& tg, int BM, int BN, int& split,
+                                         TokenTile& tile, int& r0) {
+  const int64_t tiles = (int64_t)tg.row_tiles * tg.tok_tiles;
+  const int64_t item = xcd_contiguous(blockIdx.x, gridDim.x);
+  if (item >= tiles * tg.splits) return false;
+  split = (int)(item / tiles);
+  const int t = (int)(item % tiles);
+  const int band = t / (kTokBand * tg.row_tiles);
+  const int in_band = min(kTokBand, tg.tok_tiles - band * kTokBand);
+  const int rest = t - band * kTokBand * tg.row_tiles;
+  tile = find_tile(p, band * kTokBand + rest % in_band, BN);
+  r0 = rest / in_band * BM;
+  return tile.valid;
 }
 
 // Two waves per SIMD where the accumulators leave room for them.
 template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT>
 __global__ __launch_bounds__(64 * WR * WC, RB * CB <= 8 ? 2 : 1) void mx_tile_kernel(MxOperands p, TileGrid tg) {
-  constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  // Workgroup -> (split, tile of X rows, tile of W rows).
-  const int64_t tiles = (int64_t)tg.row_tiles * tg.tok_tiles;
-  const int64_t item = xcd_contiguous(blockIdx.x, gridDim.x);
-  if (item >= tiles * tg.splits) return;
-  const int split = (int)(item / tiles);
-  const int t = (int)(item % tiles);
-  const int band = t / (kTokBand * tg.row_tiles);
-  const int in_band = min(kTokBand, tg.tok_tiles - band * kTokBand);
-  const int rest = t - band * kTokBand * tg.row_tiles;
-  const TokenTile tile = find_tile(p, band * kTokBand + rest % in_band, BN);
-  if (!tile.valid) return;
-  const int r0 = rest / in_band * BM;
+  int split, r0;
+  TokenTile tile;
+  if (!tile_of_workgroup(p, tg, 32 * WR * RB, 32 * WC * CB, split, tile, r0)) return;
   const bool done = tile_product<XT, WR, WC, RB, CB, PB, DIRECT, false>(p, tg, tile, r0, split, smem);
   if constexpr (XT == GPTQ_F16) {
     if (!done) tile_product<XT, WR, WC, RB, CB, PB, DIRECT, true>(p, tg, tile, r0, split, smem);
   }
 }
 
-// Adds the splits' sums in order.  Rows that belong to no expert stay.
+template <int XT, int WR, int WC, int RB, int CB>
+__global__ __launch_bounds__(64 * WR * WC, 2) void mx_big_tile_kernel(MxOperands p, TileGrid tg) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  int split, r0;
+  TokenTile tile;
+  if (!tile_of_workgroup(p, tg, 32 * WR * RB, 32 * WC * CB, split, tile, r0)) return;
+  const bool done = big_tile_product<XT, WR, WC, RB, CB, false>(p, tg, tile, r0, split, smem);
+  if constexpr (XT == GPTQ_F16) {
+    if (!done) big_tile_product<XT, WR, WC, RB, CB, true>(p, tg, tile, r0, split, smem);
+  }
+}
+
+// Adds the splits' sums in order, four columns a thread and four splits' loads
+// in flight (one at a time they cost a memory latency a split).  Rows that
+// belong to no expert stay.
 __global__ __launch_bounds__(256) void mx_join_kernel(MxOperands p, TileGrid tg) {
-  int lo = 0, hi = p.rows;
+  const int x = (int)blockIdx.y, r = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4;
+  if (r >= p.m) return;
   if (p.offsets != nullptr) {
-    lo = min(max(p.offsets[0], 0), p.rows);
-    hi = min(max(p.offsets[p.experts], 0), p.rows);
+    const int lo = min(max(p.offsets[0], 0), p.rows), hi = min(max(p.offsets[p.experts], 0), p.rows);
+    if (x < lo || x >= hi) return;
   }
   const int64_t total = (int64_t)p.rows * p.m;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t x = i / p.m, r = i - x * p.m;
-    if (x < lo || x >= hi) continue;
-    float v = tg.part[i];
-    for (int s = 1; s < tg.splits; ++s) v += tg.part[s * total + i];
-    store_y(p, x * p.ldy + r, v);
+  const float* part = tg.part + (int64_t)x * p.m;
+  const int left = p.m - r;
+  auto load = [&](int split) {
+    const float* at = part + min(split, tg.splits - 1) * total;
+    if (left >= 4) return *reinterpret_cast<const floatx4_a4*>(at + r);
+    return floatx4{at[r], at[min(r + 1, p.m - 1)], at[min(r + 2, p.m - 1)], 0.f};
+  };
+  floatx4 v = load(0);
+  for (int s = 1; s < tg.splits; s += 4) {
+    floatx4 t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = load(s + i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (s + i < tg.splits) v += t[i];
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) store_y(p, (int64_t)x * p.ldy + r + i, v[i]);
 }
 
 // Tiles that the rows can form at most: every expert with rows may end in a
@@ -1188,29 +1437,30 @@ constexpr int kSplitCols = 256;              // a split is a multiple of this
 
 // The rules below follow sweeps of all kinds over sizes (times in us, the kind
 // taken first): products small enough for their operands to come through L2
-// run on the row kernels, whose waves split the columns (64 x 4096 x 4096: 11.5
-// against 13.1 on tiles; 64 x 12288 x 12288: 75 against 36), long matrices with
+// run on the row kernels, whose waves split the columns (64 x 4096 x 4096: 11.7
+// against 13.8 on tiles; 64 x 12288 x 12288: 75 against 36), long matrices with
 // few rows of X on the stream kernel (16 x 49152 x 12288: 78 against 93), the
-// rest on tiles, as wide as still gives half the 256 CUs one, their columns
-// split until there are about 384 (16 x 12288 x 12288: 28 with 4 splits, 45
-// with 1).  256 x 256 tiles are the fastest where they fill whole rounds of the
-// CUs (4096 x 8192 x 8192: 437 against 464), 256 x 128 (two to a CU) otherwise
-// (2048 x 11008 x 4096: 179 against 209).
+// rest on tiles, as wide as still gives 256 of them with splits of 1024 columns,
+// split until there are about 384 (16 x 12288 x 12288: 28 with 4 splits, 45 with
+// 1; 64 x 11008 x 4096 on 128 x 64 with 4 splits 20, on 128 x 32 with 2 22).
+// 256 x 256 tiles are the fastest where they fill the CUs once or in whole
+// rounds (1024 x 11008 x 4096: 83 against 101 on 256 x 128, 4096 x 8192 x 8192:
+// 373 against 414), 256 x 128 (two to a CU) otherwise (2048 x 11008 x 4096: 158
+// against 168).
 constexpr int64_t kWantTiles = 384, kMinSplitCols = 512;
 
 Plan tile_plan(int64_t m, int64_t n, int64_t rows, bool mx) {
   auto tiles = [&](int bm, int bn) { return ceil_div(m, bm) * ceil_div(rows, bn); };
   if (rows >= 192) {
-    const int64_t t = tiles(256, 256);
-    const int64_t rounds = ceil_div(t, 256) * 256;
-    if (t >= 192 && (mx || t * 10 >= rounds * 9)) return Plan{kTile256x256, 1};
+    const int64_t t = tiles(256, 256), rounds = ceil_div(t, 256) * 256;
+    if (mx ? t >= 192 : (t >= 160 && t <= 256) || (t > 256 && t * 10 >= rounds * 9)) return Plan{kTile256x256, 1};
     if (tiles(256, 128) >= 192 && (!mx || rows >= 1024)) return Plan{kTile256x128, 1};
   }
   const Kind kinds[3] = {kTile128x128, kTile128x64, kTile128x32};
   const int widths[3] = {128, 64, 32};
   for (int i = 0; i < 3; ++i) {
     const int64_t t = tiles(128, widths[i]);
-    if (i < 2 && (t < 128 || rows <= widths[i] / 2)) continue;
+    if (i < 2 && (t * std::max<int64_t>(1, n / 1024) < 256 || rows <= widths[i] / 2)) continue;
     const int64_t most = std::max<int64_t>(1, n / kMinSplitCols);
     const int64_t splits = t >= 256 ? 1 : std::max<int64_t>(1, (kWantTiles + t / 2) / t);
     return Plan{kinds[i], (int)std::min(splits, most)};
@@ -1249,34 +1499,49 @@ size_t plan_ws(const Plan& pl, int64_t m, int64_t rows) {
   return pl.splits > 1 ? align256((size_t)pl.splits * (size_t)rows * (size_t)m * sizeof(float)) : 0;
 }
 
-template <int XT, int WR, int WC, int RB, int CB, int PB>
-gptq_status launch_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStream_t st) {
-  constexpr bool MX = XT == kMx;
-  constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB;
-  constexpr int kLds = tile_lds<XT, WR, WC, RB, CB, PB>();
+// Runs tile kernel k (tiles of BM x BN) and, with splits, the sum over them.
+gptq_status run_tiles(void (*k)(MxOperands, TileGrid), int BM, int BN, int threads, int lds, const MxOperands& p,
+                      const Plan& pl, void* ws, hipStream_t st) {
   const int64_t cols = round_up(std::max<int64_t>(ceil_div(p.n, pl.splits), 1), kSplitCols);
-  TileGrid tg{(int)ceil_div(p.m, BM), (int)max_tiles(p.rows, p.experts, p.offsets != nullptr, BN), pl.splits,
+  // Whole splits can leave fewer of them than were asked for.
+  const int splits = (int)std::max<int64_t>(ceil_div(p.n, cols), 1);
+  TileGrid tg{(int)ceil_div(p.m, BM), (int)max_tiles(p.rows, p.experts, p.offsets != nullptr, BN), splits,
               (int)cols, static_cast<float*>(ws)};
   const int64_t items = (int64_t)tg.row_tiles * tg.tok_tiles * tg.splits;
   if (items > ((int64_t)1 << 30)) return GPTQ_ERR_UNSUPPORTED;
-  const unsigned grid = (unsigned)round_up(items, kXcds);
-  const int xb = MX ? 4 : 2;
-  const bool direct = ((reinterpret_cast<uintptr_t>(p.X) | (uint64_t)(p.ldx * xb)) & 15) == 0 &&
-                      (!MX || ((reinterpret_cast<uintptr_t>(p.W) | (uint64_t)(p.ldp * 4) | (uint64_t)(p.w_stride * 4)) &
-                               15) == 0);
-  // By registers, a stage of the large tiles is one panel: they have to hold it.
-  constexpr int PR = RB * CB > 4 ? 1 : PB;
-  auto* k = direct ? mx_tile_kernel<XT, WR, WC, RB, CB, PB, true> : mx_tile_kernel<XT, WR, WC, RB, CB, PR, false>;
-  if (kLds > 65536)
-    GPTQ_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
-  k<<<grid, 64 * WR * WC, kLds, st>>>(p, tg);
+  if (lds > 65536)
+    GPTQ_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds));
+  k<<<(unsigned)round_up(items, kXcds), threads, lds, st>>>(p, tg);
   GPTQ_TRY_LAUNCH();
   if (tg.splits > 1) {
-    const int64_t wgs = std::min<int64_t>(ceil_div((int64_t)p.rows * p.m, 256), 2048);
-    mx_join_kernel<<<(unsigned)wgs, 256, 0, st>>>(p, tg);
+    mx_join_kernel<<<dim3((unsigned)ceil_div(p.m, 1024), (unsigned)p.rows), 256, 0, st>>>(p, tg);
     GPTQ_TRY_LAUNCH();
   }
   return GPTQ_OK;
+}
+
+// Whether every row of both operands starts at a 16-byte aligned address.
+template <int XT>
+bool aligned_x(const MxOperands& p) {
+  return ((reinterpret_cast<uintptr_t>(p.X) | (uint64_t)(p.ldx * (XT == kMx ? 4 : 2))) & 15) == 0;
+}
+bool aligned_w(const MxOperands& p) {
+  return ((reinterpret_cast<uintptr_t>(p.W) | (uint64_t)(p.ldp * 4) | (uint64_t)(p.w_stride * 4)) & 15) == 0;
+}
+
+template <int XT, int WR, int WC, int RB, int CB, int PB>
+gptq_status launch_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStream_t st) {
+  // By registers, a stage of the large tiles is one panel: they have to hold it.
+  constexpr int PR = RB * CB > 4 ? 1 : PB;
+  const bool direct = aligned_x<XT>(p) && (XT != kMx || aligned_w(p));
+  auto* k = direct ? mx_tile_kernel<XT, WR, WC, RB, CB, PB, true> : mx_tile_kernel<XT, WR, WC, RB, CB, PR, false>;
+  return run_tiles(k, 32 * WR * RB, 32 * WC * CB, 64 * WR * WC, tile_lds<XT, WR, WC, RB, CB, PB>(), p, pl, ws, st);
+}
+
+template <int XT, int WR, int WC, int RB, int CB>
+gptq_status launch_big_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStream_t st) {
+  return run_tiles(mx_big_tile_kernel<XT, WR, WC, RB, CB>, 32 * WR * RB, 32 * WC * CB, 64 * WR * WC,
+                   big_tile_lds<XT, WR, WC, RB, CB>(), p, pl, ws, st);
 }
 
 template <int XT, int RT, int NT, int D>
@@ -1308,6 +1573,11 @@ gptq_status launch(const MxOperands& p, void* ws, size_t ws_bytes, hipStream_t s
   const size_t need = plan_ws(pl, p.m, p.rows);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return GPTQ_ERR_WORKSPACE;
   constexpr int P2 = XT == kMx ? 1 : 2, P4 = XT == kMx ? 1 : 4;        // panels per stage
+  if constexpr (XT != kMx) {
+    if (aligned_x<XT>(p) && aligned_w(p)) {
+      if (pl.kind == kTile256x256) return launch_big_tiles<XT, 4, 2, 2, 4>(p, pl, ws, st);
+    }
+  }
   switch (pl.kind) {
     case kTile256x256: return launch_tiles<XT, 4, 2, 2, 4, P2>(p, pl, ws, st);
     case kTile256x128: return launch_tiles<XT, 4, 1, 2, 4, P2>(p, pl, ws, st);

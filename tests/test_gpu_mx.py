@@ -597,6 +597,8 @@ KINDS = [
     (16384, 1024, 180), (16400, 1031, 135),       # tiles of 128 x 128
     (8192, 640, 1030), (8200, 520, 1025),         # tiles of 256 x 128
     (12288, 384, 1300), (8192, 512, 2048),        # tiles of 256 x 256
+    (4099, 11007, 77), (4000, 9000, 80),          # splits that do not divide the columns, a partial last stage
+    (1100, 12000, 200), (300, 20001, 700),        # few rows of W, many splits
 ]
 
 
