@@ -1599,6 +1599,8 @@ gptq_status launch(const MxOperands& p, void* ws, size_t ws_bytes, hipStream_t s
   return launch_rows<XT, 2, 1, 2>(p, 8, st);
 }
 
+constexpr int64_t kMaxLd = (int64_t)1 << 40; // products of strides and indexes stay below 2^62
+
 // Checks shared by the products; `rows` rows of X against `experts` matrices.
 gptq_status check(int64_t m, int64_t n, int64_t rows, int64_t experts, int64_t ld_packed, int64_t ld_scales,
                   int y_dtype, int64_t ldy) {
@@ -1606,6 +1608,7 @@ gptq_status check(int64_t m, int64_t n, int64_t rows, int64_t experts, int64_t l
   if (n > kMxMaxCols || m > GPTQ_MX_MAX_ROWS || rows > GPTQ_MX_MAX_ROWS || experts > GPTQ_MX_MAX_EXPERTS)
     return GPTQ_ERR_UNSUPPORTED;
   if (ld_packed < ceil_div(n, 8) || ld_scales < ceil_div(n, kMxBlock) || ldy < m) return GPTQ_ERR_INVALID_ARG;
+  if (ld_packed > kMaxLd || ld_scales > kMaxLd || ldy > kMaxLd) return GPTQ_ERR_UNSUPPORTED;
   return GPTQ_OK;
 }
 
@@ -1633,6 +1636,7 @@ extern "C" gptq_status gptq_mx_gemm_grouped(const uint32_t* packed, int64_t expe
   const gptq_status rc = check(m, n, rows, experts, ld_packed, ld_scales, y_dtype, ldy);
   if (rc != GPTQ_OK) return rc;
   if (ldx < n || stride_packed < 0 || stride_scales < 0) return GPTQ_ERR_INVALID_ARG;
+  if (ldx > kMaxLd || stride_packed > (kMaxLd << 5) || stride_scales > (kMaxLd << 5)) return GPTQ_ERR_UNSUPPORTED;
   if (experts > 1 && (stride_packed < m * ld_packed || stride_scales < m * ld_scales)) return GPTQ_ERR_INVALID_ARG;
   if (m == 0 || rows == 0 || experts == 0) return GPTQ_OK;
   if (offsets == nullptr || Y == nullptr) return GPTQ_ERR_INVALID_ARG;
@@ -1651,6 +1655,7 @@ extern "C" gptq_status gptq_mx_gemm(const uint32_t* packed, int64_t m, int64_t n
   const gptq_status rc = check(m, n, batch, 1, ld_packed, ld_scales, y_dtype, ldy);
   if (rc != GPTQ_OK) return rc;
   if (ldx < n) return GPTQ_ERR_INVALID_ARG;
+  if (ldx > kMaxLd) return GPTQ_ERR_UNSUPPORTED;
   if (m == 0 || batch == 0) return GPTQ_OK;
   if (Y == nullptr || (n > 0 && (packed == nullptr || scales == nullptr || X == nullptr)))
     return GPTQ_ERR_INVALID_ARG;
@@ -1668,6 +1673,7 @@ extern "C" gptq_status gptq_mx_scaled_gemm(const uint32_t* packed, int64_t m, in
   const gptq_status rc = check(m, n, batch, 1, ld_packed, ld_scales, y_dtype, ldy);
   if (rc != GPTQ_OK) return rc;
   if (ld_xpacked < ceil_div(n, 8) || ld_xscales < ceil_div(n, kMxBlock)) return GPTQ_ERR_INVALID_ARG;
+  if (ld_xpacked > kMaxLd || ld_xscales > kMaxLd) return GPTQ_ERR_UNSUPPORTED;
   if (m == 0 || batch == 0) return GPTQ_OK;
   if (Y == nullptr || (n > 0 && (packed == nullptr || scales == nullptr || x_packed == nullptr || x_scales == nullptr)))
     return GPTQ_ERR_INVALID_ARG;

@@ -675,3 +675,111 @@ def test_workspace_given_too_small_and_shared(g):
     assert torch.equal(g.gptq_mx_gemm(packed, scales, X, ws=ws), want)
     with pytest.raises(g.GptqError, match="WORKSPACE"):
         g.gptq_mx_gemm(packed, scales, X, ws=ws[:1024])
+
+
+@pytest.mark.parametrize("m,n,batch", [(4096, 4608, 140), (8192, 512, 2048), (24576, 640, 12)])
+def test_graph_of_every_launch_shape(g, m, n, batch):
+    """Split columns (their workspace comes from the graph's pool), tiles with
+    more LDS than a launch has by default, and streamed X, captured and
+    replayed with new inputs and eager calls between."""
+    import torch
+    rng = _rng(m, batch, 73)
+    codes, scale = _weights(rng, m, n)
+    packed, scales = _packed(codes, scale)
+    X, _ = _to(rng.standard_normal((batch, n)), "f16")
+
+    def step():
+        q = g.gptq_mx_quantize(X)
+        return (g.gptq_mx_gemm(packed, scales, X),
+                g.gptq_mx_scaled_gemm(packed, scales, q["packed"], q["scales"], n, y_dtype=torch.bfloat16))
+
+    step()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = step()
+    for k in range(3):
+        X.copy_(torch.randn(X.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(k)))
+        gr.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        for x, y in zip(got, step()):
+            assert torch.equal(x, y)
+
+
+def test_row_pitches_past_the_tiles_range(g):
+    # Rows of X six megabytes apart: the tile kernels' 32-bit offsets end at
+    # four, the row kernels take any pitch.
+    import torch
+    rng = _rng(79)
+    m, n, batch = 49152, 640, 80
+    codes, scale = _weights(rng, m, n)
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((batch, n)), "f16")
+    far = torch.empty((batch, 3000000), dtype=torch.float16, device="cuda")[:, :n]
+    far.copy_(X)
+    rows = np.r_[0, m - 1, rng.permutation(m)[:100]]
+    want, mags = oracle.mx_matmul(codes[rows], scale[rows], X64)
+    _check(g.gptq_mx_gemm(packed, scales, far)[:, torch.from_numpy(rows).cuda()], want, mags, n, "f32", "far rows")
+
+
+def test_offsets_past_32_bits(g):
+    """Weights whose elements and bytes pass 2^32: the last rows against the
+    oracle, and as the last of a stack of experts."""
+    import torch
+    m, n = 1048576, 9216
+    gen = torch.Generator(device="cuda").manual_seed(83)
+    W = torch.empty((m, n), dtype=torch.bfloat16, device="cuda").normal_(0, 0.02, generator=gen)
+    q = g.gptq_mx_quantize(W)
+    last = W[-40:].double().cpu().numpy()
+    del W
+    codes, scale = oracle.mx_quantize(last)
+    gc, gs = _unpack({k: q[k][-40:] for k in ("packed", "scales")}, n)
+    assert np.array_equal(gc, codes) and np.array_equal(gs, scale)
+    rng = _rng(83)
+    for batch in (2, 20):
+        X, X64 = _to(rng.standard_normal((batch, n)), "bf16")
+        want, mags = oracle.mx_matmul(codes, scale, X64)
+        _check(g.gptq_mx_gemm(q["packed"], q["scales"], X)[:, -40:], want, mags, n, "f32", f"last rows, batch {batch}")
+        E = 1024
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[-1] = batch
+        Y = g.gptq_mx_gemm_grouped(q["packed"].view(E, m // E, -1), q["scales"].view(E, m // E, -1), X, off)
+        _check(Y[:, -40:], want, mags, n, "f32", f"last expert, batch {batch}")
+
+
+def test_many_rows_of_x(g):
+    import torch
+    rng = _rng(89)
+    m, n, rows = 5, 40, 100003
+    codes, scale = _weights(rng, m, n)
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((rows, n)), "bf16")
+    want, mags = oracle.mx_matmul(codes, scale, X64)
+    _check(g.gptq_mx_gemm(packed, scales, X), want, mags, n, "f32", "100003 rows of X")
+    off = torch.tensor([0, 3, rows], dtype=torch.int32, device="cuda")
+    Y = g.gptq_mx_gemm_grouped(packed.expand(2, -1, -1).contiguous(), scales.expand(2, -1, -1).contiguous(), X, off)
+    _check(Y, want, mags, n, "f32", "100003 rows of X, grouped")
+
+
+def test_two_streams_at_once(g):
+    """Calls that need a workspace on two streams at the same time."""
+    import torch
+    rng = _rng(97)
+    m, n, batch = 4096, 4608, 140
+    jobs = []
+    for k in range(2):
+        codes, scale = _weights(rng, m, n)
+        packed, scales = _packed(codes, scale)
+        X, _ = _to(rng.standard_normal((batch, n)), "bf16")
+        jobs.append((packed, scales, X, g.gptq_mx_gemm(packed, scales, X)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    out = [[], []]
+    for _ in range(5):
+        for k, (packed, scales, X, _) in enumerate(jobs):
+            out[k].append(g.gptq_mx_gemm(packed, scales, X, stream=streams[k]))
+    torch.cuda.synchronize()
+    for k, job in enumerate(jobs):
+        for Y in out[k]:
+            assert torch.equal(Y, job[3])

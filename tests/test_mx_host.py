@@ -91,6 +91,8 @@ GEMM_BAD = [
     (INVALID, dict(ldp=8)), (INVALID, dict(lds=2)), (INVALID, dict(ldy=39)),
     (UNSUPPORTED, dict(n=(1 << 20) + 1, ldp=1 << 20, lds=1 << 20)),
     (UNSUPPORTED, dict(m=(1 << 20) + 1, ldy=1 << 21)), (UNSUPPORTED, dict(batch=(1 << 20) + 1)),
+    (UNSUPPORTED, dict(ldp=1 << 62)), (UNSUPPORTED, dict(lds=1 << 62)), (UNSUPPORTED, dict(ldy=1 << 62)),
+    (UNSUPPORTED, dict(ldx=1 << 62)),
     (OK, dict(m=0)), (OK, dict(batch=0)),
 ]
 
@@ -120,7 +122,8 @@ GROUPED = dict(packed=_p(), experts=6, m=40, n=70, ldp=9, sp=360, scales=_p(), l
 @pytest.mark.parametrize("want,kw", GEMM_BAD + [
     (INVALID, dict(dt=0)), (INVALID, dict(X=None)), (INVALID, dict(ldx=69)), (INVALID, dict(offsets=None)),
     (INVALID, dict(experts=-1)), (INVALID, dict(sp=359)), (INVALID, dict(ss=119)), (INVALID, dict(sp=-1)),
-    (UNSUPPORTED, dict(experts=65537)), (OK, dict(experts=0)),
+    (UNSUPPORTED, dict(experts=65537)), (UNSUPPORTED, dict(sp=1 << 62)), (UNSUPPORTED, dict(ss=1 << 62)),
+    (OK, dict(experts=0)),
 ])
 def test_grouped_gemm_argument_errors(lib, want, kw):
     assert _call(lib.gptq_mx_gemm_grouped, GROUPED, **kw) == want
@@ -131,6 +134,19 @@ def test_workspace_query(lib):
         assert lib.gptq_mx_gemm_ws_bytes(*bad) == 0
     for zero in ((0, 64, 1, 1), (64, 64, 0, 1), (64, 64, 1, 0)):
         assert lib.gptq_mx_gemm_ws_bytes(*zero) == 0
+
+
+def test_missing_workspace_is_refused_before_any_launch(lib):
+    # Sizes whose columns are split need the queried workspace.
+    m, n, batch = 4096, 4608, 140
+    need = lib.gptq_mx_gemm_ws_bytes(m, n, batch, 1)
+    assert need > 0
+    base = dict(GEMM, m=m, n=n, ldp=n // 8, lds=n // 32, batch=batch, ldx=n, ldy=m)
+    for kw in (dict(), dict(ws=_p(), ws_bytes=need // 2), dict(ws_bytes=need)):
+        assert _call(lib.gptq_mx_gemm, base, **kw) == _lib.GPTQ_ERR_WORKSPACE
+    base = dict(SCALED, m=12288, n=12288, ldp=1536, lds=384, batch=64, ldx=1536, ldxs=384, ldy=12288)
+    assert lib.gptq_mx_gemm_ws_bytes(12288, 12288, 64, 1) > 0
+    assert _call(lib.gptq_mx_scaled_gemm, base) == _lib.GPTQ_ERR_WORKSPACE
 
 
 def test_binding_refuses_host_tensors_and_wrong_types():
