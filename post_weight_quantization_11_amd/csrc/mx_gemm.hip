@@ -17,6 +17,8 @@
 // neighbouring lanes and go out in contiguous runs.
 #include "mx.h"
 
+#include <type_traits>
+
 namespace gptq {
 namespace {
 
@@ -1144,48 +1146,56 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
 }
 
 // One large tile of 16-bit X with 16-byte aligned rows of both operands.  As
-// tile_product, but the codes of W are staged in LDS too, a super-stage of 256
-// columns (128 bytes of a row: whole cache lines) at a time, and its scale bytes
+// tile_product, but the codes of W are staged in LDS too, a super-stage of SP
+// panels (64 SP columns: 32 SP bytes of a row) at a time, and its scale bytes
 // with them: loaded into registers by the lanes that use them, 32 bytes of a row
 // at a time, codes and scales took 59 and 56 of 433 us at 4096 x 8192 x 8192.  A
-// stage of X is one panel (64 columns); each of the four stages of a super-stage
-// fetches a quarter of the next one's W.
-template <int XT, int WR, int WC, int RB, int CB>
+// stage of X is one panel; each of the SP stages of a super-stage fetches its
+// share of the next one's W, and each super-stage a quarter of the rows of the
+// next four super-stages' scales (no branch in the loop).
+template <int XT, int WR, int WC, int RB, int CB, int SP>
 constexpr int big_tile_lds() {
   const int x = 32 * WC * CB, w = 32 * WR * RB;
-  return std::max(2 * (x + w) * kPanelRow + 2 * w * 8, WR * WC * 32 * out_pitch(RB) * 4);
+  return std::max(2 * x * kPanelRow + 2 * w * 32 * SP + 8 * w * 2 * SP, WR * WC * 32 * out_pitch(RB) * 4);
 }
 
-template <int XT, int WR, int WC, int RB, int CB, bool SPLIT>
+template <int XT, int WR, int WC, int RB, int CB, int SP, bool SPLIT>
 __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg, const TokenTile& tile, int r0,
                                         int split, unsigned char* smem) {
+  static_assert(SP == 2 || SP == 4, "64 or 128 bytes of a row");
   constexpr int kThreads = 64 * WR * WC, kWaves = WR * WC;
-  constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB;
-  constexpr int kX = BN * kPanelRow, kW = BM * kPanelRow;     // bytes of a buffer
+  constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB, kCols = 64 * SP;
+  constexpr int kWRow = 32 * SP, kWLanes = 2 * SP, kWRows = 64 / kWLanes;    // of W: a row, its lanes, rows a load
+  constexpr int kX = BN * kPanelRow, kW = BM * kWRow;         // bytes of a buffer
   constexpr int kXLoads = BN / (8 * kWaves), kWLoads = BM / (32 * kWaves);   // a wave's per stage
-  static_assert(BN % (8 * kWaves) == 0 && BM % (32 * kWaves) == 0 && kThreads % BM == 0, "every wave loads whole rows");
+  static_assert(BN % (8 * kWaves) == 0 && BM % (32 * kWaves) == 0 && kWaves % 2 == 0, "every wave loads whole rows");
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / WC, wc = wave % WC;
   unsigned char* xs = smem;                  // [2][BN][128]
-  unsigned char* wsm = smem + 2 * kX;        // [2][BM][128]
-  uint32_t* ssm = reinterpret_cast<uint32_t*>(smem + 2 * kX + 2 * kW);       // [2][BM][half]
+  unsigned char* wsm = smem + 2 * kX;        // [2][BM][kWRow]
+  unsigned char* ssm = wsm + 2 * kW;         // [8 super-stages][BM][2 SP]
   const int64_t x_pitch = p.ldx * 2, w_pitch = p.ldp * 4;
   const char* xbase = static_cast<const char*>(p.X) + (int64_t)tile.begin * x_pitch;
   const char* wbase = reinterpret_cast<const char*>(p.W + (int64_t)tile.expert * p.w_stride + (int64_t)r0 * p.ldp);
   const uint8_t* sbase = p.S + (int64_t)tile.expert * p.s_stride + (int64_t)r0 * p.lds;
   auto x_row = [&](int r) { return (uint32_t)min(r, tile.end - 1 - tile.begin) * (uint32_t)x_pitch; };
   auto w_row = [&](int r) { return (uint32_t)min(r, p.m - 1 - r0) * (uint32_t)w_pitch; };
+  // Slot of a row's chunk of W: sixteen neighbouring rows' cover all banks.
+  auto w_swizzle = [](int row) { return SP == 4 ? swizzle(row) : (row >> 2) & 3; };
 
-  // Supers [lo, hi) of this split; whole ones below `whole`.
-  const int per_split = tg.cols_per_split / 256;
-  const int lo = split * per_split, hi = min((p.n + 255) / 256, lo + per_split), whole = min(hi, p.n / 256);
-  const uint32_t chunk_at = ((lane & 7) ^ swizzle(wave * 8 + (lane >> 3))) << 4;   // source chunk of the lane's slot
-  uint32_t x_at[kXLoads], w_at[4 * kWLoads];
+  // Super-stages [lo, hi) of this split; whole ones below `whole`.
+  const int per_split = tg.cols_per_split / kCols;
+  const int lo = split * per_split, hi = min((p.n + kCols - 1) / kCols, lo + per_split), whole = min(hi, p.n / kCols);
+  uint32_t x_at[kXLoads], w_at[SP * kWLoads];
 #pragma unroll
-  for (int i = 0; i < kXLoads; ++i) x_at[i] = x_row((wave + i * kWaves) * 8 + (lane >> 3)) + chunk_at;
+  for (int i = 0; i < kXLoads; ++i)          // source chunk of the lane's slot
+    x_at[i] = x_row((wave + i * kWaves) * 8 + (lane >> 3)) + (((lane & 7) ^ swizzle(wave * 8 + (lane >> 3))) << 4);
 #pragma unroll
-  for (int i = 0; i < 4 * kWLoads; ++i) w_at[i] = w_row((wave + i * kWaves) * 8 + (lane >> 3)) + chunk_at;
+  for (int i = 0; i < SP * kWLoads; ++i) {
+    const int r = (wave + i * kWaves) * kWRows + lane / kWLanes;
+    w_at[i] = w_row(r) + (((lane % kWLanes) ^ w_swizzle(r)) << 4);
+  }
   auto direct = [&](unsigned char* dst, const char* src, uint32_t offset) {
     // As in tile_product: M0 is the LDS destination, waited for explicitly.
     const uint32_t d = (uint32_t)reinterpret_cast<uintptr_t>((lds_void*)dst);
@@ -1197,20 +1207,27 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
     for (int i = 0; i < kXLoads; ++i)
       direct(xs + buf * kX + (wave + i * kWaves) * 8 * kPanelRow, xbase + (int64_t)panel * kPanelRow, x_at[i]);
   };
-  auto fetch_w = [&](int super, int quarter) {
+  auto fetch_w = [&](int super, int share) {
 #pragma unroll
-    for (int i = quarter * kWLoads; i < (quarter + 1) * kWLoads; ++i)
-      direct(wsm + (super & 1) * kW + (wave + i * kWaves) * 8 * kPanelRow,
-             wbase + (int64_t)min(super, whole - 1) * kPanelRow, w_at[i]);
+    for (int i = share * kWLoads; i < (share + 1) * kWLoads; ++i)
+      direct(wsm + (super & 1) * kW + (wave + i * kWaves) * kWRows * kWRow,
+             wbase + (int64_t)min(super, whole - 1) * kWRow, w_at[i]);
   };
-  // Scale bytes of a super-stage: thread t those of row t % BM (the threads
-  // beyond BM write the same values).
-  const int srow = tid % BM;
-  const uint8_t* sptr = sbase + (int64_t)min(srow, p.m - 1 - r0) * p.lds;
-  u32x2 sreg;
-  auto fetch_s = [&](int super) { sreg = *reinterpret_cast<const u32x2_a1*>(sptr + 8 * min(super, whole - 1)); };
-  auto put_s = [&](int super) {
-    *reinterpret_cast<u32x2*>(ssm + ((super & 1) * BM + srow) * 2) = order_scales8(sreg[0], sreg[1]);
+  // Scale bytes: four lanes to a row, one for each super-stage of the group (of
+  // four); the threads beyond a quarter's rows write the same values again.
+  typedef std::conditional_t<SP == 4, u32x2, uint32_t> Scale;
+  typedef std::conditional_t<SP == 4, u32x2_a1, u32_a1> ScaleA1;
+  auto s_row = [&](int quarter) { return quarter * (BM / 4) + (tid >> 2) % (BM / 4); };
+  Scale sreg;
+  auto fetch_s = [&](int group, int quarter) {
+    const int super = min(lo + 4 * group + (tid & 3), whole - 1);
+    const uint8_t* row = sbase + (int64_t)min(s_row(quarter), p.m - 1 - r0) * p.lds;
+    sreg = *reinterpret_cast<const ScaleA1*>(row + 2 * SP * super);
+  };
+  auto put_s = [&](int group, int quarter) {
+    Scale* at = reinterpret_cast<Scale*>(ssm) + (4 * (group & 1) + (tid & 3)) * BM + s_row(quarter);
+    if constexpr (SP == 4) *at = order_scales8(sreg[0], sreg[1]);
+    else *at = sreg;
   };
 
   floatx16 acc[RB][CB];
@@ -1218,14 +1235,14 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
   for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = floatx16{};
-  uint32_t frag_x[4], frag_w[4];             // this lane's addresses of step j, of stage u's codes
+  uint32_t frag_x[4], frag_w[SP];            // this lane's addresses of step j, of stage u's codes
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     frag_x[j] = (uint32_t)((wc * CB * 32 + l32) * kPanelRow + (((4 * h + j) ^ swizzle(l32)) << 4));
-    frag_w[j] = (uint32_t)((wr * RB * 32 + l32) * kPanelRow + (((2 * j + h) ^ swizzle(l32)) << 4));
+    if (j < SP) frag_w[j] = (uint32_t)((wr * RB * 32 + l32) * kWRow + (((2 * j + h) ^ w_swizzle(l32)) << 4));
   }
   u32x4 x[2][CB], w[2][RB];
-  uint32_t sc[RB], exact = 0u;
+  uint32_t sc[RB], inexact = 0u;
   auto load_x = [&](int buf, int step, u32x4 (&o)[CB]) {
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb)
@@ -1234,14 +1251,19 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
   auto load_w = [&](int super, int u, u32x4 (&o)[RB]) {
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
-      o[rb] = *reinterpret_cast<const u32x4*>(wsm + (super & 1) * kW + frag_w[u] + rb * 32 * kPanelRow);
+      o[rb] = *reinterpret_cast<const u32x4*>(wsm + (super & 1) * kW + frag_w[u] + rb * 32 * kWRow);
   };
+  // Four scale bytes: this half's of the four stages, or both halves' of the two.
   auto load_s = [&](int super) {
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-      sc[rb] = ssm[((super & 1) * BM + (wr * RB + rb) * 32 + l32) * 2 + h];
-      if constexpr (XT == GPTQ_F16 && !SPLIT) exact |= f16_inexact4(sc[rb]);
+      const int at = ((super - lo) & 7) * BM + (wr * RB + rb) * 32 + l32;
+      sc[rb] = reinterpret_cast<const uint32_t*>(ssm)[SP == 4 ? 2 * at + h : at];
+      if constexpr (XT == GPTQ_F16 && !SPLIT) inexact |= f16_inexact4(sc[rb]);
     }
+  };
+  auto scale_of = [&](int u, int rb) {
+    return mx_scale_operand((SP == 4 ? sc[rb] >> (8 * u) : sc[rb] >> (16 * u + 8 * h)) & 255u);
   };
   // Products of step j of stage u, row blocks [from, to).
   auto products = [&](int u, int j, const u32x4 (&xf)[CB], const u32x4 (&wf)[RB], int from, int to) {
@@ -1252,7 +1274,7 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
         split8(xf[cb], top, rest);
 #pragma unroll
         for (int rb = from; rb < to; ++rb) {
-          const u32x4 wv = widen8<GPTQ_BF16>(wf[rb][j], mx_scale_operand((sc[rb] >> (8 * u)) & 255u));
+          const u32x4 wv = widen8<GPTQ_BF16>(wf[rb][j], scale_of(u, rb));
           acc[rb][cb] = mfma32<GPTQ_BF16>(top, wv, acc[rb][cb]);
           acc[rb][cb] = mfma32<GPTQ_BF16>(rest, wv, acc[rb][cb]);
         }
@@ -1261,7 +1283,7 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
     } else {
 #pragma unroll
       for (int rb = from; rb < to; ++rb) {
-        const u32x4 wv = widen8<XT>(wf[rb][j], mx_scale_operand((sc[rb] >> (8 * u)) & 255u));
+        const u32x4 wv = widen8<XT>(wf[rb][j], scale_of(u, rb));
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = mfma32<XT>(xf[cb], wv, acc[rb][cb]);
       }
@@ -1269,29 +1291,33 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
       for (int i = 0; i < (to - from) * CB; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
-        __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);   // one VALU
+        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);   // two VALU
       }
     }
   };
 
   if (lo < whole) {
-    fetch_x(4 * lo, 0);
+    fetch_x(SP * lo, 0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) fetch_w(lo, u);
-    fetch_s(lo);
-    put_s(lo);
+    for (int u = 0; u < SP; ++u) fetch_w(lo, u);
+#pragma unroll
+    for (int quarter = 0; quarter < 4; ++quarter) {
+      fetch_s(0, quarter);
+      put_s(0, quarter);
+    }
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     lds_barrier();
     load_x(0, 0, x[0]);
     load_w(lo, 0, w[0]);
     load_s(lo);
     for (int super = lo; super < whole; ++super) {
+      const int group = ((super - lo) >> 2) + 1, quarter = (super - lo) & 3;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < SP; ++u) {
         // Past the last panel that panel is fetched again, for no one.
-        fetch_x(min(4 * super + u + 1, 4 * whole - 1), (u + 1) & 1);
+        fetch_x(min(SP * super + u + 1, SP * whole - 1), (u + 1) & 1);
         fetch_w(super + 1, u);
-        if (u == 0) fetch_s(super + 1);
+        if (u == 0) fetch_s(group, quarter);
         __builtin_amdgcn_sched_barrier(0);   // the loads are issued before the products
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
@@ -1299,20 +1325,20 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
           products(u, j, x[j & 1], w[u & 1], 0, RB);
         }
         products(u, 3, x[1], w[u & 1], 0, RB / 2);
-        if (u == 3) put_s(super + 1);
+        if (u == SP - 1) put_s(group, quarter);
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
         lds_barrier();
         load_x((u + 1) & 1, 0, x[0]);
-        load_w(super + (u == 3), (u + 1) & 3, w[(u + 1) & 1]);
+        load_w(super + (u == SP - 1), (u + 1) % SP, w[(u + 1) & 1]);
         products(u, 3, x[1], w[u & 1], RB / 2, RB);
-        if (u == 3) load_s(super + 1);
+        if (u == SP - 1) load_s(super + 1);
       }
     }
   }
   // The columns behind the last whole super-stage, a panel at a time.
   if (lo <= whole && whole < hi) {
 #pragma unroll 1
-    for (int panel = 4 * whole; panel < (p.n + 63) / 64; ++panel) {
+    for (int panel = SP * whole; panel < (p.n + 63) / 64; ++panel) {
       lds_barrier();
 #pragma unroll
       for (int i = 0; i < BN * 8 / kThreads; ++i) {
@@ -1324,8 +1350,10 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
       for (int rb = 0; rb < RB; ++rb) {
         const int r = (wr * RB + rb) * 32 + l32;
         w[0][rb] = load_w4_tail(reinterpret_cast<const uint32_t*>(wbase + w_row(r)), 8 * panel + 4 * h, p.n);
-        sc[rb] = (load_scales4(sbase + (int64_t)min(r, p.m - 1 - r0) * p.lds, 2 * panel, p.n) >> (8 * h)) & 255u;
-        if constexpr (XT == GPTQ_F16 && !SPLIT) exact |= f16_inexact4(sc[rb] * 0x01010101u);
+        // This half's byte in every place a stage may take it from.
+        sc[rb] = ((load_scales4(sbase + (int64_t)min(r, p.m - 1 - r0) * p.lds, 2 * panel, p.n) >> (8 * h)) & 255u) *
+                 0x01010101u;
+        if constexpr (XT == GPTQ_F16 && !SPLIT) inexact |= f16_inexact4(sc[rb]);
       }
       lds_barrier();
 #pragma unroll
@@ -1336,7 +1364,7 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
     }
   }
   if constexpr (XT == GPTQ_F16 && !SPLIT) {
-    if (!__syncthreads_and(exact == 0u)) return false;
+    if (!__syncthreads_and(inexact == 0u)) return false;
   } else {
     lds_barrier();
   }
@@ -1373,15 +1401,15 @@ __global__ __launch_bounds__(64 * WR * WC, RB * CB <= 8 ? 2 : 1) void mx_tile_ke
   }
 }
 
-template <int XT, int WR, int WC, int RB, int CB>
+template <int XT, int WR, int WC, int RB, int CB, int SP>
 __global__ __launch_bounds__(64 * WR * WC, 2) void mx_big_tile_kernel(MxOperands p, TileGrid tg) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   int split, r0;
   TokenTile tile;
   if (!tile_of_workgroup(p, tg, 32 * WR * RB, 32 * WC * CB, split, tile, r0)) return;
-  const bool done = big_tile_product<XT, WR, WC, RB, CB, false>(p, tg, tile, r0, split, smem);
+  const bool done = big_tile_product<XT, WR, WC, RB, CB, SP, false>(p, tg, tile, r0, split, smem);
   if constexpr (XT == GPTQ_F16) {
-    if (!done) big_tile_product<XT, WR, WC, RB, CB, true>(p, tg, tile, r0, split, smem);
+    if (!done) big_tile_product<XT, WR, WC, RB, CB, SP, true>(p, tg, tile, r0, split, smem);
   }
 }
 
@@ -1426,7 +1454,7 @@ int64_t max_tiles(int64_t rows, int64_t experts, bool grouped, int tile) {
 // What a product runs on, from its sizes alone.
 enum Kind {
   kRows1, kRows2, kRows4, kRows2x2, kRows4x2,              // mx_rows_kernel: tiles of W (x tiles of X)
-  kStream1, kStream3,                                                // mx_stream_kernel: tiles of W
+  kStream1x4, kStream1, kStream3,                                    // mx_stream_kernel: tiles of W (x rows of X staged)
   kTile128x32, kTile128x64, kTile128x128, kTile256x128, kTile256x256, // W rows x X rows of a tile
 };
 struct Plan {
@@ -1439,14 +1467,15 @@ constexpr int kSplitCols = 256;              // a split is a multiple of this
 // taken first): products small enough for their operands to come through L2
 // run on the row kernels, whose waves split the columns (64 x 4096 x 4096: 11.7
 // against 13.8 on tiles; 64 x 12288 x 12288: 75 against 36), long matrices with
-// few rows of X on the stream kernel (16 x 49152 x 12288: 78 against 93), the
-// rest on tiles, as wide as still gives 256 of them with splits of 1024 columns,
+// few rows of X on the stream kernel (16 x 49152 x 12288: 80 against 93; three
+// tiles of W a wave there, 90 with one; 16 x 28672 x 8192: 28 with one tile, 44
+// with three), the rest on tiles, as wide as still gives 256 of them with splits of 1024 columns,
 // split until there are about 384 (16 x 12288 x 12288: 28 with 4 splits, 45 with
 // 1; 64 x 11008 x 4096 on 128 x 64 with 4 splits 20, on 128 x 32 with 2 22).
 // 256 x 256 tiles are the fastest where they fill the CUs once or in whole
 // rounds (1024 x 11008 x 4096: 83 against 101 on 256 x 128, 4096 x 8192 x 8192:
-// 373 against 414), 256 x 128 (two to a CU) otherwise (2048 x 11008 x 4096: 158
-// against 168).
+// 374 against 433), 256 x 128 (two to a CU) otherwise (2048 x 11008 x 4096: 150
+// against 169).
 constexpr int64_t kWantTiles = 384, kMinSplitCols = 512;
 
 Plan tile_plan(int64_t m, int64_t n, int64_t rows, bool mx) {
@@ -1485,7 +1514,7 @@ Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped
     if (outputs <= 65536) return Plan{kRows1, 1};
     return Plan{rows <= 32 ? kRows2 : kRows2x2, 1};
   }
-  if (m >= 24576 && rows <= 16) return Plan{rows <= 4 ? kStream1 : kStream3, 1};
+  if (m >= 24576 && rows <= 16) return Plan{rows <= 4 ? kStream1x4 : m < 40960 ? kStream1 : kStream3, 1};
   if (products > 2200000000) return tile_plan(m, n, rows, false);
   if (outputs <= 65536) return Plan{kRows1, 1};
   if (rows <= 4) return Plan{kRows2, 1};
@@ -1538,10 +1567,10 @@ gptq_status launch_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStrea
   return run_tiles(k, 32 * WR * RB, 32 * WC * CB, 64 * WR * WC, tile_lds<XT, WR, WC, RB, CB, PB>(), p, pl, ws, st);
 }
 
-template <int XT, int WR, int WC, int RB, int CB>
+template <int XT, int WR, int WC, int RB, int CB, int SP>
 gptq_status launch_big_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStream_t st) {
-  return run_tiles(mx_big_tile_kernel<XT, WR, WC, RB, CB>, 32 * WR * RB, 32 * WC * CB, 64 * WR * WC,
-                   big_tile_lds<XT, WR, WC, RB, CB>(), p, pl, ws, st);
+  return run_tiles(mx_big_tile_kernel<XT, WR, WC, RB, CB, SP>, 32 * WR * RB, 32 * WC * CB, 64 * WR * WC,
+                   big_tile_lds<XT, WR, WC, RB, CB, SP>(), p, pl, ws, st);
 }
 
 template <int XT, int RT, int NT, int D>
@@ -1575,7 +1604,8 @@ gptq_status launch(const MxOperands& p, void* ws, size_t ws_bytes, hipStream_t s
   constexpr int P2 = XT == kMx ? 1 : 2, P4 = XT == kMx ? 1 : 4;        // panels per stage
   if constexpr (XT != kMx) {
     if (aligned_x<XT>(p) && aligned_w(p)) {
-      if (pl.kind == kTile256x256) return launch_big_tiles<XT, 4, 2, 2, 4>(p, pl, ws, st);
+      if (pl.kind == kTile256x256) return launch_big_tiles<XT, 4, 2, 2, 4, 4>(p, pl, ws, st);
+      if (pl.kind == kTile256x128) return launch_big_tiles<XT, 4, 1, 2, 4, 2>(p, pl, ws, st);
     }
   }
   switch (pl.kind) {
@@ -1588,8 +1618,11 @@ gptq_status launch(const MxOperands& p, void* ws, size_t ws_bytes, hipStream_t s
     case kRows4: return launch_rows<XT, 4, 1, 2>(p, 8, st);
     case kRows2x2: return launch_rows<XT, 2, 2, 2>(p, 8, st);
     case kRows4x2: return launch_rows<XT, 4, 2, 1>(p, 8, st);
-    case kStream1:
+    case kStream1x4:
       if constexpr (XT != kMx) return launch_stream<XT, 1, 1, 4>(p, st);
+      break;
+    case kStream1:
+      if constexpr (XT != kMx) return launch_stream<XT, 1, 1, 16>(p, st);
       break;
     case kStream3:
       if constexpr (XT != kMx) return launch_stream<XT, 3, 1, 16>(p, st);

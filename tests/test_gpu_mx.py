@@ -592,6 +592,7 @@ KINDS = [
     # m, n, batch
     (24576, 1024, 1), (24600, 545, 3),            # long matrices, up to four rows of X
     (24576, 1024, 16), (24590, 1160, 7),          # long matrices, up to sixteen
+    (40960, 1024, 16), (41000, 1160, 5),          # longer ones
     (4100, 4160, 160), (4096, 4608, 140),         # tiles of 128 x 32, columns split
     (8200, 4100, 70), (8192, 4096, 64),           # tiles of 128 x 64
     (16384, 1024, 180), (16400, 1031, 135),       # tiles of 128 x 128
