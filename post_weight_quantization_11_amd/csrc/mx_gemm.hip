@@ -17,6 +17,8 @@
 // neighbouring lanes and go out in contiguous runs.
 #include "mx.h"
 
+#include <cmath>
+#include <limits>
 #include <type_traits>
 
 namespace gptq {
@@ -478,142 +480,98 @@ __global__ __launch_bounds__(512) void mx_rows_kernel(MxOperands p) {
   }
 }
 
-// Few rows of 16-bit X, many rows of W: every wave owns RT tiles of W rows for
-// all columns, and the workgroup stages X once for its waves, a quad of units
-// at a time, two in LDS, in the order the matrix instructions take it: the 16
-// bytes of lane (q, row) of step j at place row ^ (4j + q) of the sixteen, so
-// that writing along a row of X and reading a step both touch all banks evenly.
-// XR: rows of X that are staged (the others' places repeat them).  The packed
-// rows stream through registers, a quad ahead.
-template <int XT, int RT, int NT, int XR, bool SPLIT>
+// Up to four rows of 16-bit X, many rows of W: every wave owns sixteen rows of W
+// for all columns, and the workgroup stages X once for its waves, a quad of
+// units at a time, two in LDS, in the order the matrix instructions take it: the
+// 16 bytes of lane (q, row) of step j at place row ^ (4j + q) of the four (the
+// matrix instruction's other rows repeat them), so that writing along a row of X
+// and reading a step both touch all banks evenly.  The packed rows stream through
+// registers, a quad ahead.  Bound by W's bytes: 1 x 49152 x 12288 59 us, 5.4 TB/s
+// (73 us on the row kernel, whose every wave loads X itself; 67 us on 128 x 32
+// tiles).
+constexpr int kStreamRows = 4;
+template <int XT, bool SPLIT>
 __device__ inline bool stream_product(const MxOperands& p, const TokenTile& tile, int r0, u32x4* xs) {
-  static_assert(XR == 4 || XR == 16 * NT, "a quarter of one tile, or all rows");
-  constexpr int kThreads = 256, kPanel = 4 * 4 * 4 * XR;       // 16-byte chunks of a quad
-  constexpr int kMine = kPanel / kThreads;
+  constexpr int kPanel = 4 * 4 * 4 * kStreamRows;             // 16-byte chunks of a quad: one a thread
   const int tid = (int)threadIdx.x, lane = tid & 63, q = lane >> 4, c16 = lane & 15;
-  const uint32_t* wrow[RT];
-  const uint8_t* wsrow[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int64_t r = min(r0 + 16 * rt + c16, p.m - 1);
-    wrow[rt] = p.W + (int64_t)tile.expert * p.w_stride + r * p.ldp;
-    wsrow[rt] = p.S + (int64_t)tile.expert * p.s_stride + r * p.lds;
-  }
+  const int64_t r = min(r0 + c16, p.m - 1);
+  const uint32_t* wrow = p.W + (int64_t)tile.expert * p.w_stride + r * p.ldp;
+  const uint8_t* wsrow = p.S + (int64_t)tile.expert * p.s_stride + r * p.lds;
   const uint16_t* X = static_cast<const uint16_t*>(p.X) + (int64_t)tile.begin * p.ldx;
   const int last = tile.end - tile.begin - 1;
-  floatx4 acc[RT][NT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[rt][nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+  floatx4 acc[1][1] = {{floatx4{0.f, 0.f, 0.f, 0.f}}};
   uint32_t inexact = 0u;
-  typedef Unit<XT, RT, NT> U;
+  typedef Unit<XT, 1, 1> U;
   const int quads = p.n >> 9;
 
-  // Thread t stages chunks t, t + 256, ... along the rows of X, 64 to a row.
-  const uint16_t* xat[kMine];
-  int xslot[kMine];
-#pragma unroll
-  for (int i = 0; i < kMine; ++i) {
-    const int c = tid + i * kThreads, row = c >> 6, at = c & 63, jq = at & 15;
-    xat[i] = X + (int64_t)min(row, last) * p.ldx + at * 8;
-    xslot[i] = ((at >> 4) * 16 + jq) * XR + (row & ~15) + ((row ^ jq) & (XR < 16 ? XR - 1 : 15));
-  }
-  u32x4 xr[kMine];
-  auto fetch_x = [&](int quad) {
-#pragma unroll
-    for (int i = 0; i < kMine; ++i)
-      xr[i] = *reinterpret_cast<const u32x4_a2*>(xat[i] + min(quad, quads - 1) * 512);
-  };
-  auto put_x = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) xs[buf * kPanel + xslot[i]] = xr[i];
-  };
-  u32x4 w[4][RT], cur[RT], nxt[RT];
+  // Thread t stages chunk t along the rows of X, 64 to a row.
+  const int xrow = tid >> 6, xat = tid & 63, xjq = xat & 15;
+  const uint16_t* xsrc = X + (int64_t)min(xrow, last) * p.ldx + xat * 8;
+  const int xslot = ((xat >> 4) * 16 + xjq) * kStreamRows + ((xrow ^ xjq) & (kStreamRows - 1));
+  u32x4 xr, w[4], cur, nxt;
+  auto fetch_x = [&](int quad) { xr = *reinterpret_cast<const u32x4_a2*>(xsrc + min(quad, quads - 1) * 512); };
+  auto put_x = [&](int buf) { xs[buf * kPanel + xslot] = xr; };
   auto load_w = [&](int quad, int d) {
-    const int unit = 4 * min(quad, quads - 1) + d;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) w[d][rt] = *reinterpret_cast<const u32x4_a4*>(wrow[rt] + 16 * unit + 4 * q);
+    w[d] = *reinterpret_cast<const u32x4_a4*>(wrow + 16 * (4 * min(quad, quads - 1) + d) + 4 * q);
   };
-  auto load_scales = [&](int quad, u32x4 (&s)[RT]) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) s[rt] = *reinterpret_cast<const u32x4_a1*>(wsrow[rt] + 16 * min(quad, quads - 1));
+  auto load_scales = [&](int quad) {
+    return *reinterpret_cast<const u32x4_a1*>(wsrow + 16 * min(quad, quads - 1));
   };
-  const uint32_t no_xs[NT] = {};
+  const uint32_t no_xs[1] = {};
   if (quads > 0) {
     fetch_x(0);
-    load_scales(0, cur);
+    cur = load_scales(0);
 #pragma unroll
     for (int d = 0; d < 4; ++d) load_w(0, d);
     put_x(0);
     lds_barrier();
     for (int quad = 0; quad < quads; ++quad) {
       fetch_x(quad + 1);
-      load_scales(quad + 1, nxt);
+      nxt = load_scales(quad + 1);
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         U u;
-        uint32_t ws[RT];
+        const uint32_t ws[1] = {cur[d]};
+        u.w[0] = w[d];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          u.w[rt] = w[d][rt];
-          ws[rt] = cur[rt][d];
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            u.x[nt][j] = xs[(quad & 1) * kPanel + (d * 16 + 4 * j + q) * XR + 16 * nt +
-                            ((c16 ^ (4 * j + q)) & (XR < 16 ? XR - 1 : 15))];
+        for (int j = 0; j < 4; ++j)
+          u.x[0][j] = xs[(quad & 1) * kPanel + (d * 16 + 4 * j + q) * kStreamRows + ((c16 ^ q) & (kStreamRows - 1))];
         multiply_unit<XT, SPLIT>(u, ws, no_xs, acc, inexact);
         load_w(quad + 1, d);
       }
       put_x((quad + 1) & 1);
       lds_barrier();
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) cur[rt] = nxt[rt];
+      cur = nxt;
     }
   }
   // The columns behind the last whole quad, X from memory.
   for (int unit = 4 * quads; unit < (p.n + 127) >> 7; ++unit) {
     U u;
-    uint32_t ws[RT];
+    u.w[0] = load_w4_tail(wrow, 16 * unit + 4 * q, p.n);
+    const uint32_t ws[1] = {load_scales4(wsrow, 4 * unit, p.n)};
+    const uint16_t* x = X + (int64_t)min(c16, last) * p.ldx;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      u.w[rt] = load_w4_tail(wrow[rt], 16 * unit + 4 * q, p.n);
-      ws[rt] = load_scales4(wsrow[rt], 4 * unit, p.n);
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const uint16_t* x = X + (int64_t)min(16 * nt + c16, last) * p.ldx;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u.x[nt][j] = load_x8_tail(x, 128 * unit + 32 * j + 8 * q, p.n);
-    }
+    for (int j = 0; j < 4; ++j) u.x[0][j] = load_x8_tail(x, 128 * unit + 32 * j + 8 * q, p.n);
     multiply_unit<XT, SPLIT>(u, ws, no_xs, acc, inexact);
   }
   if constexpr (XT == GPTQ_F16 && !SPLIT) {
     if (!__syncthreads_and(inexact == 0u)) return false;
   }
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) store_block16(p, tile, tile.begin + 16 * nt, r0 + 16 * rt, acc[rt][nt]);
+  store_block16(p, tile, tile.begin, r0, acc[0][0]);
   return true;
 }
 
-template <int XT, int RT, int NT, int XR>
+template <int XT>
 __global__ __launch_bounds__(256) void mx_stream_kernel(MxOperands p) {
-  extern __shared__ u32x4 xs[];              // [2][unit][step][quarter][XR]
-  const int wg_rows = 16 * RT * 4;
-  const int row_wgs = (p.m + wg_rows - 1) / wg_rows;
+  __shared__ u32x4 xs[2 * 64 * kStreamRows]; // [2][unit][step][quarter][row]
+  const int row_wgs = (p.m + 63) / 64;
   const int slot = (int)(blockIdx.x / row_wgs);
-  const int r0 = (int)(blockIdx.x % row_wgs) * wg_rows +
-                 __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 16 * RT;
-  const TokenTile tile = find_tile(p, slot, 16 * NT);
+  const int r0 = (int)(blockIdx.x % row_wgs) * 64 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 16;
+  const TokenTile tile = find_tile(p, slot, 16);
   if (!tile.valid) return;
-  const bool done = stream_product<XT, RT, NT, XR, false>(p, tile, r0, xs);
+  const bool done = stream_product<XT, false>(p, tile, r0, xs);
   if constexpr (XT == GPTQ_F16) {
-    if (!done) stream_product<XT, RT, NT, XR, true>(p, tile, r0, xs);
+    if (!done) stream_product<XT, true>(p, tile, r0, xs);
   }
 }
 
@@ -656,11 +614,13 @@ __device__ inline int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 constexpr int out_pitch(int row_blocks) { return (row_blocks % 2 == 0 ? 64 : 32) + 4; }
 
 // LDS of a tile: two buffers of staged rows, later the waves' output blocks.
-// The microscaled scales of eight stages stand behind the buffers.
-template <int XT, int WR, int WC, int RB, int CB, int PB>
+// Behind the buffers the microscaled scales of eight stages, or (WL) the codes of
+// W of two.
+template <int XT, int WR, int WC, int RB, int CB, int PB, bool WL>
 constexpr int tile_lds() {
   const int rows = 32 * (WC * CB + (XT == kMx ? WR * RB : 0));
-  return std::max(2 * PB * rows * kPanelRow + (XT == kMx ? 8 * rows * 8 : 0), WR * WC * 32 * out_pitch(RB) * 4);
+  const int behind = XT == kMx ? 8 * rows * 8 : WL ? 2 * 32 * WR * RB * 32 * PB : 0;
+  return std::max(2 * PB * rows * kPanelRow + behind, WR * WC * 32 * out_pitch(RB) * 4);
 }
 
 // Work of one launch: tiles of W rows, of X rows, and parts of the columns.
@@ -791,7 +751,11 @@ __device__ inline void store_tile(const MxOperands& p, const TileGrid& tg, const
 
 // One tile.  PB: panels of 128 bytes per row in a stage.  DIRECT: 16-byte
 // aligned rows; whole stages of X (and microscaled W) go from memory to LDS
-// without passing through registers.  SPLIT (float16 X): every product as two
+// without passing through registers.  WL (16-bit X, 16-byte aligned rows of W):
+// so do W's codes, 32 PB bytes of a row at a time, where the lanes that use them
+// would load 32 (64 x 11008 x 4096 on 128 x 32 tiles 23 -> 14.5 us; not for 128 x
+// 128, where the LDS costs a workgroup a CU: 64 experts' 1531 x 1024 x 2048 50 ->
+// 65 us).  SPLIT (float16 X): every product as two
 // bfloat16 ones.  Without SPLIT a float16 tile runs as if all its scales were
 // exact in float16 and says at the end whether they were (the same answer in
 // the whole workgroup); if not, nothing is stored and the caller runs it again
@@ -803,11 +767,12 @@ __device__ inline void store_tile(const MxOperands& p, const TileGrid& tg, const
 // two halves of that step's products: every wave then holds the step's
 // operands, so the other buffer is complete (its loads were waited for) and
 // this one is free, and the next stage's first reads overlap the second half.
-template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT, bool SPLIT>
+template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT, bool WL, bool SPLIT>
 __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, const TokenTile& tile, int r0, int split,
                                     unsigned char* smem) {
   constexpr bool MX = XT == kMx;
-  static_assert(!MX || PB == 1, "microscaled stages are one panel");
+  static_assert(!MX || (PB == 1 && !WL), "microscaled stages are one panel, with W's");
+  static_assert(!WL || PB >= 2, "64 or 128 bytes of a row");
   constexpr int kThreads = 64 * WR * WC, kWaves = WR * WC;
   constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB;
   constexpr int kLdsRows = MX ? BM + BN : BN;                 // X rows first, then W rows
@@ -926,6 +891,35 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
     w_at[rb] = r * (uint32_t)w_pitch;
     ws_at[rb] = r * (uint32_t)p.lds;
   }
+  constexpr int kWRow = 32 * PB, kWLanes = 2 * PB, kWRows = 64 / kWLanes;    // a row, its lanes, rows a load
+  constexpr int kWLoads = WL ? BM / (kWRows * kWaves) : 1;    // a wave's per stage
+  static_assert(!WL || BM % (kWRows * kWaves) == 0, "every wave loads whole rows");
+  unsigned char* w_lds = smem + 2 * kBuf;    // [2][BM][kWRow]
+  auto w_swizzle = [](int row) { return PB == 4 ? swizzle(row) : (row >> 2) & 3; };
+  uint32_t w_direct[kWLoads], w_frag[WL ? PB : 1];
+  if constexpr (WL) {
+#pragma unroll
+    for (int i = 0; i < kWLoads; ++i) {
+      const int r = (wave + i * kWaves) * kWRows + lane / kWLanes;
+      w_direct[i] = (uint32_t)min(r, p.m - 1 - r0) * (uint32_t)w_pitch + (((lane % kWLanes) ^ w_swizzle(r)) << 4);
+    }
+#pragma unroll
+    for (int u = 0; u < PB; ++u)
+      w_frag[u] = (uint32_t)((wr * RB * 32 + l32) * kWRow + (((2 * u + h) ^ w_swizzle(l32)) << 4));
+  }
+  auto fetch_codes = [&](int st, int buf) {
+    if constexpr (WL) {
+#pragma unroll
+      for (int i = 0; i < kWLoads; ++i) {
+        const uint32_t dst = (uint32_t)reinterpret_cast<uintptr_t>(
+            (lds_void*)(w_lds + buf * (BM * kWRow) + (wave + i * kWaves) * kWRows * kWRow));
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(w_direct[i]),
+                     "s"(wbase + (int64_t)st * kWRow)
+                     : "memory", "m0");
+      }
+    }
+  };
+
   struct Regs {
     u32x4 w[MX ? 1 : PB][RB];                // codes of this lane's block of each panel (16-bit X)
     uint32_t ws[(PB + 1) / 2][RB];           // scale bytes of two panels' blocks; microscaled: of the stage's four
@@ -934,13 +928,15 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
   Regs cur, nxt;
   auto fetch_regs = [&](int st, Regs& g) {
     if constexpr (!MX) {
+      if constexpr (!WL) {
 #pragma unroll
-      for (int u = 0; u < PB; ++u)
+        for (int u = 0; u < PB; ++u)
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          const uint32_t blk = (uint32_t)(2 * (st * PB + u) + h);
-          g.w[u][rb] = *reinterpret_cast<const u32x4_a4*>(wbase + (w_at[rb] + 16u * blk));
-        }
+          for (int rb = 0; rb < RB; ++rb) {
+            const uint32_t blk = (uint32_t)(2 * (st * PB + u) + h);
+            g.w[u][rb] = *reinterpret_cast<const u32x4_a4*>(wbase + (w_at[rb] + 16u * blk));
+          }
+      }
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         const uint8_t* at = sbase + (ws_at[rb] + 2u * PB * st);
@@ -953,7 +949,15 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
       }
     }
   };
-  auto read_scales = [&](int st, Regs& g) {
+  // What of a stage's registers comes from LDS.
+  auto read_regs = [&](int st, int buf, Regs& g) {
+    if constexpr (WL) {
+#pragma unroll
+      for (int u = 0; u < PB; ++u)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+          g.w[u][rb] = *reinterpret_cast<const u32x4*>(w_lds + buf * (BM * kWRow) + w_frag[u] + rb * 32 * kWRow);
+    }
     if constexpr (MX) {
       const uint32_t* at = scale_lds + ((st - s_lo) & 7) * kLdsRows * 2 + l32 * 2 + h;
 #pragma unroll
@@ -1042,10 +1046,10 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
       }
     }
   };
-  // 16-bit X: asks the scheduler for one LDS read and up to two conversions
-  // behind each of `count` products.
+  // Asks the scheduler for one LDS read and up to two conversions behind each of
+  // `count` products.
   auto interleave = [&](int count) {
-    if constexpr (!MX && !SPLIT) {
+    if constexpr (!SPLIT) {
 #pragma unroll
       for (int i = 0; i < count; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
@@ -1073,6 +1077,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
       fetch(s_lo);
       put(0);
     }
+    fetch_codes(s_lo, 0);
     fetch_regs(s_lo, cur);
     if constexpr (MX) {
 #pragma unroll
@@ -1084,7 +1089,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     lds_barrier();
     load_frags(0, 0, f[0]);
-    read_scales(s_lo, cur);
+    read_regs(s_lo, 0, cur);
     for (int st = s_lo; st < s_whole; ++st) {
       const int buf = (st - s_lo) & 1;
       // The last stage fetches itself again, into the buffer no one reads any
@@ -1096,6 +1101,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
       } else {
         fetch(next);
       }
+      fetch_codes(next, buf ^ 1);
       fetch_regs(next, nxt);
       if constexpr (MX) {
         fetch_scales(((st - s_lo) >> 2) + 1, (st - s_lo) & 3);
@@ -1117,7 +1123,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
       }
       lds_barrier();
       load_frags(buf ^ 1, 0, f[0]);
-      read_scales(next, nxt);
+      read_regs(next, buf ^ 1, nxt);
       products(kSteps - 1, f[1], cur, RB / 2, RB);
       interleave((RB - RB / 2) * CB);
       cur = nxt;
@@ -1389,15 +1395,15 @@ __device__ inline bool tile_of_workgroup(const MxOperands& p, const TileGrid& tg
 }
 
 // Two waves per SIMD where the accumulators leave room for them.
-template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT>
+template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT, bool WL>
 __global__ __launch_bounds__(64 * WR * WC, RB * CB <= 8 ? 2 : 1) void mx_tile_kernel(MxOperands p, TileGrid tg) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   int split, r0;
   TokenTile tile;
   if (!tile_of_workgroup(p, tg, 32 * WR * RB, 32 * WC * CB, split, tile, r0)) return;
-  const bool done = tile_product<XT, WR, WC, RB, CB, PB, DIRECT, false>(p, tg, tile, r0, split, smem);
+  const bool done = tile_product<XT, WR, WC, RB, CB, PB, DIRECT, WL, false>(p, tg, tile, r0, split, smem);
   if constexpr (XT == GPTQ_F16) {
-    if (!done) tile_product<XT, WR, WC, RB, CB, PB, DIRECT, true>(p, tg, tile, r0, split, smem);
+    if (!done) tile_product<XT, WR, WC, RB, CB, PB, DIRECT, WL, true>(p, tg, tile, r0, split, smem);
   }
 }
 
@@ -1453,8 +1459,8 @@ int64_t max_tiles(int64_t rows, int64_t experts, bool grouped, int tile) {
 
 // What a product runs on, from its sizes alone.
 enum Kind {
-  kRows1, kRows2, kRows4, kRows2x2, kRows4x2,              // mx_rows_kernel: tiles of W (x tiles of X)
-  kStream1x4, kStream1, kStream3,                                    // mx_stream_kernel: tiles of W (x rows of X staged)
+  kRows1, kRows2, kRows2x2,                  // mx_rows_kernel: tiles of W (x tiles of X)
+  kStream,                                   // mx_stream_kernel: up to kStreamRows rows of X
   kTile128x32, kTile128x64, kTile128x128, kTile256x128, kTile256x256, // W rows x X rows of a tile
 };
 struct Plan {
@@ -1463,64 +1469,95 @@ struct Plan {
 };
 constexpr int kSplitCols = 256;              // a split is a multiple of this
 
-// The rules below follow sweeps of all kinds over sizes (times in us, the kind
-// taken first): products small enough for their operands to come through L2
-// run on the row kernels, whose waves split the columns (64 x 4096 x 4096: 11.7
-// against 13.8 on tiles; 64 x 12288 x 12288: 75 against 36), long matrices with
-// few rows of X on the stream kernel (16 x 49152 x 12288: 80 against 93; three
-// tiles of W a wave there, 90 with one; 16 x 28672 x 8192: 28 with one tile, 44
-// with three), the rest on tiles, as wide as still gives 256 of them with splits of 1024 columns,
-// split until there are about 384 (16 x 12288 x 12288: 28 with 4 splits, 45 with
-// 1; 64 x 11008 x 4096 on 128 x 64 with 4 splits 20, on 128 x 32 with 2 22).
-// 256 x 256 tiles are the fastest where they fill the CUs once or in whole
-// rounds (1024 x 11008 x 4096: 83 against 101 on 256 x 128, 4096 x 8192 x 8192:
-// 374 against 433), 256 x 128 (two to a CU) otherwise (2048 x 11008 x 4096: 150
-// against 169).
-constexpr int64_t kWantTiles = 384, kMinSplitCols = 512;
-
-Plan tile_plan(int64_t m, int64_t n, int64_t rows, bool mx) {
-  auto tiles = [&](int bm, int bn) { return ceil_div(m, bm) * ceil_div(rows, bn); };
-  if (rows >= 192) {
-    const int64_t t = tiles(256, 256), rounds = ceil_div(t, 256) * 256;
-    if (mx ? t >= 192 : (t >= 160 && t <= 256) || (t > 256 && t * 10 >= rounds * 9)) return Plan{kTile256x256, 1};
-    if (tiles(256, 128) >= 192 && (!mx || rows >= 1024)) return Plan{kTile256x128, 1};
+// Products on tiles: the shape and the splits with the least time by this model,
+// in us: a launch, 256 columns of every round of workgroups, each round with as
+// many as the CUs hold at once, and the join with its splits' sums.  A round's
+// time grows from `one` (a workgroup a CU) to `full` along a square root (a few
+// CUs with two already hold the rest up).  Fitted to 180 sizes of 16-bit X from
+// 8 x 1024 x 2048 to 2048 x 49152 x 12288 and 50 of microscaled X: what it
+// chooses takes 1.02 and 1.01 times the fastest's time in the mean, 1.3 and 1.13
+// at worst.  Some of the measured pairs, the chosen first, 16-bit: 16 x 12288 x
+// 12288 on 128 x 32 with 4 splits 21, with 1 41; 256 x 4096 x 4096 on 128 x 32
+// 15, 128 x 64 20; 256 x 11008 x 4096 on 128 x 64 31, 128 x 32 36; 2048 x 11008 x
+// 4096 on 256 x 128 150, 256 x 256 169; 4096 x 8192 x 8192 on 256 x 256 374, 256 x
+// 128 433.  Microscaled: 128 x 4096 x 4096 on 128 x 32 10.5, 128 x 64 12.9; 512 x
+// 4096 x 4096 on 128 x 64 13.8, 128 x 128 16.1; 2048 x 4096 x 4096 on 128 x 128
+// 28, 256 x 256 32; 4096 x 12288 x 12288 on 256 x 256 286, 128 x 128 391.  128 x
+// 128 tiles of 16-bit X and 256 x 128 of microscaled X were the fastest of no size
+// by more than a tenth: they are not built.
+struct TileShape {
+  Kind kind;
+  int bm, bn, per_cu;
+  double launch, one, full;
+};
+constexpr TileShape kTileShapes[] = {
+    {kTile128x32, 128, 32, 2, 3.3, 0.74, 1.3},
+    {kTile128x64, 128, 64, 2, 3.5, 1.3, 2.2},
+    {kTile256x128, 256, 128, 2, 9.2, 3.5, 6.2},
+    {kTile256x256, 256, 256, 1, 5.2, 5.4, 5.4},
+};
+constexpr TileShape kScaledTileShapes[] = {
+    {kTile128x32, 128, 32, 2, 3.0, 0.46, 0.81},
+    {kTile128x64, 128, 64, 2, 2.9, 0.67, 1.0},
+    {kTile128x128, 128, 128, 1, 3.9, 0.65, 0.65},
+    {kTile256x256, 256, 256, 1, 6.8, 1.6, 1.6},
+};
+Plan tile_plan(const TileShape (&shapes)[4], int64_t m, int64_t n, int64_t rows) {
+  constexpr double kJoin = 4.3, kJoinBytes = 0.22e-6;
+  constexpr int kMaxSplits = 16;
+  Plan best{kTile128x32, 1};
+  double least = std::numeric_limits<double>::infinity();
+  const double parts = (double)m * (double)rows * 8.0;       // bytes that a split's sums move
+  for (const TileShape& s : shapes) {
+    const int64_t tiles = ceil_div(m, s.bm) * ceil_div(rows, s.bn), held = 256 * s.per_cu;
+    for (int splits = 1; splits <= kMaxSplits && (splits == 1 || n >= (int64_t)splits * kSplitCols); ++splits) {
+      const int64_t groups = tiles * splits, rest = groups % held;
+      double t = (double)(groups / held) * s.full;
+      if (rest > 256) t += s.one + (s.full - s.one) * std::sqrt((double)(rest - 256) * (1.0 / 256));
+      else if (rest > 0) t += s.one;
+      t = s.launch + t * (double)ceil_div(ceil_div(n, splits), kSplitCols);
+      if (splits > 1) t += kJoin + kJoinBytes * splits * parts;
+      if (t < least) least = t, best = Plan{s.kind, splits};
+      if (groups > 2 * held) break;          // more splits only add sums
+    }
   }
-  const Kind kinds[3] = {kTile128x128, kTile128x64, kTile128x32};
-  const int widths[3] = {128, 64, 32};
-  for (int i = 0; i < 3; ++i) {
-    const int64_t t = tiles(128, widths[i]);
-    if (i < 2 && (t * std::max<int64_t>(1, n / 1024) < 256 || rows <= widths[i] / 2)) continue;
-    const int64_t most = std::max<int64_t>(1, n / kMinSplitCols);
-    const int64_t splits = t >= 256 ? 1 : std::max<int64_t>(1, (kWantTiles + t / 2) / t);
-    return Plan{kinds[i], (int)std::min(splits, most)};
-  }
-  return Plan{kTile128x32, 1};
+  return best;
 }
 
+// The row kernels, whose waves split the columns, take products small enough for
+// their operands to come through L2 (32 x 4096 x 4096: 9.3 against 10.6 us on
+// tiles; 64 x 4096 x 4096: 15 against 11.6; 1 x 4096 x 11008: 9.0 against 11.4;
+// 4 x 11008 x 4096: 11.5 against 10.6).  Their waves load X's rows in pieces:
+// rows of odd lengths slow them down (2 x 4099 x 11007: 21 against 15.6; 8 x 130
+// x 1001 still 5.6 against 7.6).  Microscaled X, which is smaller, stays on them
+// longer (64 x 4096 x 4096: 8.0 against 10.3; 128 x 4096 x 4096: 12.5 against
+// 10.5; 8 x 11008 x 4096: 8.6 against 9.8; 32 x 11008 x 4096: 13.6 against 10.3).
+// Long matrices with up to four rows of 16-bit X take the stream kernel (1 x
+// 28672 x 8192: 24 against 30 on tiles; 1 x 12288 x 12288: 27 against 20).
 Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool mx) {
   if (grouped) {
     // By the rows an expert has on average; the workgroups of an expert without
-    // rows do not exist.
+    // rows do not exist.  64 experts of 1024 x 2048 with 2 rows each: 18 us on the
+    // row kernel, 20 on tiles; 8 of 11008 x 4096 with 4: 47 and 40, with 128 on
+    // 128 x 32 143 and on 256 x 128 147, with 256 257 and 239.
     const int64_t each = rows / experts;
     if (rows <= 4) return Plan{kRows1, 1};
-    if (each <= 8) return Plan{kRows2, 1};
-    if (each <= 32) return Plan{kTile128x32, 1};
-    if (each <= 96) return Plan{kTile128x64, 1};
-    return Plan{kTile256x128, 1};
+    if (each < 4) return Plan{kRows2, 1};
+    return Plan{each <= 128 ? kTile128x32 : kTile256x128, 1};
   }
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
+  const bool small = m * n <= ((int64_t)1 << 24);
   if (mx) {
-    if (products > 1100000000) return tile_plan(m, n, rows, true);
-    if (outputs <= 65536) return Plan{kRows1, 1};
+    if (small ? products > 1070000000 : products > 500000000) return tile_plan(kScaledTileShapes, m, n, rows);
+    if (outputs <= 65536 || !small) return Plan{kRows1, 1};
     return Plan{rows <= 32 ? kRows2 : kRows2x2, 1};
   }
-  if (m >= 24576 && rows <= 16) return Plan{rows <= 4 ? kStream1x4 : m < 40960 ? kStream1 : kStream3, 1};
-  if (products > 2200000000) return tile_plan(m, n, rows, false);
-  if (outputs <= 65536) return Plan{kRows1, 1};
-  if (rows <= 4) return Plan{kRows2, 1};
-  if (rows <= 16) return Plan{kRows4, 1};
-  if (rows <= 32) return Plan{outputs <= 131072 ? kRows2 : kRows4x2, 1};
-  return Plan{outputs <= 262144 ? kRows4 : kRows4x2, 1};
+  if (m >= 24576 && rows <= kStreamRows) return Plan{kStream, 1};
+  if (rows == 1 || n % 4 == 0 || products <= 50000000) {
+    if (small ? outputs <= 65536 : products <= 150000000) return Plan{kRows1, 1};
+    if (small && outputs <= 131072) return Plan{kRows2, 1};
+  }
+  return tile_plan(kTileShapes, m, n, rows);
 }
 
 // Workspace of a plan: the splits' sums.
@@ -1558,13 +1595,22 @@ bool aligned_w(const MxOperands& p) {
   return ((reinterpret_cast<uintptr_t>(p.W) | (uint64_t)(p.ldp * 4) | (uint64_t)(p.w_stride * 4)) & 15) == 0;
 }
 
-template <int XT, int WR, int WC, int RB, int CB, int PB>
+template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT, bool WL>
+gptq_status launch_tile(const MxOperands& p, const Plan& pl, void* ws, hipStream_t st) {
+  return run_tiles(mx_tile_kernel<XT, WR, WC, RB, CB, PB, DIRECT, WL>, 32 * WR * RB, 32 * WC * CB, 64 * WR * WC,
+                   tile_lds<XT, WR, WC, RB, CB, PB, WL>(), p, pl, ws, st);
+}
+
+// WL: the shape stages the codes of W in LDS where their rows allow it.
+template <int XT, int WR, int WC, int RB, int CB, int PB, bool WL>
 gptq_status launch_tiles(const MxOperands& p, const Plan& pl, void* ws, hipStream_t st) {
-  // By registers, a stage of the large tiles is one panel: they have to hold it.
-  constexpr int PR = RB * CB > 4 ? 1 : PB;
-  const bool direct = aligned_x<XT>(p) && (XT != kMx || aligned_w(p));
-  auto* k = direct ? mx_tile_kernel<XT, WR, WC, RB, CB, PB, true> : mx_tile_kernel<XT, WR, WC, RB, CB, PR, false>;
-  return run_tiles(k, 32 * WR * RB, 32 * WC * CB, 64 * WR * WC, tile_lds<XT, WR, WC, RB, CB, PB>(), p, pl, ws, st);
+  const bool x = aligned_x<XT>(p), w = aligned_w(p);
+  if constexpr (WL) {
+    if (w && x) return launch_tile<XT, WR, WC, RB, CB, PB, true, true>(p, pl, ws, st);
+    if (w) return launch_tile<XT, WR, WC, RB, CB, PB, false, true>(p, pl, ws, st);
+  }
+  if (x && (w || XT != kMx)) return launch_tile<XT, WR, WC, RB, CB, PB, true, false>(p, pl, ws, st);
+  return launch_tile<XT, WR, WC, RB, CB, PB, false, false>(p, pl, ws, st);
 }
 
 template <int XT, int WR, int WC, int RB, int CB, int SP>
@@ -1583,11 +1629,11 @@ gptq_status launch_rows(const MxOperands& p, int waves, hipStream_t st) {
   return GPTQ_OK;
 }
 
-template <int XT, int RT, int NT, int XR>
+template <int XT>
 gptq_status launch_stream(const MxOperands& p, hipStream_t st) {
-  const int64_t grid = ceil_div(p.m, 64 * RT) * max_tiles(p.rows, p.experts, p.offsets != nullptr, 16 * NT);
+  const int64_t grid = ceil_div(p.m, 64);
   if (grid > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  mx_stream_kernel<XT, RT, NT, XR><<<(unsigned)grid, 256, 2 * 64 * XR * 16, st>>>(p);
+  mx_stream_kernel<XT><<<(unsigned)grid, 256, 0, st>>>(p);
   GPTQ_TRY_LAUNCH();
   return GPTQ_OK;
 }
@@ -1601,31 +1647,33 @@ gptq_status launch(const MxOperands& p, void* ws, size_t ws_bytes, hipStream_t s
     pl = Plan{kRows2, 1};
   const size_t need = plan_ws(pl, p.m, p.rows);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return GPTQ_ERR_WORKSPACE;
-  constexpr int P2 = XT == kMx ? 1 : 2, P4 = XT == kMx ? 1 : 4;        // panels per stage
-  if constexpr (XT != kMx) {
+  constexpr bool MX = XT == kMx;
+  constexpr int P2 = MX ? 1 : 2, P4 = MX ? 1 : 4;            // panels per stage
+  if constexpr (!MX) {
     if (aligned_x<XT>(p) && aligned_w(p)) {
       if (pl.kind == kTile256x256) return launch_big_tiles<XT, 4, 2, 2, 4, 4>(p, pl, ws, st);
       if (pl.kind == kTile256x128) return launch_big_tiles<XT, 4, 1, 2, 4, 2>(p, pl, ws, st);
     }
   }
   switch (pl.kind) {
-    case kTile256x256: return launch_tiles<XT, 4, 2, 2, 4, P2>(p, pl, ws, st);
-    case kTile256x128: return launch_tiles<XT, 4, 1, 2, 4, P2>(p, pl, ws, st);
-    case kTile128x128: return launch_tiles<XT, 4, 1, 1, 4, P2>(p, pl, ws, st);
-    case kTile128x64: return launch_tiles<XT, 4, 1, 1, 2, P4>(p, pl, ws, st);
-    case kTile128x32: return launch_tiles<XT, 4, 1, 1, 1, P4>(p, pl, ws, st);
+    // Microscaled: 128 x 64 a wave (4096 x 12288 x 12288 298 us, 310 with 64 x 128).
+    case kTile256x256:
+      if constexpr (MX) return launch_tiles<XT, 2, 4, 4, 2, P2, false>(p, pl, ws, st);
+      else return launch_tiles<XT, 4, 2, 2, 4, P2, false>(p, pl, ws, st);
+    case kTile256x128:
+      if constexpr (!MX) return launch_tiles<XT, 4, 1, 2, 4, P2, false>(p, pl, ws, st);
+      break;
+    case kTile128x128:
+      if constexpr (MX) return launch_tiles<XT, 4, 1, 1, 4, P2, false>(p, pl, ws, st);
+      break;
+    case kTile128x64: return launch_tiles<XT, 4, 1, 1, 2, P2, !MX>(p, pl, ws, st);
+    case kTile128x32: return launch_tiles<XT, 4, 1, 1, 1, P4, !MX>(p, pl, ws, st);
     case kRows1: return launch_rows<XT, 1, 1, 4>(p, 8, st);
-    case kRows4: return launch_rows<XT, 4, 1, 2>(p, 8, st);
-    case kRows2x2: return launch_rows<XT, 2, 2, 2>(p, 8, st);
-    case kRows4x2: return launch_rows<XT, 4, 2, 1>(p, 8, st);
-    case kStream1x4:
-      if constexpr (XT != kMx) return launch_stream<XT, 1, 1, 4>(p, st);
+    case kRows2x2:
+      if constexpr (MX) return launch_rows<XT, 2, 2, 2>(p, 8, st);
       break;
-    case kStream1:
-      if constexpr (XT != kMx) return launch_stream<XT, 1, 1, 16>(p, st);
-      break;
-    case kStream3:
-      if constexpr (XT != kMx) return launch_stream<XT, 3, 1, 16>(p, st);
+    case kStream:
+      if constexpr (!MX) return launch_stream<XT>(p, st);
       break;
     default: break;
   }

@@ -590,16 +590,27 @@ def test_binding_refusals(g):
 # ---------------------------------------------------------------------------
 KINDS = [
     # m, n, batch
+    (300, 520, 3), (303, 525, 3),                 # few outputs: the row kernel
+    (300, 520, 256), (303, 525, 255),             # more of them
     (24576, 1024, 1), (24600, 545, 3),            # long matrices, up to four rows of X
-    (24576, 1024, 16), (24590, 1160, 7),          # long matrices, up to sixteen
-    (40960, 1024, 16), (41000, 1160, 5),          # longer ones
-    (4100, 4160, 160), (4096, 4608, 140),         # tiles of 128 x 32, columns split
-    (8200, 4100, 70), (8192, 4096, 64),           # tiles of 128 x 64
-    (16384, 1024, 180), (16400, 1031, 135),       # tiles of 128 x 128
-    (8192, 640, 1030), (8200, 520, 1025),         # tiles of 256 x 128
-    (12288, 384, 1300), (8192, 512, 2048),        # tiles of 256 x 256
+    (24576, 1024, 16), (24590, 1160, 7),          # and more
+    (40960, 1024, 16), (41000, 1160, 5),
+    (300, 520, 512), (8195, 2041, 3),             # tiles of 128 x 32
+    (4100, 4160, 160), (4096, 4608, 140),
+    (4096, 8192, 16), (4099, 4089, 3),            # with split columns
     (4099, 11007, 77), (4000, 9000, 80),          # splits that do not divide the columns, a partial last stage
     (1100, 12000, 200), (300, 20001, 700),        # few rows of W, many splits
+    (8200, 4100, 70), (8192, 4096, 64),
+    (24576, 520, 77), (16400, 1031, 135),         # tiles of 128 x 64
+    (4096, 12288, 40), (8195, 8185, 39),          # with split columns
+    (16384, 1024, 180), (24579, 1017, 77),        # tiles of 128 x 128 (microscaled X)
+    (300, 12288, 1024), (303, 12281, 1023),       # with split columns
+    (8192, 640, 1030), (8200, 520, 1025),
+    (4096, 2048, 2048), (16387, 525, 799),        # tiles of 256 x 128
+    (5500, 7168, 800), (5503, 7161, 799),         # with split columns
+    (12288, 384, 1300), (8192, 512, 2048),
+    (24576, 520, 400), (24579, 525, 511),         # tiles of 256 x 256
+    (5000, 10000, 800), (3003, 5993, 1499),       # with split columns
 ]
 
 
@@ -625,7 +636,8 @@ def test_every_kernel_kind(g, m, n, batch, dtype):
 
 
 @pytest.mark.parametrize("m,n,batch", [(24580, 700, 4), (24580, 700, 12), (4100, 4160, 160), (8200, 520, 1025),
-                                       (8192, 576, 2048)])
+                                       (8192, 576, 2048), (4096, 8192, 16), (24576, 520, 77), (5503, 7161, 799),
+                                       (24576, 512, 400), (4096, 2048, 2048)])
 def test_float16_scales_out_of_range_in_every_kernel_kind(g, m, n, batch):
     # One block of one row far outside float16's exact range.
     import torch
@@ -665,7 +677,7 @@ def test_workspace_given_too_small_and_shared(g):
     import torch
     from post_weight_quantization_11_amd import _lib
     rng = _rng(71)
-    m, n, batch = 4096, 4608, 140
+    m, n, batch = 1100, 12000, 200
     need = _lib.load().gptq_mx_gemm_ws_bytes(m, n, batch, 1)
     assert need > 0
     codes, scale = _weights(rng, m, n)
@@ -678,7 +690,7 @@ def test_workspace_given_too_small_and_shared(g):
         g.gptq_mx_gemm(packed, scales, X, ws=ws[:1024])
 
 
-@pytest.mark.parametrize("m,n,batch", [(4096, 4608, 140), (8192, 512, 2048), (24576, 640, 12)])
+@pytest.mark.parametrize("m,n,batch", [(1100, 12000, 200), (8192, 512, 2048), (24576, 640, 12), (24576, 640, 3)])
 def test_graph_of_every_launch_shape(g, m, n, batch):
     """Split columns (their workspace comes from the graph's pool), tiles with
     more LDS than a launch has by default, and streamed X, captured and
@@ -767,7 +779,7 @@ def test_two_streams_at_once(g):
     """Calls that need a workspace on two streams at the same time."""
     import torch
     rng = _rng(97)
-    m, n, batch = 4096, 4608, 140
+    m, n, batch = 1100, 12000, 200
     jobs = []
     for k in range(2):
         codes, scale = _weights(rng, m, n)

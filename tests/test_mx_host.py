@@ -138,7 +138,7 @@ def test_workspace_query(lib):
 
 def test_missing_workspace_is_refused_before_any_launch(lib):
     # Sizes whose columns are split need the queried workspace.
-    m, n, batch = 4096, 4608, 140
+    m, n, batch = 1100, 12000, 200
     need = lib.gptq_mx_gemm_ws_bytes(m, n, batch, 1)
     assert need > 0
     base = dict(GEMM, m=m, n=n, ldp=n // 8, lds=n // 32, batch=batch, ldx=n, ldy=m)
