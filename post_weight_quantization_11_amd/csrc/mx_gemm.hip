@@ -762,11 +762,15 @@ __device__ inline void store_tile(const MxOperands& p, const TileGrid& tg, const
 // with SPLIT: trained weights have no such scales, and a branch on them in the
 // main loop made the compiler move the accumulators.
 //
-// Pipeline: a step's operands are read from LDS while the step before it
-// multiplies.  The one barrier of a stage stands in its last step, between the
-// two halves of that step's products: every wave then holds the step's
-// operands, so the other buffer is complete (its loads were waited for) and
-// this one is free, and the next stage's first reads overlap the second half.
+// Pipeline, 16-bit X: a step's operands are read from LDS while the step before
+// it multiplies.  The one barrier of a stage stands in its last step, between the
+// two halves of that step's products: every wave then holds the step's operands,
+// so the other buffer is complete (its loads were waited for) and this one is
+// free, and the next stage's first reads overlap the second half.
+// Microscaled X, whose steps take half as long: operands are read two steps
+// ahead, so the barrier stands in the middle of the stage, and behind it the
+// stage after the next is fetched (512 x 4096 x 11008 36 -> 32 us, 256 x 12288 x
+// 12288 47 -> 42; the 256 x 256 tiles, at half the matrix cores' rate, lose 1%).
 template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT, bool WL, bool SPLIT>
 __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, const TokenTile& tile, int r0, int split,
                                     unsigned char* smem) {
@@ -997,7 +1001,7 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
   struct Frags {
     u32x4 x[CB], w[MX ? RB : 1];
   };
-  Frags f[2];
+  Frags f[MX ? 4 : 2];
   // This lane's address of chunk j in the wave's first X row block (and, the
   // constant w_off further, its first W row block).
   uint32_t frag_at[4];
@@ -1069,7 +1073,59 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
   };
 
   // Whole stages first; a partial one at the rows' end is staged alone.
-  if (s_lo < s_whole) {
+  if constexpr (MX) {
+    if (s_lo < s_whole) {
+      // The last stages fetch the last one again, into buffers no one reads any
+      // more: no branch around the loads.
+      auto stage = [&](int st, int buf) {
+        if constexpr (DIRECT) {
+#pragma unroll
+          for (int i = 0; i < kDirect; ++i) fetch_direct(min(st, s_whole - 1), buf, i);
+        } else {
+          fetch(min(st, s_whole - 1));
+        }
+      };
+      stage(s_lo, 0);
+      if constexpr (!DIRECT) put(0);
+      stage(s_lo + 1, 1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        fetch_scales(0, q);
+        put_scales(0, q);
+      }
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      lds_barrier();
+      load_frags(0, 0, f[0]);
+      load_frags(0, 1, f[1]);
+      read_regs(s_lo, 0, cur);
+      fetch_scales(1, 0);
+      for (int st = s_lo; st < s_whole; ++st) {
+        const int buf = (st - s_lo) & 1;
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+          load_frags(buf, step + 2, f[step + 2]);
+          products(step, f[step], cur, 0, RB);
+          interleave(RB * CB);
+        }
+        if constexpr (!DIRECT) put(buf ^ 1);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        put_scales(((st - s_lo) >> 2) + 1, (st - s_lo) & 3);
+        lds_barrier();
+        stage(st + 2, buf);
+        fetch_scales(((st + 1 - s_lo) >> 2) + 1, (st + 1 - s_lo) & 3);
+        __builtin_amdgcn_sched_barrier(0);   // the loads are issued before the products
+        read_regs(min(st + 1, s_whole - 1), buf ^ 1, nxt);
+#pragma unroll
+        for (int step = 2; step < 4; ++step) {
+          load_frags(buf ^ 1, step - 2, f[step - 2]);
+          products(step, f[step], cur, 0, RB);
+          interleave(RB * CB);
+        }
+        cur = nxt;
+      }
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));   // none is left in flight to the buffers
+    }
+  } else if (s_lo < s_whole) {
     if constexpr (DIRECT) {
 #pragma unroll
       for (int i = 0; i < kDirect; ++i) fetch_direct(s_lo, 0, i);
@@ -1079,13 +1135,6 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
     }
     fetch_codes(s_lo, 0);
     fetch_regs(s_lo, cur);
-    if constexpr (MX) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        fetch_scales(0, q);
-        put_scales(0, q);
-      }
-    }
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     lds_barrier();
     load_frags(0, 0, f[0]);
@@ -1103,9 +1152,6 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
       }
       fetch_codes(next, buf ^ 1);
       fetch_regs(next, nxt);
-      if constexpr (MX) {
-        fetch_scales(((st - s_lo) >> 2) + 1, (st - s_lo) & 3);
-      }
       __builtin_amdgcn_sched_barrier(0);     // the loads are issued before the products
       check_scales(cur);
 #pragma unroll
@@ -1118,9 +1164,6 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
       interleave(RB / 2 * CB);
       if constexpr (!DIRECT) put(buf ^ 1);
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-      if constexpr (MX) {
-        put_scales(((st - s_lo) >> 2) + 1, (st - s_lo) & 3);
-      }
       lds_barrier();
       load_frags(buf ^ 1, 0, f[0]);
       read_regs(next, buf ^ 1, nxt);
