@@ -323,7 +323,10 @@ __device__ inline void multiply_unit(const Unit<XT, RT, NT>& u, const uint32_t (
 // of X rows, take every KW-th quad of units (512 columns), and add their sums
 // through LDS in wave order.  X comes straight from memory.  D units are in
 // flight per wave; a row's sixteen scale bytes of a quad are one load, a quad
-// ahead (one byte a lane and unit cost 30 of 88 us at 49152 x 12288).  Returns
+// ahead (one byte a lane and unit cost 30 of 88 us at 49152 x 12288).  Bound by
+// latency at the sizes it is chosen for: 1 x 4096 x 4096 5.6 us (8.9 MB, of which
+// launch and two dependent loads are 4), 64 experts' 16 x 1024 x 2048 7.2 us (the
+// tile search reads the offsets first).  Returns
 // false, with nothing stored, if a float16 workgroup met scales that are not
 // exact in float16 (the caller then runs it again with SPLIT).
 template <int XT, int RT, int NT, int D, bool SPLIT>
@@ -588,11 +591,22 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxOperands p) {
 // cover all 64 banks (with c ^ r % 8 alone rows r and r + 8 share theirs, which
 // doubled the cycles LDS was busy).
 //
-// 16-bit X: the codes of W go from memory straight into registers (a row's 32
-// codes of a block are 16 bytes: 1/4 of what X needs) and become operands
-// there; of a panel's two blocks, lane half h takes block h, and step j the
-// codes 8j .. 8j+7 of both.  Microscaled X: W's codes are staged in LDS like
-// X's; step j takes blocks 2j + h.
+// 16-bit X: the codes of W (a row's 32 codes of a block are 16 bytes: 1/4 of what
+// X needs) become operands in the registers of the lanes that use them, loaded
+// there or staged in LDS first; of a panel's two blocks, lane half h takes block
+// h, and step j the codes 8j .. 8j+7 of both.  Microscaled X: W's codes are staged
+// in LDS like X's; step j takes blocks 2j + h.
+//
+// Measured: 16 x 49152 x 12288 80 us (128 x 32; 324 MB, 4.1 TB/s: bound by W's
+// bytes, 384 workgroups on 256 CUs), 77 x 4099 x 11007 20 us (five splits: a
+// chain of 9 stages, 16 us, and the join, 4), 64 experts' 1531 x 1030 x 2044 32 us
+// (84 MB: eight stages a workgroup, first loads and the stores), 2048 x 11008 x
+// 4096 148 us (256 x 128; 1.24 PFLOP/s), 4096 x 8192 x 8192 374 us (256 x 256;
+// 1.47 PFLOP/s, the matrix cores 81% busy at 1.7 GHz: power).  Microscaled: 4096 x
+// 12288 x 12288 290 us (4.3 PFLOP/s, the matrix cores 50% busy at 1.95 GHz; with
+// the loads from memory taken out 275: LDS reads, six 16-byte ones a lane for
+// eight products, and the products do not overlap fully.  Four waves of 128 x 128
+// read a third less but took 306, one wave a SIMD).
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -753,10 +767,8 @@ __device__ inline void store_tile(const MxOperands& p, const TileGrid& tg, const
 // aligned rows; whole stages of X (and microscaled W) go from memory to LDS
 // without passing through registers.  WL (16-bit X, 16-byte aligned rows of W):
 // so do W's codes, 32 PB bytes of a row at a time, where the lanes that use them
-// would load 32 (64 x 11008 x 4096 on 128 x 32 tiles 23 -> 14.5 us; not for 128 x
-// 128, where the LDS costs a workgroup a CU: 64 experts' 1531 x 1024 x 2048 50 ->
-// 65 us).  SPLIT (float16 X): every product as two
-// bfloat16 ones.  Without SPLIT a float16 tile runs as if all its scales were
+// would load 32 (64 x 11008 x 4096 on 128 x 32 tiles 20 -> 14.5 us).  SPLIT (float16
+// X): every product as two bfloat16 ones.  Without SPLIT a float16 tile runs as if all its scales were
 // exact in float16 and says at the end whether they were (the same answer in
 // the whole workgroup); if not, nothing is stored and the caller runs it again
 // with SPLIT: trained weights have no such scales, and a branch on them in the

@@ -15,7 +15,9 @@
 // threads a block; the block maximum is an integer maximum of the absolute
 // bit patterns (monotonic in |w|, with infinities and NaN above every finite
 // pattern), two steps across the four lanes.  Reads, packed words and Wq are
-// contiguous over a wave.
+// contiguous over a wave.  Bound by memory: 49152 x 12288 float16 with Wq 436 us
+// for 2.74 GB (6.3 TB/s), without Wq 279 us for 1.53 GB (5.5 TB/s); 256 x 256
+// float32 2.8 us, a launch.
 #include "mx.h"
 
 namespace gptq {
