@@ -796,3 +796,19 @@ def test_two_streams_at_once(g):
     for k, job in enumerate(jobs):
         for Y in out[k]:
             assert torch.equal(Y, job[3])
+
+
+@pytest.mark.parametrize("m,batch", [(4, 3), (4096, 512), (24576, 2), (8192, 4096)])
+def test_no_columns_in_every_kernel_kind(g, m, batch):
+    import torch
+    packed = torch.empty((m, 0), dtype=torch.int32, device="cuda")
+    scales = torch.empty((m, 0), dtype=torch.uint8, device="cuda")
+    for dtype in (torch.float16, torch.bfloat16):
+        X = torch.empty((batch, 0), dtype=dtype, device="cuda")
+        Y = torch.full((batch, m), 7.0, device="cuda")
+        g.gptq_mx_gemm(packed, scales, X, Y=Y)
+        assert not Y.any()
+    Y = torch.full((batch, m), 7.0, device="cuda")
+    g.gptq_mx_scaled_gemm(packed, scales, packed[:1].expand(batch, 0).contiguous(),
+                          scales[:1].expand(batch, 0).contiguous(), 0, Y=Y)
+    assert not Y.any()
