@@ -1557,15 +1557,24 @@ constexpr TileShape kScaledTileShapes[] = {
     {kTile128x128, 128, 128, 1, 3.9, 0.65, 0.65},
     {kTile256x256, 256, 256, 1, 6.8, 1.6, 1.6},
 };
-Plan tile_plan(const TileShape (&shapes)[4], int64_t m, int64_t n, int64_t rows) {
+// Grouped by expert: half a tile more for every expert that can have rows, and no
+// splits.  64 experts of 1024 x 2048 with 64 rows each on 128 x 32 37 us, 256 x 128
+// 50, with 256 101 and 85; 8 of 11008 x 4096 with 128 143 and 147, with 256 257 and
+// 239; 28 of 120 x 10624 with 196 46 and 127 (57
+// workgroups); 8 of 4096 x 4096 with 375 139 and 106.  128 x 64 tiles were
+// the fastest of no size by a tenth.
+constexpr TileShape kGroupedTileShapes[] = {kTileShapes[0], kTileShapes[2]};
+template <size_t N>
+Plan tile_plan(const TileShape (&shapes)[N], int64_t m, int64_t n, int64_t rows, int64_t experts = 0) {
   constexpr double kJoin = 4.3, kJoinBytes = 0.22e-6;
-  constexpr int kMaxSplits = 16;
+  const int max_splits = experts > 0 ? 1 : 16;
   Plan best{kTile128x32, 1};
   double least = std::numeric_limits<double>::infinity();
   const double parts = (double)m * (double)rows * 8.0;       // bytes that a split's sums move
   for (const TileShape& s : shapes) {
-    const int64_t tiles = ceil_div(m, s.bm) * ceil_div(rows, s.bn), held = 256 * s.per_cu;
-    for (int splits = 1; splits <= kMaxSplits && (splits == 1 || n >= (int64_t)splits * kSplitCols); ++splits) {
+    const int64_t partial = (std::min(experts, rows) + 1) / 2, held = 256 * s.per_cu;
+    const int64_t tiles = ceil_div(m, s.bm) * (ceil_div(rows, s.bn) + partial);
+    for (int splits = 1; splits <= max_splits && (splits == 1 || n >= (int64_t)splits * kSplitCols); ++splits) {
       const int64_t groups = tiles * splits, rest = groups % held;
       double t = (double)(groups / held) * s.full;
       if (rest > 256) t += s.one + (s.full - s.one) * std::sqrt((double)(rest - 256) * (1.0 / 256));
@@ -1593,12 +1602,10 @@ Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped
   if (grouped) {
     // By the rows an expert has on average; the workgroups of an expert without
     // rows do not exist.  64 experts of 1024 x 2048 with 2 rows each: 18 us on the
-    // row kernel, 20 on tiles; 8 of 11008 x 4096 with 4: 47 and 40, with 128 on
-    // 128 x 32 143 and on 256 x 128 147, with 256 257 and 239.
-    const int64_t each = rows / experts;
+    // row kernel, 20 on tiles; 8 of 11008 x 4096 with 4: 47 and 40.
     if (rows <= 4) return Plan{kRows1, 1};
-    if (each < 4) return Plan{kRows2, 1};
-    return Plan{each <= 128 ? kTile128x32 : kTile256x128, 1};
+    if (rows / experts < 4) return Plan{kRows2, 1};
+    return tile_plan(kGroupedTileShapes, m, n, rows, experts);
   }
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
   const bool small = m * n <= ((int64_t)1 << 24);

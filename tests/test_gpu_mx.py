@@ -673,6 +673,31 @@ def test_grouped_kernel_kinds(g, each):
         _check(Y, want, mags, n, "f32", f"grouped, {each} rows an expert, {dtype}")
 
 
+@pytest.mark.parametrize("m,n", [(4096, 2048), (4099, 2056), (4090, 2061)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_grouped_large_tiles(g, m, n, dtype):
+    import torch
+    rng = _rng(101, m, n)
+    E, rows = 4, 3000
+    off = [2, 2, 1100, 1101, 2990]
+    codes, scale = _weights(rng, E * m, n)
+    if dtype == "f16":
+        scale[2 * m + 7, 3] = 200                                         # far outside float16's exact range
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((rows, n)), dtype)
+    Y = torch.full((rows, m), 7.0, device="cuda")
+    g.gptq_mx_gemm_grouped(packed.view(E, m, -1), scales.view(E, m, -1), X,
+                           torch.tensor(off, dtype=torch.int32, device="cuda"), Y=Y)
+    assert bool((Y[:2] == 7).all()) and bool((Y[2990:] == 7).all())
+    pick = np.r_[0, 7, m - 1, rng.permutation(m)[:60]]
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        if lo == hi:
+            continue
+        want, mags = oracle.mx_matmul(codes[e * m + pick], scale[e * m + pick], X64[lo:hi])
+        _check(Y[lo:hi][:, torch.from_numpy(pick).cuda()], want, mags, n, "f32", f"expert {e} of {m}x{n} {dtype}")
+
+
 def test_workspace_given_too_small_and_shared(g):
     import torch
     from post_weight_quantization_11_amd import _lib
