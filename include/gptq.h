@@ -444,11 +444,12 @@ gptq_status gptq_mx_quantize(const void* W, int w_dtype, int64_t m, int64_t n, i
  *           `stream` is done: calls that may run at the same time (two streams,
  *           two captured graphs) need one each.
  * Products are exact in float32 and accumulation is float32, in an order that
- * depends on the sizes alone (the same call gives the same bits): the error
+ * depends on sizes, strides and alignment alone (the same call gives the same
+ * bits): the error
  * before the one rounding to y_dtype is at most (n/32 + 80) 2^-23
  * sum_k |What[r, k] X[b, k]|, unless that sum passes float32's range.  A weight
- * value outside float32's range counts as infinite.  Non-finite weights or X make the outputs that they enter
- * non-finite.  With n = 0, Y is 0. */
+ * value outside float32's range counts as infinite.  Non-finite weights or X
+ * make the outputs that they enter non-finite.  With n = 0, Y is 0. */
 size_t gptq_mx_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, int64_t experts);
 gptq_status gptq_mx_gemm(const uint32_t* packed, int64_t m, int64_t n, int64_t ld_packed,
                          const uint8_t* scales, int64_t ld_scales, const void* X, int x_dtype,

@@ -70,7 +70,7 @@ struct TokenTile {
 __device__ inline TokenTile find_tile(const MxOperands& p, int slot, int tile) {
   if (p.offsets == nullptr) return TokenTile{0, slot * tile, min(p.rows, (slot + 1) * tile), true};
   const int lane = (int)threadIdx.x & 63;
-  int before = 0;                            // tiles of the experts before this round's
+  int before = 0;                            // tiles of the experts before these 64
   for (int e0 = 0; e0 < p.experts; e0 += 64) {
     const int e = e0 + lane;
     int lo = 0, hi = 0;
