@@ -1475,10 +1475,13 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void mx_big_tile_kernel(MxOperands
 }
 
 // Adds the splits' sums in order, four columns a thread and four splits' loads
-// in flight (one at a time they cost a memory latency a split).  Rows that
-// belong to no expert stay.
-__global__ __launch_bounds__(256) void mx_join_kernel(MxOperands p, TileGrid tg) {
-  const int x = (int)blockIdx.y, r = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4;
+// in flight (one at a time they cost a memory latency a split).  All workgroups
+// lie along x, a row of X after the other: there can be more rows than a grid
+// has along y (65535).  Rows that belong to no expert stay.
+constexpr int kJoinCols = 1024;              // columns of Y a workgroup
+__global__ __launch_bounds__(kJoinCols / 4) void mx_join_kernel(MxOperands p, TileGrid tg) {
+  const int chunks = (p.m + kJoinCols - 1) / kJoinCols;
+  const int x = (int)(blockIdx.x / chunks), r = (int)(blockIdx.x % chunks) * kJoinCols + (int)threadIdx.x * 4;
   if (r >= p.m) return;
   if (p.offsets != nullptr) {
     const int lo = min(max(p.offsets[0], 0), p.rows), hi = min(max(p.offsets[p.experts], 0), p.rows);
@@ -1642,7 +1645,7 @@ gptq_status run_tiles(void (*k)(MxOperands, TileGrid), int BM, int BN, int threa
   k<<<(unsigned)round_up(items, kXcds), threads, lds, st>>>(p, tg);
   GPTQ_TRY_LAUNCH();
   if (tg.splits > 1) {
-    mx_join_kernel<<<dim3((unsigned)ceil_div(p.m, 1024), (unsigned)p.rows), 256, 0, st>>>(p, tg);
+    mx_join_kernel<<<(unsigned)(ceil_div(p.m, kJoinCols) * p.rows), kJoinCols / 4, 0, st>>>(p, tg);
     GPTQ_TRY_LAUNCH();
   }
   return GPTQ_OK;

@@ -1,0 +1,118 @@
+"""Records what the library's entry points would launch, without a GPU.
+
+A child process loads a small library that defines the HIP runtime calls of a
+kernel launch, then libgptq.so, whose calls bind to those definitions: nothing
+reaches a device and no pointer is followed.  Each launch is reported with its
+kernel's name and template arguments, its grid, its workgroup and its LDS.
+"""
+import ctypes
+import json
+import os
+import re
+import subprocess
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+SOURCE = r"""
+#include <stddef.h>
+#include <stdio.h>
+
+typedef struct { unsigned x, y, z; } dim3;
+static dim3 s_grid, s_block;
+static size_t s_lds;
+static void* s_stream;
+static struct { const void* f; const char* name; } s_names[4096];
+static int s_count;
+static FILE* s_out;
+
+void recorder_open(const char* path) { s_out = fopen(path, "w"); }
+void recorder_mark(int call, int rc) { fprintf(s_out, "call %d %d\n", call, rc); fflush(s_out); }
+
+void** __hipRegisterFatBinary(const void* data) { static void* module; (void)data; return &module; }
+void __hipUnregisterFatBinary(void** m) { (void)m; }
+void __hipRegisterFunction(void** m, const void* f, char* d, const char* name, unsigned t, void* a, void* b, void* c,
+                           void* e, int* w) {
+  (void)m; (void)d; (void)t; (void)a; (void)b; (void)c; (void)e; (void)w;
+  if (s_count < 4096) { s_names[s_count].f = f; s_names[s_count++].name = name; }
+}
+void __hipRegisterVar(void** m, void* v, char* h, char* d, int e, size_t s, int c, int g) {
+  (void)m; (void)v; (void)h; (void)d; (void)e; (void)s; (void)c; (void)g;
+}
+int __hipPushCallConfiguration(dim3 g, dim3 b, size_t lds, void* st) {
+  s_grid = g; s_block = b; s_lds = lds; s_stream = st;
+  return 0;
+}
+int __hipPopCallConfiguration(dim3* g, dim3* b, size_t* lds, void** st) {
+  *g = s_grid; *b = s_block; *lds = s_lds; *st = s_stream;
+  return 0;
+}
+int hipLaunchKernel(const void* f, dim3 g, dim3 b, void** args, size_t lds, void* st) {
+  const char* name = "?";
+  (void)args; (void)st;
+  for (int i = 0; i < s_count; ++i)
+    if (s_names[i].f == f) name = s_names[i].name;
+  fprintf(s_out, "launch %s %u %u %u %u %u %u %zu\n", name, g.x, g.y, g.z, b.x, b.y, b.z, lds);
+  return 0;
+}
+int hipGetLastError(void) { return 0; }
+int hipFuncSetAttribute(const void* f, int attr, int v) { (void)f; (void)attr; (void)v; return 0; }
+"""
+
+TEMPLATE = re.compile(r"_ZN\w*?\d+(mx_\w+?_kernel)(?:I((?:L[ib]\d+E)+)E)?E")
+
+
+def _kernel(mangled):
+    """(name, template arguments as integers) of a mangled kernel name."""
+    m = TEMPLATE.match(mangled)
+    if not m:
+        return mangled, ()
+    return m.group(1), tuple(int(v) for v in re.findall(r"L[ib](\d+)E", m.group(2) or ""))
+
+
+def build(folder):
+    src, so = os.path.join(folder, "recorder.c"), os.path.join(folder, "recorder.so")
+    with open(src, "w") as f:
+        f.write(SOURCE)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O1", "-o", so, src], check=True)
+    return so
+
+
+def record(so, calls):
+    """calls: [(entry point, its arguments: whole numbers, None for a null
+    pointer)].  Returns [(status, [launch])], a launch being a dict of kernel,
+    args, grid, block, lds."""
+    folder = os.path.dirname(so)
+    todo, done = os.path.join(folder, "calls.json"), os.path.join(folder, "launches.txt")
+    with open(todo, "w") as f:
+        json.dump(calls, f)
+    subprocess.run([sys.executable, os.path.abspath(__file__), so, todo, done], check=True, cwd=ROOT)
+    out, pending = [], []
+    with open(done) as f:
+        for line in f:
+            w = line.split()
+            if w[0] == "call":
+                out.append((int(w[2]), pending))
+                pending = []
+            else:
+                kernel, args = _kernel(w[1])
+                g = [int(v) for v in w[2:9]]
+                pending.append(dict(kernel=kernel, args=args, grid=tuple(g[:3]), block=tuple(g[3:6]), lds=g[6]))
+    assert len(out) == len(calls)
+    return out
+
+
+def _child(so, todo, done):
+    sys.path.insert(0, ROOT)
+    rec = ctypes.CDLL(so, mode=ctypes.RTLD_GLOBAL)     # before the library: its calls bind to these definitions
+    rec.recorder_open(done.encode())
+    from post_weight_quantization_11_amd import _lib
+    lib = _lib.load()
+    with open(todo) as f:
+        calls = json.load(f)
+    for i, (name, args) in enumerate(calls):
+        rec.recorder_mark(i, getattr(lib, name)(*args))
+
+
+if __name__ == "__main__":
+    _child(*sys.argv[1:4])

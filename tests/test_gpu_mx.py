@@ -837,3 +837,29 @@ def test_no_columns_in_every_kernel_kind(g, m, batch):
     g.gptq_mx_scaled_gemm(packed, scales, packed[:1].expand(batch, 0).contiguous(),
                           scales[:1].expand(batch, 0).contiguous(), 0, Y=Y)
     assert not Y.any()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "mx"])
+def test_split_columns_with_many_rows_of_x(g, dtype):
+    """More rows of X than a grid has along y (65535), columns split."""
+    import torch
+    from post_weight_quantization_11_amd import _lib
+    rng = _rng(103)
+    m, n, batch = (130, 8192, 65600) if dtype == "f16" else (130, 32768, 70000)
+    assert _lib.load().gptq_mx_gemm_ws_bytes(m, n, batch, 1) > 0
+    codes, scale = _weights(rng, m, n)
+    packed, scales = _packed(codes, scale)
+    at = np.r_[0, 1, 65534, 65535, 65536, batch - 1, rng.integers(0, batch, size=20)]
+    X = torch.randn((batch, n), device="cuda", dtype=torch.float16,
+                    generator=torch.Generator(device="cuda").manual_seed(103))
+    Y = torch.full((batch, m), float("nan"), device="cuda")
+    if dtype == "f16":
+        X64 = X[torch.from_numpy(at).cuda()].double().cpu().numpy()
+        g.gptq_mx_gemm(packed, scales, X, Y=Y)
+    else:
+        q = g.gptq_mx_quantize(X)
+        X64 = oracle.mx_dequantize(*oracle.mx_quantize(X[torch.from_numpy(at).cuda()].double().cpu().numpy()))
+        g.gptq_mx_scaled_gemm(packed, scales, q["packed"], q["scales"], n, Y=Y)
+    assert not bool(Y.isnan().any())
+    want, mags = oracle.mx_matmul(codes, scale, X64)
+    _check(Y[torch.from_numpy(at).cuda()], want, mags, n, "f32", f"{batch}x{m}x{n} {dtype}")
