@@ -1630,6 +1630,26 @@ size_t plan_ws(const Plan& pl, int64_t m, int64_t rows) {
   return pl.splits > 1 ? align256((size_t)pl.splits * (size_t)rows * (size_t)m * sizeof(float)) : 0;
 }
 
+// A launch has fewer than 2^32 threads.  Calls launch(operands) for the rows of W in
+// parts of whole tiles of bm rows, as many as fit when each tile of W takes `slots`
+// workgroups (at most 2^20 / 16 + 65536 tiles of X: one tile of W always fits).
+// Split columns, whose sums are laid out for all rows at once, never have more
+// than one part: the plan adds splits up to 2048 workgroups.
+template <typename Launch>
+gptq_status in_row_parts(const MxOperands& p, int bm, int64_t slots, int threads, Launch launch) {
+  const int64_t part = std::max<int64_t>(((int64_t)1 << 31) / (slots * threads), 1) * bm;
+  for (int64_t r = 0; r < p.m; r += part) {
+    MxOperands q = p;
+    q.W += r * p.ldp;
+    q.S += r * p.lds;
+    q.Y = static_cast<char*>(p.Y) + r * elem_bytes(p.y_dtype);
+    q.m = (int)std::min(part, p.m - r);
+    launch(q);
+    GPTQ_TRY_LAUNCH();
+  }
+  return GPTQ_OK;
+}
+
 // Runs tile kernel k (tiles of BM x BN) and, with splits, the sum over them.
 gptq_status run_tiles(void (*k)(MxOperands, TileGrid), int BM, int BN, int threads, int lds, const MxOperands& p,
                       const Plan& pl, void* ws, hipStream_t st) {
@@ -1638,12 +1658,14 @@ gptq_status run_tiles(void (*k)(MxOperands, TileGrid), int BM, int BN, int threa
   const int splits = (int)std::max<int64_t>(ceil_div(p.n, cols), 1);
   TileGrid tg{(int)ceil_div(p.m, BM), (int)max_tiles(p.rows, p.experts, p.offsets != nullptr, BN), splits,
               (int)cols, static_cast<float*>(ws)};
-  const int64_t items = (int64_t)tg.row_tiles * tg.tok_tiles * tg.splits;
-  if (items > ((int64_t)1 << 30)) return GPTQ_ERR_UNSUPPORTED;
+  const int64_t slots = (int64_t)tg.tok_tiles * tg.splits;
   if (lds > 65536)
     GPTQ_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds));
-  k<<<(unsigned)round_up(items, kXcds), threads, lds, st>>>(p, tg);
-  GPTQ_TRY_LAUNCH();
+  const gptq_status rc = in_row_parts(p, BM, slots, threads, [&](const MxOperands& q) {
+    tg.row_tiles = (int)ceil_div(q.m, BM);
+    k<<<(unsigned)round_up(tg.row_tiles * slots, kXcds), threads, lds, st>>>(q, tg);
+  });
+  if (rc != GPTQ_OK) return rc;
   if (tg.splits > 1) {
     mx_join_kernel<<<(unsigned)(ceil_div(p.m, kJoinCols) * p.rows), kJoinCols / 4, 0, st>>>(p, tg);
     GPTQ_TRY_LAUNCH();
@@ -1686,19 +1708,16 @@ gptq_status launch_big_tiles(const MxOperands& p, const Plan& pl, void* ws, hipS
 
 template <int XT, int RT, int NT, int D>
 gptq_status launch_rows(const MxOperands& p, int waves, hipStream_t st) {
-  const int64_t grid = ceil_div(p.m, 16 * RT) * max_tiles(p.rows, p.experts, p.offsets != nullptr, 16 * NT);
-  if (grid > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  mx_rows_kernel<XT, RT, NT, D>
-      <<<(unsigned)grid, 64 * waves, waves * RT * NT * 64 * sizeof(floatx4), st>>>(p);
-  GPTQ_TRY_LAUNCH();
-  return GPTQ_OK;
+  const int64_t slots = max_tiles(p.rows, p.experts, p.offsets != nullptr, 16 * NT);
+  return in_row_parts(p, 16 * RT, slots, 64 * waves, [&](const MxOperands& q) {
+    mx_rows_kernel<XT, RT, NT, D>
+        <<<(unsigned)(ceil_div(q.m, 16 * RT) * slots), 64 * waves, waves * RT * NT * 64 * sizeof(floatx4), st>>>(q);
+  });
 }
 
 template <int XT>
 gptq_status launch_stream(const MxOperands& p, hipStream_t st) {
-  const int64_t grid = ceil_div(p.m, 64);
-  if (grid > INT32_MAX) return GPTQ_ERR_UNSUPPORTED;
-  mx_stream_kernel<XT><<<(unsigned)grid, 256, 0, st>>>(p);
+  mx_stream_kernel<XT><<<(unsigned)ceil_div(p.m, 64), 256, 0, st>>>(p);
   GPTQ_TRY_LAUNCH();
   return GPTQ_OK;
 }

@@ -863,3 +863,31 @@ def test_split_columns_with_many_rows_of_x(g, dtype):
     assert not bool(Y.isnan().any())
     want, mags = oracle.mx_matmul(codes, scale, X64)
     _check(Y[torch.from_numpy(at).cuda()], want, mags, n, "f32", f"{batch}x{m}x{n} {dtype}")
+
+
+@pytest.mark.parametrize("dtype,E,rows", [("f16", 2048, 8191), ("bf16", 8192, 34768)])
+def test_grouped_in_parts_of_the_weight_rows(g, dtype, E, rows):
+    """More workgroups than one launch takes: experts of 131072 x 8 on the row
+    kernel (fewer than four rows an expert) and on tiles."""
+    import torch
+    rng = _rng(107, rows)
+    m, n = 131072, 8
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    packed = torch.randint(-(1 << 31), 1 << 31, (E, m, 1), dtype=torch.int32, device="cuda", generator=gen)
+    scales = torch.randint(110, 126, (E, m, 1), dtype=torch.uint8, device="cuda", generator=gen)
+    counts = rng.multinomial(rows - 9, np.full(E, 1.0 / E))
+    off = np.r_[4, 4 + np.cumsum(counts)]                     # four rows before the first expert, five behind the last
+    X, X64 = _to(rng.standard_normal((rows, n)), dtype)
+    Y = torch.full((rows, m), 7.0, device="cuda", dtype=torch.bfloat16)
+    g.gptq_mx_gemm_grouped(packed, scales, X, torch.tensor(off, dtype=torch.int32, device="cuda"), Y=Y)
+    assert bool((Y[:4] == 7).all()) and bool((Y[rows - 5:] == 7).all())
+    pick = np.r_[0, 1, m - 1, rng.integers(0, m, size=200), np.arange(32, m, 4096)]
+    at = torch.from_numpy(pick).cuda()
+    for e in np.r_[0, E - 1, rng.integers(0, E, size=6)]:
+        a, b = off[e], off[e + 1]
+        if a == b:
+            continue
+        words = packed[e, at].cpu().numpy().view(np.uint32)
+        codes = oracle.unpack_codes(words, n, 4).astype(np.int64)
+        want, mags = oracle.mx_matmul(codes, scales[e, at].cpu().numpy().astype(np.int64), X64[a:b])
+        _check(Y[a:b][:, at], want, mags, n, "bf16", f"expert {e} of {E}, {rows} rows")

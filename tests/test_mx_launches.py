@@ -45,3 +45,28 @@ def test_the_sum_over_splits_stays_within_a_grid(recorder):
                 threads = k["grid"][0] * k["grid"][1] * k["block"][0]
                 assert threads >= rows * _up(m, 4)
     assert split >= 4
+
+
+def _grouped(experts, m, n, rows, x, out=2):
+    words, blocks = _up(n, 8), _up(n, 32)
+    return ("gptq_mx_gemm_grouped", [P, experts, m, n, words, m * words, P, blocks, m * blocks, P, x, rows, n, P, P, out,
+                                     m, None, 0, None])
+
+
+def test_a_launch_has_fewer_than_2_to_the_32_threads(recorder):
+    # Many experts with many rows of W on the row kernel and on tiles, and rows
+    # of X too far apart for the tiles on the row kernel: parts of W's rows.
+    calls = [_grouped(2048, 131072, 8, 8191, F16), _grouped(8192, 131072, 8, 34768, BF16),
+             _grouped(65536, 4096, 32, 196608, BF16), _grouped(65536, 65536, 8, 262144, BF16), _grouped(65536, 1 << 20, 1, 1 << 20, F16),
+             _gemm(4096, 32, 1 << 20, F16, ldx=3000000), _gemm(1 << 20, 64, 1 << 17, MX, ldx=1 << 21)]
+    for call, (rc, launches) in zip(calls, _record(recorder, calls)):
+        assert rc == 0 and len(launches) > 1, call
+        for k in launches:
+            assert k["grid"][0] * k["block"][0] < 1 << 32 and k["grid"][1:] == (1, 1), (call, k)
+
+
+def test_usual_sizes_take_one_launch(recorder):
+    calls = [_gemm(49152, 12288, 2048, F16), _gemm(1 << 20, 9216, 20, BF16), _grouped(64, 1024, 2048, 1531, F16),
+             _grouped(1024, 1024, 9216, 20, BF16), _gemm(49152, 640, 80, F16, ldx=3000000)]
+    for call, (rc, launches) in zip(calls, _record(recorder, calls)):
+        assert rc == 0 and len(launches) == 1, call
