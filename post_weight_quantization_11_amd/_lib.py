@@ -490,7 +490,8 @@ def gptq_mx_quantize(W, want_wq: bool = False, out=None, stream=None):
     Returns dict(packed (... x m x ceil(n/8) int32 words: bit patterns of
     uint32, the code of column k at bits [4k, 4k + 4) of its row), scales
     (... x m x ceil(n/32) uint8, 2^(byte - 127)), Wq (W's shape and dtype, the
-    quantized values) or None).  `out` may hold those tensors."""
+    quantized values) or None).  `out` may hold any of those tensors; it gets
+    the others, Wq only with want_wq."""
     torch = _torch()
     lib = load()
     ctx = _mx_elsewhere(W, stream)
@@ -504,24 +505,31 @@ def gptq_mx_quantize(W, want_wq: bool = False, out=None, stream=None):
     *lead, n = W.shape
     dev = W.device
     words, blocks = -(-n // 8), -(-n // MX_BLOCK)
+    ldw = _mx_folded(W, "W", W.dtype, lead, n, dev)
     if out is None:
-        packed = torch.empty((*lead, words), dtype=torch.int32, device=dev)
-        scales = torch.empty((*lead, blocks), dtype=torch.uint8, device=dev)
-        wq = torch.empty(W.shape, dtype=W.dtype, device=dev) if want_wq else None
-        out = dict(packed=packed, scales=scales, Wq=wq)
-        ld_packed, ld_scales, ld_wq = words, blocks, n
+        out = {}
+    packed, scales, wq = out.get("packed"), out.get("scales"), out.get("Wq")
+    if packed is None:
+        packed, ld_packed = torch.empty((*lead, words), dtype=torch.int32, device=dev), words
     else:
-        packed, scales, wq = out["packed"], out["scales"], out.setdefault("Wq", None)
         ld_packed = _mx_folded(packed, "packed", torch.int32, lead, words, dev)
+    if scales is None:
+        scales, ld_scales = torch.empty((*lead, blocks), dtype=torch.uint8, device=dev), blocks
+    else:
         ld_scales = _mx_folded(scales, "scales", torch.uint8, lead, blocks, dev)
-        ld_wq = 0 if wq is None else _mx_folded(wq, "Wq", W.dtype, lead, n, dev)
+    ld_wq = n
+    if wq is not None:
+        ld_wq = _mx_folded(wq, "Wq", W.dtype, lead, n, dev)
+    elif want_wq:
+        wq = torch.empty(W.shape, dtype=W.dtype, device=dev)
     code = GPTQ_F32 if W.dtype is torch.float32 else GPTQ_BF16 if W.dtype is torch.bfloat16 else GPTQ_F16
     m = lead[0] if len(lead) == 1 else lead[0] * lead[1]
-    rc = lib.gptq_mx_quantize(W.data_ptr(), code, m, n, _mx_folded(W, "W", W.dtype, lead, n, dev), packed.data_ptr(),
-                              ld_packed, scales.data_ptr(), ld_scales, None if wq is None else wq.data_ptr(), ld_wq,
+    rc = lib.gptq_mx_quantize(W.data_ptr(), code, m, n, ldw, packed.data_ptr(), ld_packed, scales.data_ptr(), ld_scales,
+                              None if wq is None else wq.data_ptr(), ld_wq,
                               torch._C._cuda_getCurrentRawStream(dev.index))
     if rc:
         _check(rc, "gptq_mx_quantize")
+    out.update(packed=packed, scales=scales, Wq=wq)
     return out
 
 

@@ -891,3 +891,20 @@ def test_grouped_in_parts_of_the_weight_rows(g, dtype, E, rows):
         codes = oracle.unpack_codes(words, n, 4).astype(np.int64)
         want, mags = oracle.mx_matmul(codes, scales[e, at].cpu().numpy().astype(np.int64), X64[a:b])
         _check(Y[a:b][:, at], want, mags, n, "bf16", f"expert {e} of {E}, {rows} rows")
+
+
+def test_quantize_fills_what_out_lacks(g):
+    import torch
+    rng = _rng(109)
+    W, W64 = _to(rng.standard_normal((7, 77)), "bf16")
+    own = dict(packed=torch.empty((7, 10), dtype=torch.int32, device="cuda"),
+               scales=torch.empty((7, 3), dtype=torch.uint8, device="cuda"),
+               Wq=torch.empty((7, 77), dtype=torch.bfloat16, device="cuda"))
+    for held in ((), ("packed",), ("scales", "Wq"), ("packed", "scales"), ("packed", "scales", "Wq")):
+        for want_wq in (False, True):
+            for missing in ({}, {k: None for k in own if k not in held}):
+                out = {k: own[k].zero_() for k in held} | missing
+                q = g.gptq_mx_quantize(W, want_wq=want_wq, out=out)
+                assert q is out and all(q[k] is own[k] for k in held)
+                assert (q["Wq"] is not None) == (want_wq or "Wq" in held)
+                _check_quantized(q, W64, 77, "bf16")
