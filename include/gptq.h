@@ -443,11 +443,16 @@ gptq_status gptq_mx_quantize(const void* W, int w_dtype, int64_t m, int64_t n, i
  *           (NULL allowed when that is 0), in use until the call's work on
  *           `stream` is done: calls that may run at the same time (two streams,
  *           two captured graphs) need one each.
- * Products are exact in float32 and accumulation is float32, in an order that
+ * Products are exact and accumulation is float32, in an order that
  * depends on sizes, strides and alignment alone (the same call gives the same
- * bits): the error
- * before the one rounding to y_dtype is at most (n/32 + 80) 2^-23
- * sum_k |What[r, k] X[b, k]|, unless that sum passes float32's range.  A weight
+ * bits).  With S = sum_k |What[r, k] X[b, k]|, the error before the one rounding
+ * to y_dtype is at most
+ *     (n/16 + 80) 2^-23 S + n 2^-149,
+ * with n/8 in place of n/16 where X is float16 and a scale byte of the matrix
+ * lies outside 104 .. 140, unless S passes float32's range: the matrix
+ * instructions round once for every eight columns (twice with such scales), by
+ * at most 2^-24 of the sum so far, and cut the terms of those eight 2^-24 below
+ * the largest.  A weight
  * value outside float32's range counts as infinite.  Non-finite weights or X
  * make the outputs that they enter non-finite.  With n = 0, Y is 0. */
 size_t gptq_mx_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, int64_t experts);
@@ -478,7 +483,9 @@ gptq_status gptq_mx_gemm_grouped(const uint32_t* packed, int64_t experts, int64_
 
 /* Y = Xhat What^T with both operands microscaled (X quantized by
  * gptq_mx_quantize): the scaled 4-bit matrix instructions, float32
- * accumulation, the error bound of gptq_mx_gemm.
+ * accumulation.  The error before the rounding to y_dtype is at most
+ * (n/64 + 80) 2^-23 S + n 2^-149, S as for gptq_mx_gemm (one rounding for every
+ * 32 columns).
  *   x_packed, x_scales  device, batch rows of ceil(n/8) words (ld_xpacked) and
  *                       ceil(n/32) bytes (ld_xscales). */
 gptq_status gptq_mx_scaled_gemm(const uint32_t* packed, int64_t m, int64_t n, int64_t ld_packed,

@@ -43,6 +43,7 @@ from .mx_oracle import (  # noqa: F401,E402
     mx_block_byte,
     mx_blocks,
     mx_dequantize,
+    mx_error_bound,
     mx_matmul,
     mx_matmul_bound,
     mx_nearest_code,

@@ -908,3 +908,67 @@ def test_quantize_fills_what_out_lacks(g):
                 assert q is out and all(q[k] is own[k] for k in held)
                 assert (q["Wq"] is not None) == (want_wq or "Wq" in held)
                 _check_quantized(q, W64, 77, "bf16")
+
+
+# ---------------------------------------------------------------------------
+# The error bound, on sums built to reach it.
+# ---------------------------------------------------------------------------
+def _worst_sums(n, parts):
+    """Codes, scale bytes and float16 X of one row whose roundings line up: a
+    first term 1, then in every eight columns a term just below half a unit of
+    it, and (parts = 2) the same from what float16 X has behind its first eight
+    bits: 1 + 7 * 2^-10 and -1 leave 7 * 2^-10 there, under the factor 2^-17 0.44
+    units.  Exact sums are 1 + (n / 8) * 0.49 (0.93) units of 2^-23; the running
+    sum stays 1."""
+    codes = np.full((1, n), 2)                                  # the element 1
+    scale = np.full((1, n // 32), 127 - 17)
+    scale[0, 0] = 127
+    x = np.zeros((1, n))
+    x[0, 0] = 1.0
+    x[0, 32::8] = 2.0 ** -7 * (1 - 2.0 ** -6)
+    if parts == 2:
+        x[0, 33::8] = 1 + 7 * 2.0 ** -10
+        x[0, 34::8] = -1.0
+        codes[0, -32:] = 0
+        scale[0, -1] = 50                                       # not a float16 scale
+    return codes, scale, x
+
+
+@pytest.mark.parametrize("dtype,parts", [("bf16", 1), ("f16", 1), ("f16", 2)])
+@pytest.mark.parametrize("m,n,batch", [(300, 12288, 3), (24576, 4096, 4), (49152, 4096, 16), (24579, 4104, 511),
+                                       (24576, 8192, 520), (8192, 12288, 2048)])
+def test_gemm_error_bound_on_sums_built_for_it(g, m, n, batch, dtype, parts):
+    import torch
+    codes, scale, x = _worst_sums(n - n % 32, parts)
+    if n % 32:
+        codes, x = np.pad(codes, ((0, 0), (0, n % 32))), np.pad(x, ((0, 0), (0, n % 32)))
+        scale = np.pad(scale, ((0, 0), (0, 1)), constant_values=127)
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(x, dtype)
+    assert np.array_equal(X64, x)
+    Y = g.gptq_mx_gemm(packed.expand(m, -1).contiguous(), scales.expand(m, -1).contiguous(),
+                       X.expand(batch, -1).contiguous())
+    want, mags = oracle.mx_matmul(codes, scale, X64)
+    err = float((Y.double() - float(want[0, 0])).abs().max())
+    tol = float(oracle.mx_error_bound(n, mags[0, 0], 8, parts))
+    log(f"  worst sums {batch}x{m}x{n} {dtype}, {parts} parts: {err * 2.0 ** 23:.0f} units, bound {tol * 2.0 ** 23:.0f}")
+    assert err <= tol
+
+
+@pytest.mark.parametrize("m,n,batch", [(300, 12288, 3), (8192, 12288, 2048), (16384, 4096, 80)])
+def test_scaled_gemm_error_bound_on_sums_built_for_it(g, m, n, batch):
+    # A first term 1, then one of 2^-24 in every 32 columns: half a unit, which
+    # rounds to the even sum, 1.
+    codes, scale = np.full((1, n), 2), np.full((1, n // 32), 127)
+    xc, xs = np.zeros((1, n), dtype=np.int64), np.full((1, n // 32), 127 - 24)
+    xc[0, ::32] = 2
+    xs[0, 0] = 127
+    packed, scales = _packed(codes, scale)
+    xp, xsc = _packed(xc, xs)
+    Y = g.gptq_mx_scaled_gemm(packed.expand(m, -1).contiguous(), scales.expand(m, -1).contiguous(),
+                              xp.expand(batch, -1).contiguous(), xsc.expand(batch, -1).contiguous(), n)
+    want, mags = oracle.mx_matmul(codes, scale, oracle.mx_dequantize(xc, xs))
+    err = float((Y.double() - float(want[0, 0])).abs().max())
+    tol = float(oracle.mx_error_bound(n, mags[0, 0], 32))
+    log(f"  worst sums {batch}x{m}x{n} mx: {err * 2.0 ** 23:.0f} units, bound {tol * 2.0 ** 23:.0f}")
+    assert err <= tol
