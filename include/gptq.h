@@ -443,17 +443,20 @@ gptq_status gptq_mx_quantize(const void* W, int w_dtype, int64_t m, int64_t n, i
  *           (NULL allowed when that is 0), in use until the call's work on
  *           `stream` is done: calls that may run at the same time (two streams,
  *           two captured graphs) need one each.
- * Products are exact and accumulation is float32, in an order that
- * depends on sizes, strides and alignment alone (the same call gives the same
- * bits).  With S = sum_k |What[r, k] X[b, k]|, the error before the one rounding
- * to y_dtype is at most
- *     (n/16 + 80) 2^-23 S + n 2^-149,
- * with n/8 in place of n/16 where X is float16 and a scale byte of the matrix
- * lies outside 104 .. 140, unless S passes float32's range: the matrix
- * instructions round once for every eight columns (twice with such scales), by
+ * Products are exact and accumulation is float32.  The same call gives the same
+ * bits: the order of the sums depends on sizes, strides and alignment alone,
+ * but for float16 X under scale bytes outside 104 .. 135 (trained weights have
+ * none).  Float16 does not hold those scales, so a workgroup that meets one
+ * multiplies its rows of W (up to 256 neighbouring ones) in bfloat16, X as a sum
+ * of two numbers.
+ * With S = sum_k |What[r, k] X[b, k]|, the error before the one rounding to
+ * y_dtype is at most
+ *     (n/16 + 80) 2^-23 S + n 2^-149
+ * unless S passes float32's range; n/8 in place of n/16 for rows multiplied in
+ * bfloat16 so.  (The matrix instructions round once for every eight columns, by
  * at most 2^-24 of the sum so far, and cut the terms of those eight 2^-24 below
- * the largest.  A weight
- * value outside float32's range counts as infinite.  Non-finite weights or X
+ * the largest.)
+ * A weight value outside float32's range counts as infinite.  Non-finite weights or X
  * make the outputs that they enter non-finite.  With n = 0, Y is 0. */
 size_t gptq_mx_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, int64_t experts);
 gptq_status gptq_mx_gemm(const uint32_t* packed, int64_t m, int64_t n, int64_t ld_packed,

@@ -972,3 +972,20 @@ def test_scaled_gemm_error_bound_on_sums_built_for_it(g, m, n, batch):
     tol = float(oracle.mx_error_bound(n, mags[0, 0], 32))
     log(f"  worst sums {batch}x{m}x{n} mx: {err * 2.0 ** 23:.0f} units, bound {tol * 2.0 ** 23:.0f}")
     assert err <= tol
+
+
+@pytest.mark.parametrize("m,n,batch", [(1000, 1024, 2), (1000, 1024, 200), (24579, 525, 511), (24576, 576, 512)])
+def test_far_scales_change_the_bits_of_neighbouring_rows_only(g, m, n, batch):
+    import torch
+    rng = _rng(113, m, batch)
+    codes, scale = _weights(rng, m, n)
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((batch, n)), "f16")
+    before = g.gptq_mx_gemm(packed, scales, X)
+    scale[300, 5] = 90
+    packed, scales = _packed(codes, scale)
+    after = g.gptq_mx_gemm(packed, scales, X)
+    assert torch.equal(before[:, :256], after[:, :256]) and torch.equal(before[:, 512:], after[:, 512:])
+    want, mags = oracle.mx_matmul(codes[256:512], scale[256:512], X64)
+    err = np.abs(after[:, 256:512].double().cpu().numpy() - want)
+    assert np.all(err <= oracle.mx_error_bound(n, mags, 8, 2))
