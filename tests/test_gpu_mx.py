@@ -989,3 +989,160 @@ def test_far_scales_change_the_bits_of_neighbouring_rows_only(g, m, n, batch):
     want, mags = oracle.mx_matmul(codes[256:512], scale[256:512], X64)
     err = np.abs(after[:, 256:512].double().cpu().numpy() - want)
     assert np.all(err <= oracle.mx_error_bound(n, mags, 8, 2))
+
+
+# ---------------------------------------------------------------------------
+# The ends of the range and non-finite operands, in every kernel kind.
+# ---------------------------------------------------------------------------
+ENDS = [(100, 700, 3), (24576, 1024, 2), (300, 1100, 70), (4100, 4160, 160), (24579, 525, 511), (24576, 1032, 512),
+        (8192, 2048, 2048), (4096, 2056, 2048), (24576, 512, 400), (8192, 7168, 800)]
+
+
+def _check_finite_part(Y, want, mags, non_finite, n, columns, parts, what):
+    """Non-finite exactly at non_finite; elsewhere within the bound, but where
+    the magnitudes pass float32's range."""
+    got = Y.double().cpu().numpy()
+    tol = oracle.mx_error_bound(n, mags, columns, parts)
+    over = mags + tol > float(np.finfo(np.float32).max)
+    assert np.all(~np.isfinite(got[non_finite])), what
+    ok = ~non_finite & ~over
+    assert np.mean(ok) > 0.3 and np.all(np.isfinite(got[ok])), what
+    assert np.all(np.abs(got - want)[ok] <= tol[ok]), what
+
+
+@pytest.mark.parametrize("m,n,batch", ENDS)
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_weights_up_to_the_end_of_float32s_range(g, m, n, batch, dtype):
+    """Bytes 225 to 252 hold values of float32, 253 and 254 some beyond it,
+    which count as infinite."""
+    import torch
+    rng = _rng(127, m, n)
+    codes, scale = _weights(rng, m, n, 225, 252)
+    pick = np.sort(rng.permutation(m)[:120])
+    beyond = pick[:40]
+    scale[beyond] = rng.integers(225, 255, size=(40, scale.shape[1]))
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((batch, n)) * 2.0 ** -12, dtype)
+    Y = g.gptq_mx_gemm(packed, scales, X)[:, torch.from_numpy(pick).cuda()]
+    W = oracle.mx_dequantize(codes[pick], scale[pick])
+    inf = np.abs(W) >= 2.0 ** 128
+    assert 10 < np.sum(inf.any(1)) <= 40
+    W = np.where(inf, 0.0, W)
+    _check_finite_part(Y, X64 @ W.T, np.abs(X64) @ np.abs(W).T, np.broadcast_to(inf.any(1), (batch, len(pick))), n, 8, 2,
+                       f"{batch}x{m}x{n} {dtype}")
+
+
+@pytest.mark.parametrize("m,n,batch", ENDS)
+def test_scaled_gemm_over_the_whole_range_of_bytes(g, m, n, batch):
+    # Large weights with small X and the other way round: every byte from 0 to
+    # 254 on both sides, the products around 1.
+    import torch
+    rng = _rng(131, m, n)
+    codes, scale = _weights(rng, m, n)
+    xc, xs = _weights(rng, batch, n)
+    nb = oracle.mx_blocks(n)
+    mid = rng.integers(0, 255, size=nb)
+    mid[:3] = 0, 127, 254
+    scale = np.clip(mid + rng.integers(-3, 4, size=(m, nb)), 0, 254)
+    xs = np.clip(254 - mid + rng.integers(-3, 4, size=(batch, nb)), 0, 254)
+    packed, scales = _packed(codes, scale)
+    xp, xsc = _packed(xc, xs)
+    pick = rng.permutation(m)[:100]
+    Y = g.gptq_mx_scaled_gemm(packed, scales, xp, xsc, n)[:, torch.from_numpy(pick).cuda()]
+    want, mags = oracle.mx_matmul(codes[pick], scale[pick], oracle.mx_dequantize(xc, xs))
+    _check_finite_part(Y, want, mags, np.zeros(want.shape, dtype=bool), n, 32, 1, f"{batch}x{m}x{n} mx")
+
+
+@pytest.mark.parametrize("m,n,batch", ENDS)
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "mx"])
+def test_nan_scales_anywhere_in_every_kernel_kind(g, m, n, batch, dtype):
+    import torch
+    rng = _rng(137, m, n)
+    codes, scale = _weights(rng, m, n)
+    pick = rng.permutation(m)[:100]
+    nb = scale.shape[1]
+    scale[pick[:30], rng.integers(0, nb, size=30)] = 255
+    scale[pick[30], 0] = scale[pick[31], -1] = 255
+    codes[pick[:16]] = 0                                         # NaN even where every code is 0
+    packed, scales = _packed(codes, scale)
+    bad = np.zeros((batch, 100), dtype=bool)
+    bad[:, :32] = True
+    at = torch.from_numpy(pick).cuda()
+    if dtype == "mx":
+        xc, xs = _weights(rng, batch, n, 118, 130)
+        for t in rng.integers(0, batch, size=min(batch, 20) // 2):
+            xs[t, rng.integers(0, nb)] = 255
+            bad[t] = True
+        xp, xsc = _packed(xc, xs)
+        X64 = oracle.mx_dequantize(xc, np.where(xs == 255, 127, xs))
+        Y = g.gptq_mx_scaled_gemm(packed, scales, xp, xsc, n)[:, at]
+    else:
+        X, X64 = _to(rng.standard_normal((batch, n)), dtype)
+        Y = g.gptq_mx_gemm(packed, scales, X)[:, at]
+    assert np.array_equal(np.isnan(Y.cpu().numpy()), bad)
+    want, mags = oracle.mx_matmul(codes[pick], np.where(scale[pick] == 255, 127, scale[pick]), X64)
+    _check_finite_part(Y, want, mags, bad, n, 32 if dtype == "mx" else 8, 2, f"{batch}x{m}x{n} {dtype}")
+
+
+@pytest.mark.parametrize("m,n,batch", ENDS)
+@pytest.mark.parametrize("dtype,far", [("f16", False), ("f16", True), ("bf16", False)])
+def test_infinities_and_nan_in_x_in_every_kernel_kind(g, m, n, batch, dtype, far):
+    """As the sums say: an infinity times a code 0, two infinities of opposite
+    signs and a NaN give NaN, other infinities theirs.  far: every workgroup
+    multiplies in bfloat16, X as the sum of two numbers."""
+    import torch
+    rng = _rng(139, m, n)
+    codes, scale = _weights(rng, m, n)
+    if far:
+        codes[:, :32] = 0
+        scale[:, 0] = 90
+    packed, scales = _packed(codes, scale)
+    x = rng.standard_normal((batch, n))
+    hit = np.zeros(batch, dtype=bool)
+    for t, k, v in zip(range(0, batch, max(1, batch // 40)), rng.integers(32, n, size=64), [np.inf, -np.inf, np.nan] * 20):
+        if t == batch - 1 and batch > 1:
+            break
+        x[t, k] = v
+        if t % 2:
+            x[t, 33 + (k - 32) % (n - 40)] = np.inf
+        hit[t] = True
+    X, X64 = _to(x, dtype)
+    pick = rng.permutation(m)[:100]
+    Y = g.gptq_mx_gemm(packed, scales, X)[:, torch.from_numpy(pick).cuda()]
+    W = oracle.mx_dequantize(codes[pick], scale[pick])
+    got = Y.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        want = np.stack([(X64[t] * W).sum(1) for t in np.flatnonzero(hit)])
+    assert not np.isfinite(want).any()
+    assert np.array_equal(got[hit], want, equal_nan=True)
+    X0 = X64[~hit]
+    _check_finite_part(Y[torch.from_numpy(~hit).cuda()], X0 @ W.T, np.abs(X0) @ np.abs(W).T,
+                       np.zeros((len(X0), 100), dtype=bool), n, 8, 2, f"{batch}x{m}x{n} {dtype}")
+
+
+@pytest.mark.parametrize("experts,m,n,off,rows", GROUPED + [(64, 70, 520, list(range(0, 65 * 3, 3)), 192),
+                                                            (4, 4100, 2056, [2, 2, 1100, 1101, 2990], 3000)])
+def test_grouped_float16_scales_out_of_range(g, experts, m, n, off, rows):
+    """Float16 X and Y, one expert in two with a far scale, rows outside all
+    experts as they were."""
+    import torch
+    rng = _rng(149, experts, m, rows)
+    codes, scale = _weights(rng, experts * m, n, 112, 118)
+    for e in range(0, experts, 2):
+        r = e * m + int(rng.integers(0, m))
+        scale[r, int(rng.integers(0, scale.shape[1]))] = int(rng.choice([3, 60, 103]))
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((rows, n)), "f16")
+    Y = torch.full((rows, m), 7.0, device="cuda", dtype=torch.float16)
+    g.gptq_mx_gemm_grouped(packed.view(experts, m, -1), scales.view(experts, m, -1), X,
+                           torch.tensor(off, dtype=torch.int32, device="cuda"), Y=Y)
+    got = Y.double().cpu().numpy()
+    assert np.all(got[:off[0]] == 7.0) and np.all(got[off[-1]:] == 7.0)
+    for e in range(experts):
+        a, b = off[e], off[e + 1]
+        if a == b:
+            continue
+        want, mags = oracle.mx_matmul(codes[e * m:(e + 1) * m], scale[e * m:(e + 1) * m], X64[a:b])
+        tol = oracle.mx_error_bound(n, mags, 8, 2)
+        tol = tol + np.maximum(2.0 ** -11 * (np.abs(want) + tol), 2.0 ** -25)
+        assert np.all(np.abs(got[a:b] - want) <= tol), e
