@@ -1597,8 +1597,9 @@ Plan tile_plan(const TileShape (&shapes)[N], int64_t m, int64_t n, int64_t rows,
 // 4 x 11008 x 4096: 11.5 against 10.6).  Their waves load X's rows in pieces:
 // rows of odd lengths slow them down (2 x 4099 x 11007: 21 against 15.6; 8 x 130
 // x 1001 still 5.6 against 7.6).  Microscaled X, which is smaller, stays on them
-// longer (64 x 4096 x 4096: 8.0 against 10.3; 128 x 4096 x 4096: 12.5 against
-// 10.5; 8 x 11008 x 4096: 8.6 against 9.8; 32 x 11008 x 4096: 13.6 against 10.3).
+// longer, up to 2^30 products (64 x 4096 x 4096, the last of them: 8.2 against 12.8;
+// 128 x 4096 x 4096: 12.5 against 10.5; 8 x 11008 x 4096: 8.6 against 9.8; 32 x
+// 11008 x 4096: 13.6 against 10.3).
 // Long matrices with up to four rows of 16-bit X take the stream kernel (1 x
 // 28672 x 8192: 24 against 30 on tiles; 1 x 12288 x 12288: 27 against 20).
 Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool mx) {
@@ -1613,7 +1614,7 @@ Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
   const bool small = m * n <= ((int64_t)1 << 24);
   if (mx) {
-    if (small ? products > 1070000000 : products > 500000000) return tile_plan(kScaledTileShapes, m, n, rows);
+    if (small ? products > ((int64_t)1 << 30) : products > 500000000) return tile_plan(kScaledTileShapes, m, n, rows);
     if (outputs <= 65536 || !small) return Plan{kRows1, 1};
     return Plan{rows <= 32 ? kRows2 : kRows2x2, 1};
   }

@@ -70,3 +70,30 @@ def test_usual_sizes_take_one_launch(recorder):
              _grouped(1024, 1024, 9216, 20, BF16), _gemm(49152, 640, 80, F16, ldx=3000000)]
     for call, (rc, launches) in zip(calls, _record(recorder, calls)):
         assert rc == 0 and len(launches) == 1, call
+
+
+def _kind(launch):
+    """Kernel of a product, tiles as (W rows, X rows)."""
+    k, a = launch["kernel"], launch["args"]
+    if k in ("mx_tile_kernel", "mx_big_tile_kernel"):
+        return 32 * a[1] * a[3], 32 * a[2] * a[4]
+    return {"mx_rows_kernel": "rows", "mx_stream_kernel": "stream"}[k]
+
+
+# Rows of X, of W and columns of sizes measured on two kernels, and the faster one.
+MEASURED = [
+    (64, 4096, 4096, MX, "rows"), (128, 4096, 4096, MX, (128, 32)), (8, 11008, 4096, MX, "rows"),
+    (32, 11008, 4096, MX, (128, 32)), (512, 4096, 4096, MX, (128, 64)), (2048, 4096, 4096, MX, (128, 128)),
+    (4096, 12288, 12288, MX, (256, 256)),
+    (32, 4096, 4096, F16, "rows"), (64, 4096, 4096, F16, (128, 32)), (1, 4096, 11008, F16, "rows"),
+    (4, 11008, 4096, F16, (128, 32)), (2, 4099, 11007, F16, (128, 32)), (8, 130, 1001, F16, "rows"),
+    (1, 49152, 12288, F16, "stream"), (1, 28672, 8192, F16, "stream"), (1, 12288, 12288, F16, (128, 32)),
+    (256, 4096, 4096, BF16, (128, 32)), (256, 11008, 4096, BF16, (128, 64)), (2048, 11008, 4096, BF16, (256, 128)),
+    (4096, 8192, 8192, BF16, (256, 256)),
+]
+
+
+@pytest.mark.parametrize("rows,m,n,x,want", MEASURED)
+def test_the_plan_takes_the_kernel_that_measured_faster(recorder, rows, m, n, x, want):
+    rc, launches = _record(recorder, [_gemm(m, n, rows, x)])[0]
+    assert rc == 0 and _kind(launches[0]) == want
