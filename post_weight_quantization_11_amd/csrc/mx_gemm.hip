@@ -25,7 +25,6 @@ namespace gptq {
 namespace {
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef uint16_t u16_a1 __attribute__((aligned(1)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
@@ -567,11 +566,8 @@ __device__ inline bool stream_product(const MxOperands& p, const TokenTile& tile
 template <int XT>
 __global__ __launch_bounds__(256) void mx_stream_kernel(MxOperands p) {
   __shared__ u32x4 xs[2 * 64 * kStreamRows]; // [2][unit][step][quarter][row]
-  const int row_wgs = (p.m + 63) / 64;
-  const int slot = (int)(blockIdx.x / row_wgs);
-  const int r0 = (int)(blockIdx.x % row_wgs) * 64 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 16;
-  const TokenTile tile = find_tile(p, slot, 16);
-  if (!tile.valid) return;
+  const int r0 = (int)blockIdx.x * 64 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 16;
+  const TokenTile tile{0, 0, p.rows, true};  // never grouped by expert, at most kStreamRows rows
   const bool done = stream_product<XT, false>(p, tile, r0, xs);
   if constexpr (XT == GPTQ_F16) {
     if (!done) stream_product<XT, true>(p, tile, r0, xs);
@@ -787,8 +783,7 @@ template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT, bool WL, 
 __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, const TokenTile& tile, int r0, int split,
                                     unsigned char* smem) {
   constexpr bool MX = XT == kMx;
-  static_assert(!MX || (PB == 1 && !WL), "microscaled stages are one panel, with W's");
-  static_assert(!WL || PB >= 2, "64 or 128 bytes of a row");
+  static_assert(MX ? PB == 1 && !WL : PB == 2 || PB == 4, "microscaled stages are one panel, with W's");
   constexpr int kThreads = 64 * WR * WC, kWaves = WR * WC;
   constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB;
   constexpr int kLdsRows = MX ? BM + BN : BN;                 // X rows first, then W rows
@@ -956,12 +951,8 @@ __device__ inline bool tile_product(const MxOperands& p, const TileGrid& tg, con
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         const uint8_t* at = sbase + (ws_at[rb] + 2u * PB * st);
-        if constexpr (PB == 1) {
-          g.ws[0][rb] = *reinterpret_cast<const u16_a1*>(at);
-        } else {
 #pragma unroll
-          for (int i = 0; i < PB / 2; ++i) g.ws[i][rb] = reinterpret_cast<const u32_a1*>(at)[i];
-        }
+        for (int i = 0; i < PB / 2; ++i) g.ws[i][rb] = reinterpret_cast<const u32_a1*>(at)[i];
       }
     }
   };
@@ -1477,16 +1468,13 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void mx_big_tile_kernel(MxOperands
 // Adds the splits' sums in order, four columns a thread and four splits' loads
 // in flight (one at a time they cost a memory latency a split).  All workgroups
 // lie along x, a row of X after the other: there can be more rows than a grid
-// has along y (65535).  Rows that belong to no expert stay.
+// has along y (65535).  Every row has a sum: products grouped by expert are never
+// split.
 constexpr int kJoinCols = 1024;              // columns of Y a workgroup
 __global__ __launch_bounds__(kJoinCols / 4) void mx_join_kernel(MxOperands p, TileGrid tg) {
   const int chunks = (p.m + kJoinCols - 1) / kJoinCols;
   const int x = (int)(blockIdx.x / chunks), r = (int)(blockIdx.x % chunks) * kJoinCols + (int)threadIdx.x * 4;
   if (r >= p.m) return;
-  if (p.offsets != nullptr) {
-    const int lo = min(max(p.offsets[0], 0), p.rows), hi = min(max(p.offsets[p.experts], 0), p.rows);
-    if (x < lo || x >= hi) return;
-  }
   const int64_t total = (int64_t)p.rows * p.m;
   const float* part = tg.part + (int64_t)x * p.m;
   const int left = p.m - r;
