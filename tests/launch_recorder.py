@@ -27,6 +27,7 @@ static int s_count;
 static FILE* s_out;
 
 void recorder_open(const char* path) { s_out = fopen(path, "w"); }
+void recorder_kernels(void) { for (int i = 0; i < s_count; ++i) fprintf(s_out, "kernel %s\n", s_names[i].name); }
 void recorder_mark(int call, int rc) { fprintf(s_out, "call %d %d\n", call, rc); fflush(s_out); }
 
 void** __hipRegisterFatBinary(const void* data) { static void* module; (void)data; return &module; }
@@ -78,28 +79,37 @@ def build(folder):
     return so
 
 
+def kernels(so):
+    """Every kernel the library holds: {(kernel, args)}."""
+    return {_kernel(w[1]) for w in _run(so, []) if w[0] == "kernel"}
+
+
 def record(so, calls):
     """calls: [(entry point, its arguments: whole numbers, None for a null
     pointer)].  Returns [(status, [launch])], a launch being a dict of kernel,
     args, grid, block, lds."""
+    out, pending = [], []
+    for w in _run(so, calls):
+        if w[0] == "call":
+            out.append((int(w[2]), pending))
+            pending = []
+        elif w[0] == "launch":
+            kernel, args = _kernel(w[1])
+            g = [int(v) for v in w[2:9]]
+            pending.append(dict(kernel=kernel, args=args, grid=tuple(g[:3]), block=tuple(g[3:6]), lds=g[6]))
+    assert len(out) == len(calls)
+    return out
+
+
+def _run(so, calls):
+    """The child's lines, split into words: the kernels if there are no calls."""
     folder = os.path.dirname(so)
     todo, done = os.path.join(folder, "calls.json"), os.path.join(folder, "launches.txt")
     with open(todo, "w") as f:
         json.dump(calls, f)
     subprocess.run([sys.executable, os.path.abspath(__file__), so, todo, done], check=True, cwd=ROOT)
-    out, pending = [], []
     with open(done) as f:
-        for line in f:
-            w = line.split()
-            if w[0] == "call":
-                out.append((int(w[2]), pending))
-                pending = []
-            else:
-                kernel, args = _kernel(w[1])
-                g = [int(v) for v in w[2:9]]
-                pending.append(dict(kernel=kernel, args=args, grid=tuple(g[:3]), block=tuple(g[3:6]), lds=g[6]))
-    assert len(out) == len(calls)
-    return out
+        return [line.split() for line in f]
 
 
 def _child(so, todo, done):
@@ -110,6 +120,9 @@ def _child(so, todo, done):
     lib = _lib.load()
     with open(todo) as f:
         calls = json.load(f)
+    if not calls:
+        rec.recorder_kernels()
+        rec.recorder_mark(-1, 0)
     for i, (name, args) in enumerate(calls):
         rec.recorder_mark(i, getattr(lib, name)(*args))
 

@@ -1146,3 +1146,38 @@ def test_grouped_float16_scales_out_of_range(g, experts, m, n, off, rows):
         tol = oracle.mx_error_bound(n, mags, 8, 2)
         tol = tol + np.maximum(2.0 ** -11 * (np.abs(want) + tol), 2.0 ** -25)
         assert np.all(np.abs(got[a:b] - want) <= tol), e
+
+
+# Rows that are not 16-byte aligned, of W, of X and of both, on every tile shape.
+FAR_MORE = [(8192, 4093, 70), (4096, 4104, 160), (16400, 1031, 135), (16400, 1021, 135), (8195, 8168, 39),
+            (16387, 525, 799)]
+
+
+@pytest.mark.parametrize("m,n,batch", FAR_MORE)
+def test_float16_scales_out_of_range_under_unaligned_rows(g, m, n, batch):
+    import torch
+    rng = _rng(m, n, batch, 151)
+    codes, scale = _weights(rng, m, n)
+    at = rng.integers(0, m, size=4)
+    scale[at[0], -1], scale[at[1], 0], scale[at[2], 5], scale[at[3], 9] = 3, 200, 141, 103
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((batch, n)), "f16")
+    Y = g.gptq_mx_gemm(packed, scales, X)
+    # Those rows, the 256 around each of them, and others.
+    rows = np.unique(np.concatenate([*(np.arange(r // 256 * 256, min(m, r // 256 * 256 + 256)) for r in at),
+                                     rng.permutation(m)[:100]]))
+    want, mags = oracle.mx_matmul(codes[rows], scale[rows], X64)
+    err = np.abs(Y[:, torch.from_numpy(rows).cuda()].double().cpu().numpy() - want)
+    assert np.all(err <= oracle.mx_error_bound(n, mags, 8, 2))
+
+
+def test_fewer_columns_than_the_last_word_and_block_hold(g):
+    # 57 to 64 columns have the same words and scale bytes.
+    rng = _rng(157)
+    codes, scale = _weights(rng, 4, 64)
+    packed, scales = _packed(codes, scale)
+    X, X64 = _to(rng.standard_normal((3, 64)), "f16")
+    for n in (57, 60, 63, 64):
+        want, mags = oracle.mx_matmul(codes[:, :n], scale, X64[:, :n])
+        err = np.abs(g.gptq_mx_gemm(packed, scales, X[:, :n]).double().cpu().numpy() - want)
+        assert np.all(err <= oracle.mx_error_bound(n, mags))

@@ -97,3 +97,28 @@ MEASURED = [
 def test_the_plan_takes_the_kernel_that_measured_faster(recorder, rows, m, n, x, want):
     rc, launches = _record(recorder, [_gemm(m, n, rows, x)])[0]
     assert rc == 0 and _kind(launches[0]) == want
+
+
+def test_gpu_tests_reach_every_kernel(recorder):
+    """The sizes of the parity tests launch every kernel of the products in the
+    library; those with scales that float16 does not hold, every one that
+    multiplies float16 X."""
+    from tests import test_gpu_mx as sizes
+
+    def reached(calls):
+        out = set()
+        for rc, launches in _record(recorder, calls):
+            assert rc == 0
+            out |= {(k["kernel"], k["args"]) for k in launches}
+        return out
+
+    held = {k for k in launch_recorder.kernels(recorder) if k[0].startswith("mx_") and k[0] != "mx_quantize_kernel"}
+    assert len(held) > 40
+    shapes = sizes.GEMM + sizes.KINDS + sizes.ENDS
+    large = [(4, m, n, 3000) for m, n in ((4096, 2048), (4099, 2056), (4090, 2061))]
+    grouped = [(e, m, n, rows) for e, m, n, _, rows in sizes.GROUPED] + large
+    assert reached([_gemm(*s, x) for s in shapes for x in (F16, BF16, MX)] +
+                   [_grouped(*s, x) for s in grouped for x in (F16, BF16)]) == held
+    far = [_gemm(*s, F16) for s in sizes.ENDS + sizes.FAR_MORE]
+    far += [_grouped(e, m, n, rows, F16) for e, m, n, _, rows in sizes.GROUPED] + [_grouped(*s, F16) for s in large]
+    assert {k for k in held if k[1][:1] == (F16,)} <= reached(far)
