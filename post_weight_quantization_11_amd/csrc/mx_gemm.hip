@@ -65,11 +65,12 @@ struct TokenTile {
 
 // The slot-th tile, counting every expert's ceil(rows / tile) tiles in order.
 // All 64 lanes of the calling wave take part.  Offsets are clamped to the rows
-// there are, so whatever they hold no access leaves X or Y.
+// there are, so whatever they hold no access leaves X or Y (the counts wrap where
+// descending offsets count rows more than once: up to 2^16 experts of 2^16 tiles).
 __device__ inline TokenTile find_tile(const MxOperands& p, int slot, int tile) {
   if (p.offsets == nullptr) return TokenTile{0, slot * tile, min(p.rows, (slot + 1) * tile), true};
   const int lane = (int)threadIdx.x & 63;
-  int before = 0;                            // tiles of the experts before these 64
+  uint32_t before = 0u;                      // tiles of the experts before these 64
   for (int e0 = 0; e0 < p.experts; e0 += 64) {
     const int e = e0 + lane;
     int lo = 0, hi = 0;
@@ -77,22 +78,22 @@ __device__ inline TokenTile find_tile(const MxOperands& p, int slot, int tile) {
       lo = min(max(p.offsets[e], 0), p.rows);
       hi = min(max(p.offsets[e + 1], lo), p.rows);
     }
-    const int own = (hi - lo + tile - 1) / tile;
-    int upto = own;                          // inclusive sum over the lanes
+    const uint32_t own = (uint32_t)((hi - lo + tile - 1) / tile);
+    uint32_t upto = own;                     // inclusive sum over the lanes
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(upto, d, 64);
+      const uint32_t o = __shfl_up(upto, d, 64);
       if (lane >= d) upto += o;
     }
-    const int at = slot - before - (upto - own);
-    const uint64_t hit = __ballot(at >= 0 && at < own);
+    const uint32_t at = (uint32_t)slot - before - (upto - own);
+    const uint64_t hit = __ballot(at < own);
     if (hit != 0) {
       const int l = __builtin_ctzll(hit);
-      const int begin = __shfl(lo + at * tile, l, 64), end = __shfl(hi, l, 64);
+      const int begin = __shfl(lo + (int)at * tile, l, 64), end = __shfl(hi, l, 64);
       return TokenTile{e0 + l, __builtin_amdgcn_readfirstlane(begin),
                        __builtin_amdgcn_readfirstlane(min(end, begin + tile)), true};
     }
-    before += __builtin_amdgcn_readfirstlane(__shfl(upto, 63, 64));
+    before += (uint32_t)__builtin_amdgcn_readfirstlane((int)__shfl(upto, 63, 64));
   }
   return TokenTile{0, 0, 0, false};
 }

@@ -1181,3 +1181,27 @@ def test_fewer_columns_than_the_last_word_and_block_hold(g):
         want, mags = oracle.mx_matmul(codes[:, :n], scale, X64[:, :n])
         err = np.abs(g.gptq_mx_gemm(packed, scales, X[:, :n]).double().cpu().numpy() - want)
         assert np.all(err <= oracle.mx_error_bound(n, mags))
+
+
+@pytest.mark.parametrize("experts,rows", [(3000, 4099), (300, 700), (7, 700)])
+def test_grouped_descending_offsets_stay_inside_y(g, experts, rows):
+    """Offsets that go up and down count rows many times over: which rows are
+    computed is undefined, nothing around Y is written."""
+    import torch
+    rng = _rng(163, experts)
+    m, n = 40, 72
+    codes, scale = _weights(rng, m, n)
+    packed, scales = _packed(codes, scale)
+    X, _ = _to(rng.standard_normal((rows, n)), "f16")
+    P, S = (t.expand(experts, -1, -1).contiguous() for t in (packed, scales))
+    for lo, hi in ((0, rows), (-(1 << 31), (1 << 31) - 1), (rows - 1, 5)):
+        buf = torch.full((rows + 20, m), 5.0, device="cuda")
+        off = torch.tensor([lo, hi] * experts, dtype=torch.int32, device="cuda")[:experts + 1].contiguous()
+        g.gptq_mx_gemm_grouped(P, S, X, off, Y=buf[10:10 + rows])
+        assert (buf[:10] == 5.0).all() and (buf[10 + rows:] == 5.0).all()
+        if lo <= 0:
+            # The first expert's rows are all of them, and every expert's weights are the same.
+            want = g.gptq_mx_gemm(packed, scales, X)
+            err = (buf[10:10 + rows] - want).abs().double().cpu().numpy()
+            mags = np.abs(X.double().cpu().numpy()) @ np.abs(oracle.mx_dequantize(codes, scale)).T
+            assert np.all(err <= 2 * oracle.mx_error_bound(n, mags))
