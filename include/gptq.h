@@ -440,9 +440,9 @@ gptq_status gptq_mx_quantize(const void* W, int w_dtype, int64_t m, int64_t n, i
  *   Y       device, batch x m output (ldy >= m), y_dtype GPTQ_F32, GPTQ_F16 or
  *           GPTQ_BF16.  Must not overlap the inputs.
  *   ws      device workspace of gptq_mx_gemm_ws_bytes(m, n, batch, 1) bytes
- *           (NULL allowed when that is 0), in use until the call's work on
- *           `stream` is done: calls that may run at the same time (two streams,
- *           two captured graphs) need one each.
+ *           (NULL allowed when that is 0), 4-byte aligned, in use until the
+ *           call's work on `stream` is done: calls that may run at the same time
+ *           (two streams, two captured graphs) need one each.
  * Products are exact and accumulation is float32.  The same call gives the same
  * bits: the order of the sums depends on sizes, strides and alignment alone,
  * but for float16 X under scale bytes outside 104 .. 135 (trained weights have

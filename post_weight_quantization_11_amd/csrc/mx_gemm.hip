@@ -1721,6 +1721,7 @@ gptq_status launch(const MxOperands& p, void* ws, size_t ws_bytes, hipStream_t s
     pl = Plan{kRows2, 1};
   const size_t need = plan_ws(pl, p.m, p.rows);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return GPTQ_ERR_WORKSPACE;
+  if (need > 0 && (reinterpret_cast<uintptr_t>(ws) & 3) != 0) return GPTQ_ERR_INVALID_ARG;
   constexpr bool MX = XT == kMx;
   constexpr int P2 = MX ? 1 : 2, P4 = MX ? 1 : 4;            // panels per stage
   if constexpr (!MX) {

@@ -162,3 +162,15 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         g.gptq_mx_gemm_grouped(packed[None], scales[None], w.half(), torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         g.gptq_mx_scaled_gemm(packed, scales, packed, scales, 64)
+
+
+def test_misaligned_workspace_is_refused_before_any_launch(lib):
+    # Its sums are float32.
+    m, n, batch = 1100, 12000, 200
+    need = lib.gptq_mx_gemm_ws_bytes(m, n, batch, 1)
+    base = dict(GEMM, m=m, n=n, ldp=n // 8, lds=n // 32, batch=batch, ldx=n, ldy=m)
+    for at in (0x1001, 0x1002, 0x1003):
+        assert _call(lib.gptq_mx_gemm, base, ws=_p(at), ws_bytes=need) == INVALID
+    base = dict(SCALED, m=12288, n=12288, ldp=1536, lds=384, batch=64, ldx=1536, ldxs=384, ldy=12288)
+    need = lib.gptq_mx_gemm_ws_bytes(12288, 12288, 64, 1)
+    assert _call(lib.gptq_mx_scaled_gemm, base, ws=_p(0x1002), ws_bytes=need) == INVALID
