@@ -408,7 +408,9 @@ gptq_status gptq_dequant_gemm(const uint32_t* packed, int64_t m, int64_t n, int6
  *           (ceil(n/32) bytes to a row; the last block may be shorter): the
  *           factor 2^(byte - 127); byte 255 is NaN.
  * Sizes for all calls: 0 <= n <= 2^20, others return GPTQ_ERR_UNSUPPORTED.
- * Rows may start at any element-aligned address.
+ * Rows may start at any element-aligned address; products are fastest where the
+ * rows of X and of the packed words are 16-byte aligned, and several times slower
+ * for many rows where neighbouring rows of an operand lie more than 4 MiB apart.
  * ---------------------------------------------------------------------- */
 #define GPTQ_MX_MAX_ROWS 1048576     /* rows of W and of X in a product */
 #define GPTQ_MX_MAX_EXPERTS 65536
@@ -445,10 +447,10 @@ gptq_status gptq_mx_quantize(const void* W, int w_dtype, int64_t m, int64_t n, i
  *           (two streams, two captured graphs) need one each.
  * Products are exact and accumulation is float32.  The same call gives the same
  * bits: the order of the sums depends on sizes, strides and alignment alone,
- * but for float16 X under scale bytes outside 104 .. 135 (trained weights have
- * none).  Float16 does not hold those scales, so a workgroup that meets one
- * multiplies its rows of W (up to 256 neighbouring ones) in bfloat16, X as a sum
- * of two numbers.
+ * but for float16 X under scale bytes outside 104 .. 135 (2^-23 to 2^8, those
+ * of blocks whose largest weight is at least 2^-21 and below 2^11).  Float16 does not hold
+ * all values under other scales, so a workgroup that meets one multiplies its
+ * rows of W (up to 256 neighbouring ones) in bfloat16, X as a sum of two numbers.
  * With S = sum_k |What[r, k] X[b, k]|, the error before the one rounding to
  * y_dtype is at most
  *     (n/16 + 80) 2^-23 S + n 2^-149

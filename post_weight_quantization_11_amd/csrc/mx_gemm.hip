@@ -325,7 +325,7 @@ __device__ inline void multiply_unit(const Unit<XT, RT, NT>& u, const uint32_t (
 // flight per wave; a row's sixteen scale bytes of a quad are one load, a quad
 // ahead (one byte a lane and unit cost 30 of 88 us at 49152 x 12288).  Bound by
 // latency at the sizes it is chosen for: 1 x 4096 x 4096 5.6 us (8.9 MB, of which
-// launch and two dependent loads are 4), 64 experts' 16 x 1024 x 2048 7.2 us (the
+// launch and two dependent loads are 4), 64 experts' 16 x 1024 x 2048 7.5 us (the
 // tile search reads the offsets first).  Returns
 // false, with nothing stored, if a float16 workgroup met scales that are not
 // exact in float16 (the caller then runs it again with SPLIT).
@@ -489,9 +489,9 @@ __global__ __launch_bounds__(512) void mx_rows_kernel(MxOperands p) {
 // 16 bytes of lane (q, row) of step j at place row ^ (4j + q) of the four (the
 // matrix instruction's other rows repeat them), so that writing along a row of X
 // and reading a step both touch all banks evenly.  The packed rows stream through
-// registers, a quad ahead.  Bound by W's bytes: 1 x 49152 x 12288 59 us, 5.4 TB/s
-// (73 us on the row kernel, whose every wave loads X itself; 67 us on 128 x 32
-// tiles).
+// registers, a quad ahead.  Bound by W's bytes: 1 x 49152 x 12288, W from memory,
+// 65 us in bfloat16 and 69 in float16, 4.9 and 4.6 TB/s (87 and 92 us on the row
+// kernel, whose every wave loads X itself; 79 and 84 us on 128 x 32 tiles).
 constexpr int kStreamRows = 4;
 template <int XT, bool SPLIT>
 __device__ inline bool stream_product(const MxOperands& p, const TokenTile& tile, int r0, u32x4* xs) {
@@ -594,13 +594,13 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxOperands p) {
 // h, and step j the codes 8j .. 8j+7 of both.  Microscaled X: W's codes are staged
 // in LDS like X's; step j takes blocks 2j + h.
 //
-// Measured: 16 x 49152 x 12288 80 us (128 x 32; 324 MB, 4.1 TB/s: bound by W's
+// Measured: 16 x 49152 x 12288 83 us (128 x 32; 324 MB, 3.9 TB/s: bound by W's
 // bytes, 384 workgroups on 256 CUs), 77 x 4099 x 11007 20 us (five splits: a
 // chain of 9 stages, 16 us, and the join, 4), 64 experts' 1531 x 1030 x 2044 32 us
 // (84 MB: eight stages a workgroup, first loads and the stores), 2048 x 11008 x
 // 4096 148 us (256 x 128; 1.24 PFLOP/s), 4096 x 8192 x 8192 374 us (256 x 256;
-// 1.47 PFLOP/s, the matrix cores 81% busy at 1.7 GHz: power).  Microscaled: 4096 x
-// 12288 x 12288 290 us (4.3 PFLOP/s, the matrix cores 50% busy at 1.95 GHz; with
+// 1.47 PFLOP/s, the matrix cores 80% busy at 1.7 GHz: power).  Microscaled: 4096 x
+// 12288 x 12288 290 us (4.3 PFLOP/s, the matrix cores 57% busy at 1.8 GHz; with
 // the loads from memory taken out 275: LDS reads, six 16-byte ones a lane for
 // eight products, and the products do not overlap fully.  Four waves of 128 x 128
 // read a third less but took 306, one wave a SIMD).
@@ -1523,8 +1523,11 @@ constexpr int kSplitCols = 256;              // a split is a multiple of this
 // CUs with two already hold the rest up).  Fitted to 180 sizes of 16-bit X from
 // 8 x 1024 x 2048 to 2048 x 49152 x 12288 and 50 of microscaled X: what it
 // chooses takes 1.02 and 1.01 times the fastest's time in the mean, 1.3 and 1.13
-// at worst.  Some of the measured pairs, the chosen first, 16-bit: 16 x 12288 x
-// 12288 on 128 x 32 with 4 splits 21, with 1 41; 256 x 4096 x 4096 on 128 x 32
+// at worst.  It knows sizes only: rows that are not 16-byte aligned take longer (2448
+// x 320 x 8606 28.5 us by the model, 39 measured), and so does a partial last stage
+// of the large tiles (2368 x 14720 x 864: 102 us, 38 by its bytes).  Some of the
+// measured pairs, the chosen first, 16-bit: 16 x 12288 x 12288 (W from memory) on
+// 128 x 32 with 5 splits 26, with 4 28, with 1 54; 256 x 4096 x 4096 on 128 x 32
 // 15, 128 x 64 20; 256 x 11008 x 4096 on 128 x 64 31, 128 x 32 36; 2048 x 11008 x
 // 4096 on 256 x 128 150, 256 x 256 169; 4096 x 8192 x 8192 on 256 x 256 374, 256 x
 // 128 433.  Microscaled: 128 x 4096 x 4096 on 128 x 32 10.5, 128 x 64 12.9; 512 x
@@ -1590,7 +1593,9 @@ Plan tile_plan(const TileShape (&shapes)[N], int64_t m, int64_t n, int64_t rows,
 // 128 x 4096 x 4096: 12.5 against 10.5; 8 x 11008 x 4096: 8.6 against 9.8; 32 x
 // 11008 x 4096: 13.6 against 10.3).
 // Long matrices with up to four rows of 16-bit X take the stream kernel (1 x
-// 28672 x 8192: 24 against 30 on tiles; 1 x 12288 x 12288: 27 against 20).
+// 28672 x 8192: 24 against 30 on tiles; 1 x 12288 x 12288: 27 against 20).  The
+// thresholds stand beside the model: 32 x 4096 x 4128, just past one, takes 12.6 on
+// tiles where 32 x 4096 x 4096 takes 9.5 on the row kernel.
 Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool mx) {
   if (grouped) {
     // By the rows an expert has on average; the workgroups of an expert without
@@ -1715,7 +1720,9 @@ gptq_status launch_stream(const MxOperands& p, hipStream_t st) {
 template <int XT>
 gptq_status launch(const MxOperands& p, void* ws, size_t ws_bytes, hipStream_t st) {
   Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, XT == kMx);
-  // The tile kernels address the rows of a tile with 32 bits.
+  // The tile kernels address the rows of a tile with 32 bits; rows further apart
+  // take the row kernel, which reads both operands many times over (X's rows 4.4 MB
+  // apart: 512 x 11008 x 4096 270 us instead of 64, 2048 rows 985 instead of 162).
   constexpr int64_t kMaxPitch = (int64_t)1 << 22;
   if (p.ldx * (XT == kMx ? 4 : 2) > kMaxPitch || p.ldp * 4 > kMaxPitch || p.lds > kMaxPitch || p.ldxs > kMaxPitch)
     pl = Plan{kRows2, 1};
