@@ -324,7 +324,7 @@ def _run_own(s):
     import post_weight_quantization_11_amd as g
     op = s["op"]
     if op == "quantize":
-        q = g.gptq_fp8_quantize(s["W"], block_rows=s["block_rows"], want_wq=s["values"])
+        q = g.gptq_block_quantize(s["W"], block_rows=s["block_rows"], want_wq=s["values"])
         if s["values"]:
             s["codes"] = q["codes"]
             return {"scales": q["scales"], "values": q["Wq"]}
@@ -334,13 +334,13 @@ def _run_own(s):
         return {"ids": r["ids"], "weights": r["weights"], "offsets": r["offsets"], "order": r["order"]}
     out = DTYPES[s["out"]]
     if op == "moe":
-        layer = g.gptq_fp8_moe if s["format"] == "fp8" else g.gptq_mx_moe
+        layer = g.gptq_block_moe if s["format"] == "fp8" else g.gptq_mx_moe
         return layer(s["gate_up"], s["gate_up_scales"], s["down"], s["down_scales"], s["X"], s["logits"], s["topk"],
                      renormalize=s["renormalize"], y_dtype=out)
-    q = g.gptq_fp8_quantize(s["X"])
+    q = g.gptq_block_quantize(s["X"])
     if op == "gemm":
-        return g.gptq_fp8_gemm(s["codes"], s["scales"], q["codes"], q["scales"], y_dtype=out)
-    return g.gptq_fp8_gemm_grouped(s["codes"], s["scales"], q["codes"], q["scales"], s["offsets"], Y=s["Y"])
+        return g.gptq_block_gemm(s["codes"], s["scales"], q["codes"], q["scales"], y_dtype=out)
+    return g.gptq_block_gemm_grouped(s["codes"], s["scales"], q["codes"], q["scales"], s["offsets"], Y=s["Y"])
 
 
 def run(state):
