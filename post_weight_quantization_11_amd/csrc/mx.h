@@ -24,6 +24,28 @@ typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 
+// Division by the groups per row: q = (g * mul) >> shift for g < 2^31.
+struct GroupDiv {
+  uint32_t mul;
+  int shift;
+};
+
+inline GroupDiv group_div(uint32_t d) {
+  int L = 0;
+  while (((uint64_t)1 << L) < d) ++L;
+  return GroupDiv{(uint32_t)((((uint64_t)1 << (31 + L)) + d - 1) / d), 31 + L};
+}
+
+// Element storage, and 16 bytes of it at any element-aligned address.
+template <int DT> struct Elem {
+  typedef uint16_t type;
+  typedef u32x4_a2 vec;
+};
+template <> struct Elem<GPTQ_F32> {
+  typedef uint32_t type;
+  typedef u32x4_a4 vec;
+};
+
 // The float32 whose exponent field is the byte, as the conversion and matrix
 // instructions take scales: they use the field alone, so byte 0 is 2^-127 and
 // 255 is NaN there.

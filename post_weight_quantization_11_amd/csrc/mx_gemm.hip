@@ -15,10 +15,8 @@
 // of every lane's block: X columns 32 (l / 16) + 8j .. + 7, one 16-byte load.
 // X is the first operand, so a wave's results have consecutive W rows in
 // neighbouring lanes and go out in contiguous runs.
-#include "mx.h"
+#include "product.h"
 
-#include <cmath>
-#include <limits>
 #include <type_traits>
 
 namespace gptq {
@@ -28,7 +26,6 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
-typedef floatx4 floatx4_a4 __attribute__((aligned(4)));
 
 constexpr int kMx = 3;                       // X operand kinds: GPTQ_F16, GPTQ_BF16, microscaled
 
@@ -47,56 +44,6 @@ struct MxOperands {
   int64_t ldy;
   int y_dtype;
 };
-
-__device__ inline void store_y(const MxOperands& p, int64_t at, float v) {
-  if (p.y_dtype == GPTQ_F32)
-    static_cast<float*>(p.Y)[at] = v;
-  else if (p.y_dtype == GPTQ_F16)
-    static_cast<_Float16*>(p.Y)[at] = (_Float16)v;
-  else
-    static_cast<__bf16*>(p.Y)[at] = (__bf16)v;
-}
-
-// One tile of at most `tile` rows of X that share a weight matrix.
-struct TokenTile {
-  int expert, begin, end;                    // rows [begin, end) of X
-  bool valid;
-};
-
-// The slot-th tile, counting every expert's ceil(rows / tile) tiles in order.
-// All 64 lanes of the calling wave take part.  Offsets are clamped to the rows
-// there are, so whatever they hold no access leaves X or Y (the counts wrap where
-// descending offsets count rows more than once: up to 2^16 experts of 2^16 tiles).
-__device__ inline TokenTile find_tile(const MxOperands& p, int slot, int tile) {
-  if (p.offsets == nullptr) return TokenTile{0, slot * tile, min(p.rows, (slot + 1) * tile), true};
-  const int lane = (int)threadIdx.x & 63;
-  uint32_t before = 0u;                      // tiles of the experts before these 64
-  for (int e0 = 0; e0 < p.experts; e0 += 64) {
-    const int e = e0 + lane;
-    int lo = 0, hi = 0;
-    if (e < p.experts) {
-      lo = min(max(p.offsets[e], 0), p.rows);
-      hi = min(max(p.offsets[e + 1], lo), p.rows);
-    }
-    const uint32_t own = (uint32_t)((hi - lo + tile - 1) / tile);
-    uint32_t upto = own;                     // inclusive sum over the lanes
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t o = __shfl_up(upto, d, 64);
-      if (lane >= d) upto += o;
-    }
-    const uint32_t at = (uint32_t)slot - before - (upto - own);
-    const uint64_t hit = __ballot(at < own);
-    if (hit != 0) {
-      const int l = __builtin_ctzll(hit);
-      const int begin = __shfl(lo + (int)at * tile, l, 64), end = __shfl(hi, l, 64);
-      return TokenTile{e0 + l, __builtin_amdgcn_readfirstlane(begin),
-                       __builtin_amdgcn_readfirstlane(min(end, begin + tile)), true};
-    }
-    before += (uint32_t)__builtin_amdgcn_readfirstlane((int)__shfl(upto, 63, 64));
-  }
-  return TokenTile{0, 0, 0, false};
-}
 
 // Eight codes (one word) as eight 16-bit values times the scale.
 template <int XT> __device__ inline u32x4 widen8(uint32_t w, float s);
@@ -223,16 +170,6 @@ __device__ inline uint32_t load_scales4(const uint8_t* srow, int blk, int n) {
   if (left >= 4) return v;
   const uint32_t there = (1u << (8 * max(left, 0))) - 1u;
   return (v & there) | (kMxScaleOne * 0x01010101u & ~there);
-}
-
-// s_waitcnt immediate (gfx9 encoding): vmcnt <= v, expcnt unconstrained, lgkmcnt = 0.
-constexpr int waitcnt_vm(int v) { return (v & 15) | ((v >> 4) << 14) | (7 << 4); }
-
-// Orders LDS accesses only: loads in flight are waited for explicitly.
-__device__ inline void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Stores a 16 x 16 block: accumulator register i of lane l is X row 4 (l / 16) + i,
@@ -634,17 +571,6 @@ constexpr int tile_lds() {
   return std::max(2 * PB * rows * kPanelRow + behind, WR * WC * 32 * out_pitch(RB) * 4);
 }
 
-// Work of one launch: tiles of W rows, of X rows, and parts of the columns.
-struct TileGrid {
-  int row_tiles, tok_tiles, splits, cols_per_split;
-  float* part;                               // [split][row of X][m] sums, when splits > 1
-};
-
-// Tiles of X rows are numbered within bands of eight, all W tiles of a band
-// before the next band: the workgroups an XCD runs at a time share few rows of
-// either operand in its L2.
-constexpr int kTokBand = 8;
-
 // One 16-byte chunk of a row: of a whole panel, and of a row's last columns
 // (zero past its end).
 template <int XT>
@@ -676,40 +602,6 @@ __device__ inline floatx16 mfma_mx(int step, u32x4 x, uint32_t xs, u32x4 w, uint
     case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 1, (int)xs, 1, (int)ws);
     case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 2, (int)xs, 2, (int)ws);
     default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 3, (int)xs, 3, (int)ws);
-  }
-}
-
-// The first `left` of eight neighbouring results.
-template <int YT>
-__device__ inline void store8(void* Y, int64_t at, int left, floatx4 lo, floatx4 hi) {
-  if constexpr (YT == GPTQ_F32) {
-    float* y = static_cast<float*>(Y) + at;
-    if (left >= 8) {
-      reinterpret_cast<floatx4_a4*>(y)[0] = lo;
-      reinterpret_cast<floatx4_a4*>(y)[1] = hi;
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < left) y[i] = i < 4 ? lo[i & 3] : hi[i & 3];
-  } else {
-    uint16_t* y = static_cast<uint16_t*>(Y) + at;
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = i < 2 ? lo[2 * i] : hi[2 * i - 4], b = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
-      if constexpr (YT == GPTQ_F16)
-        v[i] = __builtin_bit_cast(uint32_t, halfx2{(_Float16)a, (_Float16)b});
-      else
-        v[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-    }
-    if (left >= 8) {
-      *reinterpret_cast<u32x4_a2*>(y) = v;
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < left) y[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
   }
 }
 
@@ -1425,22 +1317,6 @@ __device__ inline bool big_tile_product(const MxOperands& p, const TileGrid& tg,
   return true;
 }
 
-// Workgroup -> (split, tile of X rows, tile of W rows); false: none.
-__device__ inline bool tile_of_workgroup(const MxOperands& p, const TileGrid& tg, int BM, int BN, int& split,
-                                         TokenTile& tile, int& r0) {
-  const int64_t tiles = (int64_t)tg.row_tiles * tg.tok_tiles;
-  const int64_t item = xcd_contiguous(blockIdx.x, gridDim.x);
-  if (item >= tiles * tg.splits) return false;
-  split = (int)(item / tiles);
-  const int t = (int)(item % tiles);
-  const int band = t / (kTokBand * tg.row_tiles);
-  const int in_band = min(kTokBand, tg.tok_tiles - band * kTokBand);
-  const int rest = t - band * kTokBand * tg.row_tiles;
-  tile = find_tile(p, band * kTokBand + rest % in_band, BN);
-  r0 = rest / in_band * BM;
-  return tile.valid;
-}
-
 // Two waves per SIMD where the accumulators leave room for them.
 template <int XT, int WR, int WC, int RB, int CB, int PB, bool DIRECT, bool WL>
 __global__ __launch_bounds__(64 * WR * WC, RB * CB <= 8 ? 2 : 1) void mx_tile_kernel(MxOperands p, TileGrid tg) {
@@ -1466,43 +1342,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void mx_big_tile_kernel(MxOperands
   }
 }
 
-// Adds the splits' sums in order, four columns a thread and four splits' loads
-// in flight (one at a time they cost a memory latency a split).  All workgroups
-// lie along x, a row of X after the other: there can be more rows than a grid
-// has along y (65535).  Every row has a sum: products grouped by expert are never
-// split.
-constexpr int kJoinCols = 1024;              // columns of Y a workgroup
-__global__ __launch_bounds__(kJoinCols / 4) void mx_join_kernel(MxOperands p, TileGrid tg) {
-  const int chunks = (p.m + kJoinCols - 1) / kJoinCols;
-  const int x = (int)(blockIdx.x / chunks), r = (int)(blockIdx.x % chunks) * kJoinCols + (int)threadIdx.x * 4;
-  if (r >= p.m) return;
-  const int64_t total = (int64_t)p.rows * p.m;
-  const float* part = tg.part + (int64_t)x * p.m;
-  const int left = p.m - r;
-  auto load = [&](int split) {
-    const float* at = part + min(split, tg.splits - 1) * total;
-    if (left >= 4) return *reinterpret_cast<const floatx4_a4*>(at + r);
-    return floatx4{at[r], at[min(r + 1, p.m - 1)], at[min(r + 2, p.m - 1)], 0.f};
-  };
-  floatx4 v = load(0);
-  for (int s = 1; s < tg.splits; s += 4) {
-    floatx4 t[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = load(s + i);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (s + i < tg.splits) v += t[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < left) store_y(p, (int64_t)x * p.ldy + r + i, v[i]);
-}
-
-// Tiles that the rows can form at most: every expert with rows may end in a
-// partial tile.
-int64_t max_tiles(int64_t rows, int64_t experts, bool grouped, int tile) {
-  return grouped ? rows / tile + std::min(experts, rows) : ceil_div(rows, tile);
-}
+__global__ __launch_bounds__(kJoinCols / 4) void mx_join_kernel(MxOperands p, TileGrid tg) { join_splits(p, tg); }
 
 // What a product runs on, from its sizes alone.
 enum Kind {
@@ -1514,13 +1354,9 @@ struct Plan {
   Kind kind;
   int splits;                                // of the columns, tiles only
 };
-constexpr int kSplitCols = 256;              // a split is a multiple of this
 
-// Products on tiles: the shape and the splits with the least time by this model,
-// in us: a launch, 256 columns of every round of workgroups, each round with as
-// many as the CUs hold at once, and the join with its splits' sums.  A round's
-// time grows from `one` (a workgroup a CU) to `full` along a square root (a few
-// CUs with two already hold the rest up).  Fitted to 180 sizes of 16-bit X from
+// Products on tiles: the shape and the splits with the least time by the model of
+// choose_tiles.  Fitted to 180 sizes of 16-bit X from
 // 8 x 1024 x 2048 to 2048 x 49152 x 12288 and 50 of microscaled X: what it
 // chooses takes 1.02 and 1.01 times the fastest's time in the mean, 1.3 and 1.13
 // at worst.  It knows sizes only: rows that are not 16-byte aligned take longer (2448
@@ -1535,11 +1371,6 @@ constexpr int kSplitCols = 256;              // a split is a multiple of this
 // 28, 256 x 256 32; 4096 x 12288 x 12288 on 256 x 256 286, 128 x 128 391.  128 x
 // 128 tiles of 16-bit X and 256 x 128 of microscaled X were the fastest of no size
 // by more than a tenth: they are not built.
-struct TileShape {
-  Kind kind;
-  int bm, bn, per_cu;
-  double launch, one, full;
-};
 constexpr TileShape kTileShapes[] = {
     {kTile128x32, 128, 32, 2, 3.3, 0.74, 1.3},
     {kTile128x64, 128, 64, 2, 3.5, 1.3, 2.2},
@@ -1561,26 +1392,8 @@ constexpr TileShape kScaledTileShapes[] = {
 constexpr TileShape kGroupedTileShapes[] = {kTileShapes[0], kTileShapes[2]};
 template <size_t N>
 Plan tile_plan(const TileShape (&shapes)[N], int64_t m, int64_t n, int64_t rows, int64_t experts = 0) {
-  constexpr double kJoin = 4.3, kJoinBytes = 0.22e-6;
-  const int max_splits = experts > 0 ? 1 : 16;
-  Plan best{kTile128x32, 1};
-  double least = std::numeric_limits<double>::infinity();
-  const double parts = (double)m * (double)rows * 8.0;       // bytes that a split's sums move
-  for (const TileShape& s : shapes) {
-    const int64_t partial = (std::min(experts, rows) + 1) / 2, held = 256 * s.per_cu;
-    const int64_t tiles = ceil_div(m, s.bm) * (ceil_div(rows, s.bn) + partial);
-    for (int splits = 1; splits <= max_splits && (splits == 1 || n >= (int64_t)splits * kSplitCols); ++splits) {
-      const int64_t groups = tiles * splits, rest = groups % held;
-      double t = (double)(groups / held) * s.full;
-      if (rest > 256) t += s.one + (s.full - s.one) * std::sqrt((double)(rest - 256) * (1.0 / 256));
-      else if (rest > 0) t += s.one;
-      t = s.launch + t * (double)ceil_div(ceil_div(n, splits), kSplitCols);
-      if (splits > 1) t += kJoin + kJoinBytes * splits * parts;
-      if (t < least) least = t, best = Plan{s.kind, splits};
-      if (groups > 2 * held) break;          // more splits only add sums
-    }
-  }
-  return best;
+  const TileChoice c = choose_tiles(shapes, m, n, rows, experts, 4.3, 0.22e-6);
+  return Plan{(Kind)c.kind, c.splits};
 }
 
 // The row kernels, whose waves split the columns, take products small enough for

@@ -26,18 +26,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kMaxSlabGroups = (int64_t)1 << 30;   // groups of 8 columns per launch
 
-// Division by the groups per row: q = (g * mul) >> shift for g < 2^31.
-struct GroupDiv {
-  uint32_t mul;
-  int shift;
-};
-
-inline GroupDiv group_div(uint32_t d) {
-  int L = 0;
-  while (((uint64_t)1 << L) < d) ++L;
-  return GroupDiv{(uint32_t)((((uint64_t)1 << (31 + L)) + d - 1) / d), 31 + L};
-}
-
 // Eight elements as loaded, the largest absolute bit pattern among them, the
 // scale byte of a block maximum, the packed word and the dequantized values.
 template <int DT> struct Mx8;
@@ -131,16 +119,6 @@ template <> struct Mx8<GPTQ_BF16> {
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
   }
-};
-
-// Element storage, and 16 bytes of it at any element-aligned address.
-template <int DT> struct Elem {
-  typedef uint16_t type;
-  typedef u32x4_a2 vec;
-};
-template <> struct Elem<GPTQ_F32> {
-  typedef uint32_t type;
-  typedef u32x4_a4 vec;
 };
 
 // groups: groups of 8 columns in this launch, `per_row` (a multiple of 4: whole
