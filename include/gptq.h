@@ -499,6 +499,86 @@ gptq_status gptq_mx_scaled_gemm(const uint32_t* packed, int64_t m, int64_t n, in
                                 int64_t ld_xscales, void* Y, int y_dtype, int64_t ldy,
                                 void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Block-scaled 8-bit floats (FP8 with a scale for each block of 128), a format
+ * between the 4-bit ones above and 16 bits (same sources: a low-bit grid whose
+ * groups have their own scaling factor).
+ *   codes   e4m3, one byte an element: bit 7 the sign, bits 3-6 the exponent
+ *           (bias 7; 0: steps of 2^-9), bits 0-2 the mantissa; 448 the largest
+ *           value, 0x7F and 0xFF NaN, no infinities.
+ *   scales  float32, for every 128 consecutive columns of one row (activations)
+ *           or of 128 consecutive rows (weights); the last blocks may be smaller.
+ * Sizes for all calls: 0 <= n <= 2^20, others return GPTQ_ERR_UNSUPPORTED.
+ * Rows may start at any address; products are fastest where the rows of both
+ * operands are 16-byte aligned, and several times slower for many rows where
+ * neighbouring rows of an operand lie more than 4 MiB apart.
+ * ---------------------------------------------------------------------- */
+
+/* Round-to-nearest quantization of `experts` matrices W (m x n each):
+ *   scale = max|w| / 448 of the block, rounded to float32; at least 2^-126, and
+ *           1 for a block of zeros,
+ *   code  = the e4m3 value nearest to the quotient w / scale (the quotient
+ *           itself, not a rounded one), ties to the even code.
+ * A block that holds a NaN or an infinity gets a NaN scale and codes 0 (all its
+ * values are NaN).
+ *   W       device, element type w_dtype, leading dimension ldw >= n, matrices
+ *           stride_w elements apart (strides count with experts > 1 only).
+ *   block_rows  rows that share a scale: 1 or 128.
+ *   codes   device output, m x ld_codes bytes a matrix, ld_codes >= n.
+ *   scales  device output, ceil(m / block_rows) x ld_scales float32 a matrix,
+ *           ld_scales >= ceil(n / 128).
+ *   Wq      device output (ldwq >= n, stride_wq) of code * scale in w_dtype,
+ *           rounded to float32 first, or NULL.
+ * Outputs must not overlap W or one another, nor the outputs of two matrices.
+ * m < 2^31, experts <= GPTQ_MX_MAX_EXPERTS. */
+gptq_status gptq_block_quantize(const void* W, int w_dtype, int64_t experts, int64_t m, int64_t n, int64_t ldw,
+                              int64_t stride_w, int block_rows, uint8_t* codes, int64_t ld_codes,
+                              int64_t stride_codes, float* scales, int64_t ld_scales, int64_t stride_scales,
+                              void* Wq, int64_t ldwq, int64_t stride_wq, void* stream);
+
+/* Y[b, r] = sum_j xs[b, j] ws[r / 128, j] sum_{k in block j} w[r, k] x[b, k],
+ * any batch >= 0: both operands in 8 bits, on the matrix cores as stored.
+ *   codes, scales      device, weights with blocks of 128 x 128 (block_rows 128).
+ *   x_codes, x_scales  device, batch rows with blocks of 128 columns (block_rows 1).
+ *   Y       device, batch x m output (ldy >= m), y_dtype GPTQ_F32, GPTQ_F16 or
+ *           GPTQ_BF16.  Must not overlap the inputs.
+ *   ws      device workspace of gptq_block_gemm_ws_bytes(m, n, batch, 1) bytes
+ *           (NULL allowed when that is 0), 4-byte aligned, in use until the
+ *           call's work on `stream` is done: calls that may run at the same time
+ *           (two streams, two captured graphs) need one each.
+ * The same call gives the same bits: the order of the sums depends on sizes,
+ * strides and alignment alone.  With S = sum |terms|, the error before the one
+ * rounding to y_dtype is at most
+ *     (n/256 + 40) 2^-23 S + n 2^-149
+ * for a float32 Y, unless S passes float32's range.  A 16-bit Y of more than 16
+ * rows may come from the matrix instructions on 8-bit operands, twice as fast,
+ * which cut each product at 2^-13 of the largest of eight neighbouring ones: up to
+ * 2^-10 S' more (S' is S with non-zero codes below 2^-6 counted as 2^-6; 1.4e-5 of
+ * the results for quantized normal data).  The product of two scales is taken in
+ * float32: one outside its range counts as infinite (or as rounded to a
+ * subnormal number).  Non-finite scales and NaN codes make the outputs that they
+ * enter non-finite.  With n = 0, Y is 0.
+ * m, batch <= GPTQ_MX_MAX_ROWS. */
+size_t gptq_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, int64_t experts);
+gptq_status gptq_block_gemm(const uint8_t* codes, int64_t m, int64_t n, int64_t ld_codes, const float* scales,
+                          int64_t ld_scales, const uint8_t* x_codes, int64_t batch, int64_t ld_xcodes,
+                          const float* x_scales, int64_t ld_xscales, void* Y, int y_dtype, int64_t ldy,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* The same product grouped by expert: rows offsets[e] .. offsets[e+1] - 1 of X
+ * with expert e's weights; offsets, rows outside all experts and descending
+ * offsets as for gptq_mx_gemm_grouped.
+ *   codes, scales   device, `experts` matrices: expert e's first row is at codes +
+ *                   e * stride_codes, its first block at scales + e * stride_scales
+ *                   (stride_codes >= m ld_codes, stride_scales >= ceil(m / 128)
+ *                   ld_scales).
+ *   ws      gptq_block_gemm_ws_bytes(m, n, rows, experts) bytes, as above. */
+gptq_status gptq_block_gemm_grouped(const uint8_t* codes, int64_t experts, int64_t m, int64_t n, int64_t ld_codes,
+                                  int64_t stride_codes, const float* scales, int64_t ld_scales,
+                                  int64_t stride_scales, const uint8_t* x_codes, int64_t rows, int64_t ld_xcodes,
+                                  const float* x_scales, int64_t ld_xscales, const int32_t* offsets, void* Y,
+                                  int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

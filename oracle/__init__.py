@@ -49,4 +49,16 @@ from .mx_oracle import (  # noqa: F401,E402
     mx_nearest_code,
     mx_quantize,
 )
+from .fp8_oracle import (  # noqa: F401,E402
+    FP8_BLOCK,
+    FP8_VALUES,
+    fp8_blocks,
+    fp8_dequantize,
+    fp8_error_bound,
+    fp8_matmul,
+    fp8_nearest_code,
+    fp8_quantize,
+    fp8_spread,
+    fp8_stored_bound,
+)
 from . import decoder_oracle  # noqa: F401,E402

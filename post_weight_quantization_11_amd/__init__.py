@@ -8,6 +8,9 @@ from ._lib import (  # noqa: F401
     bits_for_levels,
     gptaq_quantize_linear,
     gptq_asym_target,
+    gptq_block_gemm,
+    gptq_block_gemm_grouped,
+    gptq_block_quantize,
     gptq_dequant_gemm,
     gptq_dequant_gemv,
     gptq_hessian_accumulate,

@@ -49,11 +49,16 @@ EXPORTS = (
     "gptq_mx_gemm",
     "gptq_mx_gemm_grouped",
     "gptq_mx_scaled_gemm",
+    "gptq_block_quantize",
+    "gptq_block_gemm_ws_bytes",
+    "gptq_block_gemm",
+    "gptq_block_gemm_grouped",
 )
 
 GEMV_MAX_BATCH = 8   # X rows per pass of the VALU product kernel
 LOWRANK_MAX_RANK = 64
 MX_BLOCK = 32        # columns that share a scale of a microscaled matrix
+FP8_BLOCK = 128      # columns (and rows of a weight block) that share a scale of an 8-bit matrix
 
 _lib = None
 
@@ -132,6 +137,15 @@ def load(path: str = LIB_PATH):
                                          vp, sz, vp]
     lib.gptq_mx_scaled_gemm.restype = C
     lib.gptq_mx_scaled_gemm.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, C, i64, vp, sz, vp]
+    lib.gptq_block_quantize.restype = C
+    lib.gptq_block_quantize.argtypes = [vp, C, i64, i64, i64, i64, i64, C, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp]
+    lib.gptq_block_gemm_ws_bytes.restype = sz
+    lib.gptq_block_gemm_ws_bytes.argtypes = [i64, i64, i64, i64]
+    lib.gptq_block_gemm.restype = C
+    lib.gptq_block_gemm.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, C, i64, vp, sz, vp]
+    lib.gptq_block_gemm_grouped.restype = C
+    lib.gptq_block_gemm_grouped.argtypes = [vp, i64, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, C,
+                                          i64, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -432,10 +446,10 @@ def _mx_output(torch, Y, y_dtype, rows: int, m: int, device):
     return Y, code, _mx_rows(Y, "Y", dtype, rows, m, device)
 
 
-def _mx_workspace(ws, m: int, n: int, rows: int, experts: int, device):
+def _mx_workspace(ws, m: int, n: int, rows: int, experts: int, device, query="gptq_mx_gemm_ws_bytes"):
     """(the workspace that stays alive for the call, its address, its size)."""
     if ws is None:
-        need = _lib.gptq_mx_gemm_ws_bytes(m, n, rows, experts)
+        need = getattr(_lib, query)(m, n, rows, experts)
         if need == 0:
             return None, None, 0
         ws = _workspace(need, device)
@@ -455,6 +469,12 @@ def _mx_x(torch, X):
         if unit == 1 or n <= 1:
             return rows, n, (ld if rows > 1 else n), code
     raise ValueError("X must be a 2-D device tensor with unit column stride")
+
+
+def _mx_offsets(torch, offsets, experts: int, device):
+    if offsets.dtype is not torch.int32 or offsets.shape != (experts + 1,) or offsets.device != device or \
+            not offsets.is_contiguous():
+        raise ValueError(f"offsets must be {experts + 1} contiguous int32 on {device}")
 
 
 def _mx_folded(t, name: str, dtype, lead, cols: int, device) -> int:
@@ -576,9 +596,7 @@ def gptq_mx_gemm_grouped(packed, scales, X, offsets, Y=None, y_dtype=None, ws=No
     dev = X.device
     ldp, stride_p = _mx_stack(packed, "packed", torch.int32, experts, m, -(-n // 8), dev)
     lds, stride_s = _mx_stack(scales, "scales", torch.uint8, experts, m, -(-n // MX_BLOCK), dev)
-    if offsets.dtype is not torch.int32 or offsets.shape != (experts + 1,) or offsets.device != dev or \
-            not offsets.is_contiguous():
-        raise ValueError(f"offsets must be {experts + 1} contiguous int32 on {dev}")
+    _mx_offsets(torch, offsets, experts, dev)
     Y, yc, ldy = _mx_output(torch, Y, y_dtype, rows, m, dev)
     ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, rows, experts, dev)
     rc = lib.gptq_mx_gemm_grouped(packed.data_ptr(), experts, m, n, ldp, stride_p, scales.data_ptr(), lds, stride_s,
@@ -613,6 +631,146 @@ def gptq_mx_scaled_gemm(packed, scales, x_packed, x_scales, n: int, Y=None, y_dt
                                  torch._C._cuda_getCurrentRawStream(dev.index))
     if rc:
         _check(rc, "gptq_mx_scaled_gemm")
+    return Y
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floats with a scale for each block of 128.
+# ---------------------------------------------------------------------------
+def _fp8_matrix(t, name: str, dtype, shape, device):
+    """(leading dimension, stride of a matrix) of a matrix, or of a stack of them."""
+    if len(shape) == 3:
+        return _mx_stack(t, name, dtype, *shape, device)
+    return _mx_rows(t, name, dtype, *shape, device), 0
+
+
+def _fp8_operand(t, name: str):
+    if t.dtype is not _torch().float8_e4m3fn or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D float8_e4m3fn tensor")
+    return t.shape
+
+
+def gptq_block_quantize(W, block_rows: int = 1, want_wq: bool = False, out=None, stream=None):
+    """Rounds W (m x n, or a stack experts x m x n; float32, float16 or
+    bfloat16) to 8-bit floats (e4m3) with a float32 scale for every 128 columns
+    of a row (block_rows 1: activations) or of 128 rows (block_rows 128:
+    weights).
+
+    Returns dict(codes (W's shape, float8_e4m3fn), scales (... x ceil(m /
+    block_rows) x ceil(n / 128)), Wq (W's shape and dtype, code times scale) or
+    None).  Rows of codes that are allocated here start at multiples of 16 bytes
+    (their leading dimension is n rounded up), as the products read them
+    fastest.  `out` may hold any of those tensors; it gets the others, Wq only
+    with want_wq."""
+    torch = _torch()
+    lib = load()
+    ctx = _mx_elsewhere(W, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_block_quantize(W, block_rows, want_wq, out)
+    if W.dim() not in (2, 3):
+        raise ValueError("W must be a 2-D or 3-D device tensor")
+    code = GPTQ_F32 if W.dtype is torch.float32 else GPTQ_BF16 if W.dtype is torch.bfloat16 else \
+        GPTQ_F16 if W.dtype is torch.float16 else None
+    if code is None:
+        raise ValueError("W must be float32, float16 or bfloat16")
+    if block_rows != 1 and block_rows != FP8_BLOCK:
+        raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}")
+    shape, dev = W.shape, W.device
+    *lead, m, n = shape
+    ldw, stride_w = _fp8_matrix(W, "W", W.dtype, shape, dev)
+    if out is None:
+        out = {}
+    codes, scales, wq = out.get("codes"), out.get("scales"), out.get("Wq")
+    if codes is None:
+        ldc = -(-n // 16) * 16
+        stride_c = m * ldc
+        codes = torch.empty((*lead, m, ldc), dtype=torch.float8_e4m3fn, device=dev)
+        if ldc != n:
+            codes = codes[..., :n]
+    else:
+        ldc, stride_c = _fp8_matrix(codes, "codes", torch.float8_e4m3fn, shape, dev)
+    row_blocks, blocks = (m if block_rows == 1 else -(-m // FP8_BLOCK)), -(-n // FP8_BLOCK)
+    if scales is None:
+        lds, stride_s = blocks, row_blocks * blocks
+        scales = torch.empty((*lead, row_blocks, blocks), dtype=torch.float32, device=dev)
+    else:
+        lds, stride_s = _fp8_matrix(scales, "scales", torch.float32, (*lead, row_blocks, blocks), dev)
+    ldq, stride_q = n, m * n
+    if wq is not None:
+        ldq, stride_q = _fp8_matrix(wq, "Wq", W.dtype, shape, dev)
+    elif want_wq:
+        wq = torch.empty(shape, dtype=W.dtype, device=dev)
+    rc = lib.gptq_block_quantize(W.data_ptr(), code, lead[0] if lead else 1, m, n, ldw, stride_w, block_rows,
+                               codes.data_ptr(), ldc, stride_c, scales.data_ptr(), lds, stride_s,
+                               None if wq is None else wq.data_ptr(), ldq, stride_q,
+                               torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "gptq_block_quantize")
+    out.update(codes=codes, scales=scales, Wq=wq)
+    return out
+
+
+def gptq_block_gemm(codes, scales, x_codes, x_scales, Y=None, y_dtype=None, ws=None, stream=None):
+    """Y (batch x m; float32, or y_dtype) = Xhat What^T with both operands in
+    8-bit floats: codes m x n and scales ceil(m / 128) x ceil(n / 128) of the
+    weights (gptq_block_quantize with block_rows 128), x_codes batch x n and
+    x_scales batch x ceil(n / 128) of X (block_rows 1)."""
+    torch = _torch()
+    lib = load()
+    ctx = _mx_elsewhere(codes, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_block_gemm(codes, scales, x_codes, x_scales, Y, y_dtype, ws)
+    m, n = _fp8_operand(codes, "codes")
+    batch, _ = _fp8_operand(x_codes, "x_codes")
+    dev, f8, blocks = codes.device, codes.dtype, -(-n // FP8_BLOCK)
+    ldc = _mx_rows(codes, "codes", f8, m, n, dev)
+    lds = _mx_rows(scales, "scales", torch.float32, -(-m // FP8_BLOCK), blocks, dev)
+    ldx = _mx_rows(x_codes, "x_codes", f8, batch, n, dev)
+    ldxs = _mx_rows(x_scales, "x_scales", torch.float32, batch, blocks, dev)
+    Y, yc, ldy = _mx_output(torch, Y, y_dtype, batch, m, dev)
+    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, batch, 1, dev, "gptq_block_gemm_ws_bytes")
+    rc = lib.gptq_block_gemm(codes.data_ptr(), m, n, ldc, scales.data_ptr(), lds, x_codes.data_ptr(), batch, ldx,
+                           x_scales.data_ptr(), ldxs, Y.data_ptr(), yc, ldy, ws_at, ws_bytes,
+                           torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "gptq_block_gemm")
+    return Y
+
+
+def gptq_block_gemm_grouped(codes, scales, x_codes, x_scales, offsets, Y=None, y_dtype=None, ws=None, stream=None):
+    """Rows offsets[e] .. offsets[e+1] - 1 of X (rows x n, sorted by expert)
+    times expert e's weights: codes experts x m x n, scales experts x ceil(m /
+    128) x ceil(n / 128), x_codes and x_scales as for gptq_block_gemm, offsets
+    experts + 1 int32 (on the device; not read on the host).  Returns Y (rows x
+    m); rows of Y that belong to no expert are left as they were (unset when Y is
+    allocated here)."""
+    torch = _torch()
+    lib = load()
+    ctx = _mx_elsewhere(codes, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_block_gemm_grouped(codes, scales, x_codes, x_scales, offsets, Y, y_dtype, ws)
+    f8 = torch.float8_e4m3fn
+    if codes.dim() != 3 or codes.dtype is not f8:
+        raise ValueError("codes must be a float8_e4m3fn tensor experts x m x n")
+    experts, m, n = codes.shape
+    rows, _ = _fp8_operand(x_codes, "x_codes")
+    dev, blocks = codes.device, -(-n // FP8_BLOCK)
+    ldc, stride_c = _mx_stack(codes, "codes", f8, experts, m, n, dev)
+    lds, stride_s = _mx_stack(scales, "scales", torch.float32, experts, -(-m // FP8_BLOCK), blocks, dev)
+    ldx = _mx_rows(x_codes, "x_codes", f8, rows, n, dev)
+    ldxs = _mx_rows(x_scales, "x_scales", torch.float32, rows, blocks, dev)
+    _mx_offsets(torch, offsets, experts, dev)
+    Y, yc, ldy = _mx_output(torch, Y, y_dtype, rows, m, dev)
+    ws, ws_at, ws_bytes = _mx_workspace(ws, m, n, rows, experts, dev, "gptq_block_gemm_ws_bytes")
+    rc = lib.gptq_block_gemm_grouped(codes.data_ptr(), experts, m, n, ldc, stride_c, scales.data_ptr(), lds, stride_s,
+                                   x_codes.data_ptr(), rows, ldx, x_scales.data_ptr(), ldxs, offsets.data_ptr(),
+                                   Y.data_ptr(), yc, ldy, ws_at, ws_bytes,
+                                   torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "gptq_block_gemm_grouped")
     return Y
 
 
