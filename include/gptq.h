@@ -579,6 +579,75 @@ gptq_status gptq_block_gemm_grouped(const uint8_t* codes, int64_t experts, int64
                                   const float* x_scales, int64_t ld_xscales, const int32_t* offsets, void* Y,
                                   int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Mixtures of experts: the router, and a whole layer of experts for few tokens.
+ * ---------------------------------------------------------------------- */
+#define GPTQ_MOE_MAX_EXPERTS 1024
+#define GPTQ_MOE_MAX_TOPK 16
+#define GPTQ_MOE_MAX_TOKENS 64       /* of gptq_mx_moe and gptq_block_moe */
+
+/* Each token's topk largest logits, in descending order (ties to the lowest
+ * expert), and the pairs of token and expert sorted by expert: what products
+ * grouped by expert read.
+ *   logits   device, tokens x experts (ld_logits >= experts), element type l_dtype.
+ *            NaN counts as -inf; both zeros are equal.
+ *   ids      device int32 output, tokens x topk (dense): the experts.
+ *   weights  device float32 output, tokens x topk: their softmax probabilities over
+ *            all experts, or with renormalize != 0 divided by their sum (the softmax
+ *            over the chosen ones).  +inf logits share the probability; a token whose
+ *            logits are all -inf has experts 0 .. topk - 1 with weights 0.
+ *   offsets  device int32 output, experts + 1: pair order[i] belongs to expert e for
+ *            offsets[e] <= i < offsets[e + 1].
+ *   order    device int32 output, tokens * topk: numbers of pairs (token t's j-th
+ *            expert is pair t * topk + j), ascending inside an expert.
+ *            offsets and order may both be NULL.
+ * 1 <= topk <= min(experts, GPTQ_MOE_MAX_TOPK), experts <= GPTQ_MOE_MAX_EXPERTS,
+ * tokens <= GPTQ_MX_MAX_ROWS.  With no tokens the offsets are 0.  No workspace.
+ * Sums are float32.  A weight is off by at most (g/2 + 8) 2^-23 of it, g being how
+ * far its logit lies below the largest (the difference rounds), and by 2^-126. */
+gptq_status gptq_moe_route(const void* logits, int l_dtype, int64_t tokens, int64_t experts, int64_t ld_logits,
+                           int topk, int renormalize, int32_t* ids, float* weights, int32_t* offsets,
+                           int32_t* order, void* stream);
+
+/* A layer of experts for up to GPTQ_MOE_MAX_TOKENS tokens (more take
+ * gptq_moe_route and the products grouped by expert), in two launches:
+ *   Y[t] = sum_j weights[t, j] D_e (silu(G_e X[t]) * (U_e X[t])),  e = ids[t, j],
+ * with ids and weights as gptq_moe_route gives them for the logits, and
+ * silu(a) = a / (1 + exp(-a)).
+ *   gate_up   device, `experts` matrices of 2 f rows and d columns: the rows of G,
+ *             then those of U.  down: `experts` matrices of d rows and f columns.
+ *             Leading dimensions and strides between matrices in elements of the
+ *             arrays (strides >= rows * leading dimension; they count with experts > 1
+ *             only).  gptq_mx_moe: packed words and scale bytes as gptq_mx_quantize
+ *             writes them.  gptq_block_moe: codes and float32 scales as
+ *             gptq_block_quantize writes them with block_rows 128 (of the stack of 2 f
+ *             rows).  Experts that no token takes are not read.
+ *   X         device, tokens x d (ldx >= d), x_dtype GPTQ_F16 or GPTQ_BF16.
+ *   Y         device, tokens x d output (ldy >= d), any of the three types.  Must not
+ *             overlap the inputs.
+ *   ws        device workspace of gptq_moe_ws_bytes bytes, 16-byte aligned, in use until
+ *             the call's work on `stream` is done: calls that may run at the same time
+ *             (two streams, two captured graphs) need one each.
+ * Products are exact and sums float32; between the two launches values keep their
+ * 24 bits.  The same call gives the same bits.  A pair whose weight is 0 adds
+ * nothing, whatever its product.  d <= 2^20, f <= 2^19, f >= 1; experts and topk as
+ * for gptq_moe_route. */
+size_t gptq_moe_ws_bytes(int64_t tokens, int64_t experts, int topk, int64_t d, int64_t f);
+gptq_status gptq_mx_moe(const uint32_t* gate_up, int64_t ld_gate_up, int64_t stride_gate_up,
+                        const uint8_t* gate_up_scales, int64_t ld_gate_up_scales, int64_t stride_gate_up_scales,
+                        const uint32_t* down, int64_t ld_down, int64_t stride_down, const uint8_t* down_scales,
+                        int64_t ld_down_scales, int64_t stride_down_scales, int64_t experts, int64_t d, int64_t f,
+                        const void* X, int x_dtype, int64_t tokens, int64_t ldx, const void* logits, int l_dtype,
+                        int64_t ld_logits, int topk, int renormalize, void* Y, int y_dtype, int64_t ldy, void* ws,
+                        size_t ws_bytes, void* stream);
+gptq_status gptq_block_moe(const uint8_t* gate_up, int64_t ld_gate_up, int64_t stride_gate_up,
+                           const float* gate_up_scales, int64_t ld_gate_up_scales, int64_t stride_gate_up_scales,
+                           const uint8_t* down, int64_t ld_down, int64_t stride_down, const float* down_scales,
+                           int64_t ld_down_scales, int64_t stride_down_scales, int64_t experts, int64_t d, int64_t f,
+                           const void* X, int x_dtype, int64_t tokens, int64_t ldx, const void* logits, int l_dtype,
+                           int64_t ld_logits, int topk, int renormalize, void* Y, int y_dtype, int64_t ldy, void* ws,
+                           size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

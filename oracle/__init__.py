@@ -61,4 +61,11 @@ from .fp8_oracle import (  # noqa: F401,E402
     fp8_spread,
     fp8_stored_bound,
 )
+from .moe_oracle import (  # noqa: F401,E402
+    moe_layer,
+    moe_layer_and_bound,
+    moe_route,
+    moe_weight_bound,
+    silu,
+)
 from . import decoder_oracle  # noqa: F401,E402

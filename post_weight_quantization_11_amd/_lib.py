@@ -53,6 +53,10 @@ EXPORTS = (
     "gptq_block_gemm_ws_bytes",
     "gptq_block_gemm",
     "gptq_block_gemm_grouped",
+    "gptq_moe_route",
+    "gptq_moe_ws_bytes",
+    "gptq_mx_moe",
+    "gptq_block_moe",
 )
 
 GEMV_MAX_BATCH = 8   # X rows per pass of the VALU product kernel
@@ -146,6 +150,14 @@ def load(path: str = LIB_PATH):
     lib.gptq_block_gemm_grouped.restype = C
     lib.gptq_block_gemm_grouped.argtypes = [vp, i64, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, C,
                                           i64, vp, sz, vp]
+    lib.gptq_moe_route.restype = C
+    lib.gptq_moe_route.argtypes = [vp, C, i64, i64, i64, C, C, vp, vp, vp, vp, vp]
+    lib.gptq_moe_ws_bytes.restype = sz
+    lib.gptq_moe_ws_bytes.argtypes = [i64, i64, C, i64, i64]
+    for f in (lib.gptq_mx_moe, lib.gptq_block_moe):
+        f.restype = C
+        f.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64, i64, vp, C, i64, i64, vp, C,
+                      i64, C, C, vp, C, i64, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -772,6 +784,126 @@ def gptq_block_gemm_grouped(codes, scales, x_codes, x_scales, offsets, Y=None, y
     if rc:
         _check(rc, "gptq_block_gemm_grouped")
     return Y
+
+
+# ---------------------------------------------------------------------------
+# Mixtures of experts.
+# ---------------------------------------------------------------------------
+def _moe_logits(torch, logits, tokens, topk: int):
+    """(experts, type code, leading dimension) of router logits."""
+    code = GPTQ_F32 if logits.dtype is torch.float32 else GPTQ_BF16 if logits.dtype is torch.bfloat16 else \
+        GPTQ_F16 if logits.dtype is torch.float16 else None
+    if code is None or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D device tensor of float32, float16 or bfloat16")
+    rows, experts = logits.shape
+    ld = _mx_rows(logits, "logits", logits.dtype, rows if tokens is None else tokens, experts, logits.device)
+    if not 1 <= topk <= experts:
+        raise ValueError(f"topk must be at least 1 and at most the {experts} experts")
+    return experts, code, ld
+
+
+def gptq_moe_route(logits, topk: int, renormalize: bool = True, out=None, stream=None):
+    """Routes tokens to experts: logits tokens x experts (float32, float16 or
+    bfloat16).  Returns dict(ids (tokens x topk int32, the experts of the largest
+    logits in descending order, ties to the lowest), weights (tokens x topk
+    float32, their softmax probabilities, with renormalize divided by their sum),
+    offsets (experts + 1 int32) and order (tokens * topk int32): pair order[i]
+    (token order[i] // topk) belongs to expert e for offsets[e] <= i < offsets[e +
+    1], as the products grouped by expert take them).  `out` may hold any of those
+    tensors (contiguous); it gets the others."""
+    torch = _torch()
+    lib = load()
+    ctx = _mx_elsewhere(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_moe_route(logits, topk, renormalize, out)
+    topk = int(topk)
+    experts, code, ld = _moe_logits(torch, logits, None, topk)
+    tokens, dev = logits.shape[0], logits.device
+    if out is None:
+        out = {}
+    got = []
+    for name, dtype, shape in (("ids", torch.int32, (tokens, topk)), ("weights", torch.float32, (tokens, topk)),
+                               ("offsets", torch.int32, (experts + 1,)), ("order", torch.int32, (tokens * topk,))):
+        t = out.get(name)
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        elif t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
+        got.append(t)
+    rc = lib.gptq_moe_route(logits.data_ptr(), code, tokens, experts, ld, topk, 1 if renormalize else 0,
+                            *(t.data_ptr() for t in got), torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, "gptq_moe_route")
+    out.update(ids=got[0], weights=got[1], offsets=got[2], order=got[3])
+    return out
+
+
+def _moe_layer(name: str, code_dtype, scale_dtype, sizes, gate_up, gate_up_scales, down, down_scales, X, logits, topk,
+               renormalize, Y, y_dtype, ws):
+    torch = _torch()
+    tokens, d, ldx, xc = _mx_x(torch, X)
+    dev, topk = X.device, int(topk)
+    if logits.device != dev:
+        raise ValueError(f"logits must be on {dev}")
+    experts, lc, ldl = _moe_logits(torch, logits, tokens, topk)
+    if gate_up.dim() != 3 or gate_up.shape[1] < 2 or gate_up.shape[1] % 2:
+        raise ValueError("gate_up must be experts x 2 f x columns")
+    f = gate_up.shape[1] // 2
+    args = []
+    for what, codes, scales, m, n in (("gate_up", gate_up, gate_up_scales, 2 * f, d), ("down", down, down_scales, d, f)):
+        words, rows, blocks = sizes(m, n)
+        args += [codes.data_ptr(), *_mx_stack(codes, what, code_dtype, experts, m, words, dev), scales.data_ptr(),
+                 *_mx_stack(scales, what + "_scales", scale_dtype, experts, rows, blocks, dev)]
+    Y, yc, ldy = _mx_output(torch, Y, y_dtype, tokens, d, dev)
+    if ws is None:
+        ws = _workspace(_lib.gptq_moe_ws_bytes(tokens, experts, topk, d, f), dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {dev}")
+    rc = getattr(_lib, name)(*args, experts, d, f, X.data_ptr(), xc, tokens, ldx, logits.data_ptr(), lc, ldl, topk,
+                             1 if renormalize else 0, Y.data_ptr(), yc, ldy, None if ws is None else ws.data_ptr(),
+                             0 if ws is None else ws.numel() * ws.element_size(),
+                             torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, name)
+    return Y
+
+
+def gptq_mx_moe(gate_up, gate_up_scales, down, down_scales, X, logits, topk: int, renormalize: bool = True, Y=None,
+                y_dtype=None, ws=None, stream=None):
+    """A whole layer of experts with microscaled weights for up to 64 tokens:
+    Y[t] = sum_j weights[t, j] D_e (silu(G_e X[t]) * (U_e X[t])), e = ids[t, j], ids
+    and weights as gptq_moe_route gives them for logits (tokens x experts).
+    gate_up: experts x 2 f x ceil(d/8) packed words (the rows of G, then those of U)
+    and experts x 2 f x ceil(d/32) scale bytes, down: experts x d x ceil(f/8) and
+    experts x d x ceil(f/32), as gptq_mx_quantize returns them for stacks; X tokens x
+    d float16 or bfloat16.  Returns Y (tokens x d; float32, or y_dtype)."""
+    torch = _torch()
+    load()
+    ctx = _mx_elsewhere(X, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_mx_moe(gate_up, gate_up_scales, down, down_scales, X, logits, topk, renormalize, Y, y_dtype, ws)
+    return _moe_layer("gptq_mx_moe", torch.int32, torch.uint8, lambda m, n: (-(-n // 8), m, -(-n // MX_BLOCK)),
+                      gate_up, gate_up_scales, down, down_scales, X, logits, topk, renormalize, Y, y_dtype, ws)
+
+
+def gptq_block_moe(gate_up, gate_up_scales, down, down_scales, X, logits, topk: int, renormalize: bool = True, Y=None,
+                   y_dtype=None, ws=None, stream=None):
+    """gptq_mx_moe with weights in block-scaled 8-bit floats: gate_up experts x 2 f x
+    d codes and experts x ceil(2 f/128) x ceil(d/128) scales, down experts x d x f
+    and experts x ceil(d/128) x ceil(f/128), as gptq_block_quantize returns them for
+    stacks with block_rows 128."""
+    torch = _torch()
+    load()
+    ctx = _mx_elsewhere(X, stream)
+    if ctx is not None:
+        with ctx:
+            return gptq_block_moe(gate_up, gate_up_scales, down, down_scales, X, logits, topk, renormalize, Y, y_dtype,
+                                  ws)
+    return _moe_layer("gptq_block_moe", torch.float8_e4m3fn, torch.float32,
+                      lambda m, n: (n, -(-m // FP8_BLOCK), -(-n // FP8_BLOCK)), gate_up, gate_up_scales, down,
+                      down_scales, X, logits, topk, renormalize, Y, y_dtype, ws)
 
 
 def gptq_asym_target(W, Hc, U, perm=None, Wt=None, ws=None, stream=None):

@@ -14,11 +14,6 @@ constexpr int kFp8Block = 128;               // columns (and rows of a weight bl
 constexpr float kFp8Max = 448.f;
 constexpr int64_t kFp8MaxCols = 1 << 20;     // keeps in-row offsets far below 32 bits
 
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
-typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
-typedef int intx8 __attribute__((ext_vector_type(8)));
-
 // Eight codes (a half of four words) as bfloat16 numbers, which hold them exactly.
 __device__ inline bf16x8 fp8_widen8(u32x4 v, int half) {
   const uint32_t lo = v[2 * half], hi = v[2 * half + 1];

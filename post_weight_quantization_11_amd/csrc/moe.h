@@ -1,0 +1,117 @@
+// Device helpers of the expert router: the k largest of a token's logits and their
+// softmax probabilities, one wave a token.
+#pragma once
+
+#include "common.h"
+
+namespace gptq {
+
+constexpr int kMoeMaxExperts = GPTQ_MOE_MAX_EXPERTS, kMoeMaxTopk = GPTQ_MOE_MAX_TOPK;
+constexpr int kRouteRegs = kMoeMaxExperts / 64;
+
+// Logits as unsigned numbers in the same order; both zeros are one number, and a
+// NaN counts as -inf.  Experts that do not exist have 0, below every logit.
+constexpr uint32_t kRouteLowest = 0x007FFFFFu;              // -inf
+__device__ inline uint32_t route_key(float l) {
+  const uint32_t b = __float_as_uint(l + 0.f);
+  if (l != l) return kRouteLowest;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ inline float route_logit(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+// The largest of the 64 lanes' numbers, in every lane: four steps inside rows of
+// sixteen lanes, two across them.
+__device__ inline uint32_t wave_max(uint32_t x) {
+#define GPTQ_MAX_STEP(ctrl) \
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, ctrl, 0xF, 0xF, false))
+  GPTQ_MAX_STEP(0x111);                      // row_shr 1, 2, 4, 8
+  GPTQ_MAX_STEP(0x112);
+  GPTQ_MAX_STEP(0x114);
+  GPTQ_MAX_STEP(0x118);
+  GPTQ_MAX_STEP(0x142);                      // row_bcast 15, 31
+  GPTQ_MAX_STEP(0x143);
+#undef GPTQ_MAX_STEP
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+// What one wave knows of its token: lane i < k has the i-th expert in descending
+// order of logits, ties to the lowest index, and its logit's key.
+struct Routed {
+  int id;
+  uint32_t key;
+  uint32_t top;                              // the largest key
+  float sum;                                 // of exp(logit - largest) over all experts, where asked for
+};
+
+// exp(l - m) for logits l <= m; 1 where they are equal, also if infinite.
+__device__ inline float route_exp(float l, float m) { return l == m ? 1.f : expf(l - m); }
+
+// L: registers of 64 logits.
+template <int L>
+__device__ inline Routed route_keys(const void* logits, int dtype, int64_t row, int experts, int k, bool want_sum) {
+  const int lane = (int)threadIdx.x & 63;
+  uint32_t keys[L];
+#pragma unroll
+  for (int j = 0; j < L; ++j) {
+    const int64_t at = row + min(64 * j + lane, experts - 1);
+    const float l = dtype == GPTQ_F32   ? load_as_f32<GPTQ_F32>(logits, at)
+                    : dtype == GPTQ_F16 ? load_as_f32<GPTQ_F16>(logits, at)
+                                        : load_as_f32<GPTQ_BF16>(logits, at);
+    keys[j] = 64 * j + lane < experts ? route_key(l) : 0u;
+  }
+  Routed r{0, 0u, 0u, 0.f};
+  for (int i = 0; i < k; ++i) {
+    uint32_t best = keys[0];
+#pragma unroll
+    for (int j = 1; j < L; ++j) best = max(best, keys[j]);
+    best = wave_max(best);
+    if (i == 0) {
+      r.top = best;
+      if (want_sum) {
+        const float m = route_logit(best);
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < L; ++j) s += keys[j] != 0u ? route_exp(route_logit(keys[j]), m) : 0.f;
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) s += __shfl_xor(s, x, 64);
+        r.sum = s;
+      }
+    }
+    // The lowest index: the first register of 64 that has one, its first lane.
+    int id = -1;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      const uint64_t hit = __ballot(keys[j] == best);
+      const int l = hit != 0 && id < 0 ? __builtin_ctzll(hit) : 64;
+      id = l < 64 ? 64 * j + l : id;
+      keys[j] = lane == l ? 0u : keys[j];
+    }
+    r.id = lane == i ? id : r.id;
+    r.key = lane == i ? best : r.key;
+  }
+  return r;
+}
+
+__device__ inline Routed route_token(const void* logits, int dtype, int64_t row, int experts, int k, bool want_sum) {
+  if (experts <= 64) return route_keys<1>(logits, dtype, row, experts, k, want_sum);
+  if (experts <= 256) return route_keys<4>(logits, dtype, row, experts, k, want_sum);
+  return route_keys<kRouteRegs>(logits, dtype, row, experts, k, want_sum);
+}
+
+// Lane i's probability of the i-th expert.  A token whose logits are all -inf (or
+// NaN) has none.
+__device__ inline float route_weight(const Routed& r, int k, bool renormalize) {
+  const int lane = (int)threadIdx.x & 63;
+  if (r.top <= kRouteLowest) return 0.f;
+  float w = lane < k ? route_exp(route_logit(r.key), route_logit(r.top)) : 0.f, sum = r.sum;
+  if (renormalize) {
+    sum = w;                                 // k <= 16: the first row of lanes
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor(sum, x, 64);
+  }
+  return w / sum;
+}
+
+}  // namespace gptq
