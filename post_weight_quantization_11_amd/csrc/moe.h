@@ -7,7 +7,6 @@
 namespace gptq {
 
 constexpr int kMoeMaxExperts = GPTQ_MOE_MAX_EXPERTS, kMoeMaxTopk = GPTQ_MOE_MAX_TOPK;
-constexpr int kRouteRegs = kMoeMaxExperts / 64;
 
 // Logits as unsigned numbers in the same order; both zeros are one number, and a
 // NaN counts as -inf.  Experts that do not exist have 0, below every logit.
@@ -48,17 +47,29 @@ struct Routed {
 // exp(l - m) for logits l <= m; 1 where they are equal, also if infinite.
 __device__ inline float route_exp(float l, float m) { return l == m ? 1.f : expf(l - m); }
 
-// L: registers of 64 logits.
-template <int L>
-__device__ inline Routed route_keys(const void* logits, int dtype, int64_t row, int experts, int k, bool want_sum) {
-  const int lane = (int)threadIdx.x & 63;
+// A token's keys, expert 64 j + lane in register j.
+template <int L> struct RouteKeys {
   uint32_t keys[L];
+};
+template <int L>
+__device__ inline void route_load(RouteKeys<L>& o, const void* logits, int dtype, int64_t row, int experts) {
+  const int lane = (int)threadIdx.x & 63;
 #pragma unroll
   for (int j = 0; j < L; ++j) {
     const int64_t at = row + min(64 * j + lane, experts - 1);
-    const float l = dtype == GPTQ_F32   ? load_as_f32<GPTQ_F32>(logits, at)
-                    : dtype == GPTQ_F16 ? load_as_f32<GPTQ_F16>(logits, at)
-                                        : load_as_f32<GPTQ_BF16>(logits, at);
+    o.keys[j] = dtype == GPTQ_F32 ? static_cast<const uint32_t*>(logits)[at] : static_cast<const uint16_t*>(logits)[at];
+  }
+}
+
+template <int L>
+__device__ inline Routed route_choose(RouteKeys<L> o, int dtype, int experts, int k, bool want_sum) {
+  const int lane = (int)threadIdx.x & 63;
+  uint32_t (&keys)[L] = o.keys;
+#pragma unroll
+  for (int j = 0; j < L; ++j) {
+    const float l = dtype == GPTQ_F32   ? __uint_as_float(keys[j])
+                    : dtype == GPTQ_F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)keys[j])
+                                        : __uint_as_float(keys[j] << 16);
     keys[j] = 64 * j + lane < experts ? route_key(l) : 0u;
   }
   Routed r{0, 0u, 0u, 0.f};
@@ -94,10 +105,26 @@ __device__ inline Routed route_keys(const void* logits, int dtype, int64_t row, 
   return r;
 }
 
-__device__ inline Routed route_token(const void* logits, int dtype, int64_t row, int experts, int k, bool want_sum) {
-  if (experts <= 64) return route_keys<1>(logits, dtype, row, experts, k, want_sum);
-  if (experts <= 256) return route_keys<4>(logits, dtype, row, experts, k, want_sum);
-  return route_keys<kRouteRegs>(logits, dtype, row, experts, k, want_sum);
+// Tokens t, t + step, ... below `tokens`, one after the other; the next one's logits
+// are on their way meanwhile.  done(t, Routed).
+template <int L, typename Done>
+__device__ inline void route_some(const void* logits, int dtype, int64_t ld, int t, int tokens, int step, int experts,
+                                  int k, bool want_sum, Done done) {
+  if (t >= tokens) return;
+  RouteKeys<L> next;
+  route_load(next, logits, dtype, (int64_t)t * ld, experts);
+  for (; t < tokens; t += step) {
+    const RouteKeys<L> now = next;
+    route_load(next, logits, dtype, (int64_t)min(t + step, tokens - 1) * ld, experts);
+    done(t, route_choose(now, dtype, experts, k, want_sum));
+  }
+}
+template <typename Done>
+__device__ inline void route_tokens(const void* logits, int dtype, int64_t ld, int t, int tokens, int step, int experts,
+                                    int k, bool want_sum, Done done) {
+  if (experts <= 64) route_some<1>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
+  else if (experts <= 256) route_some<4>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
+  else route_some<kMoeMaxExperts / 64>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
 }
 
 // Lane i's probability of the i-th expert.  A token whose logits are all -inf (or

@@ -3,21 +3,25 @@
 // with the experts and probabilities of the router, and G, U (rows of one stack)
 // and D microscaled or in block-scaled 8-bit floats.
 //
-// First launch (moe_up_kernel): every workgroup routes all tokens itself (a wave a
-// token, the experts' tokens as 64-bit masks in LDS), takes the slot-th expert that
-// has any, and 16 rows of its G with the same 16 of its U; its eight waves split
-// the columns.  h = silu(g) * u goes to the workspace as three bfloat16 numbers
-// that add up to its float32 value (8 bits each), so that the second launch's
-// products, exact in float32, lose none of it.
+// Slots: an expert with tokens has one for every sixteen of them.
 //
-// Second launch (moe_down_kernel): a workgroup takes 64 rows of D for all experts
-// and tokens; the waves of the row group's `splits` workgroups share the list of
-// (expert, 128 columns) and add p h D into sums of their own, in float32, joined in
-// wave order and, by the workgroup that comes last, in split order.  The first
-// launch clears the counters that tell the last.
+// First launch (moe_up_kernel): every workgroup routes all tokens itself (a wave a
+// token, the experts' tokens as 64-bit masks in LDS) and takes its share of the
+// list of (slot, 16 rows of G with the same 16 of U); its eight waves split the
+// columns.  h = silu(g) * u goes to the workspace as three bfloat16 numbers that add
+// up to its float32 value (8 bits each), so that the second launch's products,
+// exact in float32, lose none of it.
+//
+// Second launch (moe_down_kernel): a workgroup takes 32 rows of D for all slots; the
+// waves of the row group's `splits` workgroups share the list of (slot, 128 columns).
+// A matrix instruction's sixteen columns are five tokens' three parts of h.  Sums
+// times p go to the wave's own sums of its tokens in LDS, joined in wave order and,
+// by the workgroup that comes last, in split order.  The first launch clears the
+// counters that tell the last.
 //
 // Both are bound by the weights' bytes, or for small layers by latency: routing,
-// one load after it, and the joins.
+// one load after it, and the joins.  The waves' loads are two units of 128 columns
+// ahead, across the borders of tiles and slots.
 #include "fp8.h"
 #include "moe.h"
 #include "mx_operands.h"
@@ -28,8 +32,11 @@ namespace {
 
 constexpr int kMxWeights = 0, kBlockWeights = 1;             // formats of the weights
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kSlot = 16;                    // tokens of a slot
 constexpr int kPlanes = 3;                   // bfloat16 numbers of an h
-constexpr int kDownTiles = 4, kDownRows = 16 * kDownTiles;
+constexpr int kPart = 5;                     // tokens whose three parts are columns of one instruction
+constexpr int kPadCols = 256;                // rows of h are whole units of either format
+constexpr int kDownTiles = 2, kDownRows = 16 * kDownTiles;
 
 // A stack of weights: `experts` matrices.
 struct Weights {
@@ -47,8 +54,9 @@ struct MoeArgs {
   int l_dtype;
   int64_t ld_logits;
   // Workspace.
-  int32_t* ids;                              // tokens x k
-  float* weights;
+  float* weights;                            // of the pairs: tokens x k
+  int* slots;                                // their number, then the expert of each
+  uint32_t* slot_pairs;                      // [slot][16]: pair, token in the upper half
   uint32_t* arrived;                         // a counter for each group of rows of D
   uint16_t* h;                               // [plane][tokens * k][f_pad]
   float* part;                               // [split][token][d]
@@ -57,49 +65,109 @@ struct MoeArgs {
   int y_dtype;
 };
 
-// What a wave multiplies of one row of weights in 128 columns.
+// Slots there can be.
+__host__ __device__ inline int max_slots(int tokens, int experts, int k) {
+  return (experts < tokens * k ? experts : tokens * k) + tokens * k / kSlot;
+}
+
+// What a lane holds of a unit of a row of weights: 128 bytes of codes, a whole line
+// of the caches, in two neighbouring loads (units of 64 bytes, half a line at a time,
+// reached three quarters of the rate).
 template <int WF> struct Row;
 template <> struct Row<kMxWeights> {
-  const uint32_t* codes;
-  const uint8_t* scales;
-  u32x4 w;
-  uint32_t s;
+  static constexpr int kCols = 256, kSteps = 8;
+  u32x4 w[2];
+  u32x2 s;
 };
 template <> struct Row<kBlockWeights> {
-  const uint8_t* codes;
-  const float* scales;
+  static constexpr int kCols = 128, kSteps = 4;
   u32x4 w[2];
   float s;
 };
 
-// Row r of expert e (clamped by the caller).
-__device__ inline void point(Row<kMxWeights>& o, const Weights& w, int64_t e, int64_t r) {
-  o.codes = static_cast<const uint32_t*>(w.codes) + e * w.stride + r * w.ld;
-  o.scales = static_cast<const uint8_t*>(w.scales) + e * w.s_stride + r * w.lds;
+// Lane quarter q's share of unit u of the row whose codes and scales start at `codes
+// + at`, `scales + s_at` (bytes).
+__device__ inline void load_row(Row<kMxWeights>& o, const char* codes, uint32_t at, const char* scales, uint32_t s_at,
+                                int u, int q) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    o.w[h] = *reinterpret_cast<const u32x4_a4*>(codes + (at + 128u * u + 64u * h + 16u * q));
+  o.s = *reinterpret_cast<const u32x2_a1*>(scales + (s_at + 8u * u));
 }
-__device__ inline void point(Row<kBlockWeights>& o, const Weights& w, int64_t e, int64_t r) {
-  o.codes = static_cast<const uint8_t*>(w.codes) + e * w.stride + r * w.ld;
-  o.scales = static_cast<const float*>(w.scales) + e * w.s_stride + (r >> 7) * w.lds;
+__device__ inline void load_row(Row<kBlockWeights>& o, const char* codes, uint32_t at, const char* scales, uint32_t s_at,
+                                int u, int q) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    o.w[h] = *reinterpret_cast<const u32x4_a1*>(codes + (at + 128u * u + 64u * h + 16u * q));
+  o.s = *reinterpret_cast<const float*>(scales + (s_at + 4u * u));
 }
-
-// Lane quarter q's share of unit u (columns 128 u ..); n: columns of the row, `all`
-// of the unit's there or not.
-__device__ inline void load_row(Row<kMxWeights>& o, int u, int q, bool all, int n) {
-  if (all) {
-    o.w = *reinterpret_cast<const u32x4_a4*>(o.codes + 16 * u + 4 * q);
-    o.s = *reinterpret_cast<const u32_a1*>(o.scales + 4 * u);
-  } else {
-    o.w = load_w4_tail(o.codes, 16 * u + 4 * q, n);
-    o.s = load_scales4(o.scales, 4 * u, n);
-  }
-}
-__device__ inline void load_row(Row<kBlockWeights>& o, int u, int q, bool all, int n) {
+// The same of the unit behind the last whole one of n columns.
+__device__ inline void load_row_tail(Row<kMxWeights>& o, const char* codes, uint32_t at, const char* scales,
+                                     uint32_t s_at, int u, int q, int n) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int k = 128 * u + 64 * h + 16 * q;
-    o.w[h] = all ? (u32x4)*reinterpret_cast<const u32x4_a1*>(o.codes + k) : fp8_load16_tail(o.codes, k, n);
+    o.w[h] = load_w4_tail(reinterpret_cast<const uint32_t*>(codes + at), 32 * u + 16 * h + 4 * q, n);
+    o.s[h] = load_scales4(reinterpret_cast<const uint8_t*>(scales + s_at), 8 * u + 4 * h, n);
   }
-  o.s = o.scales[u];
+}
+__device__ inline void load_row_tail(Row<kBlockWeights>& o, const char* codes, uint32_t at, const char* scales,
+                                     uint32_t s_at, int u, int q, int n) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    o.w[h] = fp8_load16_tail(reinterpret_cast<const uint8_t*>(codes + at), 128 * u + 64 * h + 16 * q, n);
+  o.s = *reinterpret_cast<const float*>(scales + (s_at + 4u * u));
+}
+
+// Step s alone of the unit behind the last whole one: eight weights as 16-bit
+// numbers (0 past column n), and their scale where it is not in them.
+template <int T>
+__device__ inline u32x4 load_step(Row<kMxWeights>& o, const char* codes, uint32_t at, const char* scales, uint32_t s_at,
+                                  int u, int s, int q, int n) {
+  const int word = 32 * u + 4 * s + q, block = 8 * u + s, left = n - 8 * word;
+  const uint32_t w = reinterpret_cast<const uint32_t*>(codes + at)[min(word, (n - 1) >> 3)];
+  const uint32_t b = reinterpret_cast<const uint8_t*>(scales + s_at)[min(block, (n - 1) >> 5)];
+  o.s[0] = left > 0 ? b : (uint32_t)kMxScaleOne;
+  return widen8<T>(left >= 8 ? w : w & ((1u << (4 * max(left, 0))) - 1u), mx_scale_operand(o.s[0]));
+}
+template <int T>
+__device__ inline u32x4 load_step(Row<kBlockWeights>& o, const char* codes, uint32_t at, const char* scales,
+                                  uint32_t s_at, int u, int s, int q, int n) {
+  const uint8_t* row = reinterpret_cast<const uint8_t*>(codes + at);
+  const int k = 128 * u + 64 * (s >> 1) + 16 * q + 8 * (s & 1);
+  uint64_t v = 0;
+  if (n >= 8) {                              // one load that ends at the row's end, shifted down
+    const int from = min(k, n - 8);
+    const u32x2 w = *reinterpret_cast<const u32x2_a1*>(row + from);
+    v = k - from < 8 ? ((uint64_t)w[1] << 32 | w[0]) >> (8 * (k - from)) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v |= (uint64_t)(k + i < n ? row[min(k + i, n - 1)] : 0) << (8 * i);
+  }
+  o.s = *reinterpret_cast<const float*>(scales + (s_at + 4u * u));
+  const int lo = (int)v, hi = (int)(v >> 32);
+  return T == GPTQ_BF16
+             ? u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true))}
+             : u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true))};
+}
+
+// Where row r of a matrix has its codes and scales, in bytes from the matrix's.
+template <int WF> __device__ inline uint32_t codes_at(const Weights& w, int r) {
+  return (uint32_t)r * (uint32_t)w.ld * (WF == kMxWeights ? 4u : 1u);
+}
+template <int WF> __device__ inline uint32_t scales_at(const Weights& w, int r) {
+  return WF == kMxWeights ? (uint32_t)r * (uint32_t)w.lds : (uint32_t)(r >> 7) * (uint32_t)w.lds * 4u;
+}
+template <int WF> __device__ inline const char* matrix_codes(const Weights& w, int e) {
+  return static_cast<const char*>(w.codes) + e * w.stride * (WF == kMxWeights ? 4 : 1);
+}
+template <int WF> __device__ inline const char* matrix_scales(const Weights& w, int e) {
+  return static_cast<const char*>(w.scales) + e * w.s_stride * (WF == kMxWeights ? 1 : 4);
 }
 
 // The column, inside a unit, of the eight that lane quarter q holds in step s.
@@ -107,11 +175,18 @@ template <int WF> __device__ inline int step_col(int s, int q) {
   return WF == kMxWeights ? 32 * s + 8 * q : 64 * (s >> 1) + 16 * q + 8 * (s & 1);
 }
 
-// Eight weights of step s as 16-bit numbers.  (w: of microscaled codes, transposed.)
-template <int T> __device__ inline u32x4 widen(const Row<kMxWeights>& o, u32x4 w, int s) {
-  return widen8<T>(w[s], mx_scale_operand((o.s >> (8 * s)) & 255u));
+// Codes in the order of the steps.
+__device__ inline void arrange(Row<kMxWeights>& o) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) o.w[h] = transpose_quarters(o.w[h]);
 }
-template <int T> __device__ inline u32x4 widen(const Row<kBlockWeights>& o, u32x4, int s) {
+__device__ inline void arrange(Row<kBlockWeights>&) {}
+
+// Eight weights of step s as 16-bit numbers.
+template <int T> __device__ inline u32x4 widen(const Row<kMxWeights>& o, int s) {
+  return widen8<T>(o.w[s >> 2][s & 3], mx_scale_operand((o.s[s >> 2] >> (8 * (s & 3))) & 255u));
+}
+template <int T> __device__ inline u32x4 widen(const Row<kBlockWeights>& o, int s) {
   if constexpr (T == GPTQ_BF16) {
     return __builtin_bit_cast(u32x4, fp8_widen8(o.w[s >> 1], s & 1));
   } else {
@@ -122,361 +197,429 @@ template <int T> __device__ inline u32x4 widen(const Row<kBlockWeights>& o, u32x
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true))};
   }
 }
-__device__ inline u32x4 transposed(const Row<kMxWeights>& o) { return transpose_quarters(o.w); }
-__device__ inline u32x4 transposed(const Row<kBlockWeights>&) { return u32x4{0u, 0u, 0u, 0u}; }
 
-// The index of the n-th set bit (n below their count; the last one otherwise).
-__device__ inline int nth_bit(uint64_t mask, int n) {
-  int at = 0;
-  for (int i = 0; mask != 0; ++i, mask &= mask - 1)           // the same for all lanes
-    if (i <= n) at = __builtin_ctzll(mask);
-  return at;
-}
-
-// The place of expert e among token t's.
-__device__ inline int place_of(const int* ids, int t, int k, int e) {
-  int j = 0;
-  for (int i = 1; i < k; ++i)
-    if (ids[t * k + i] == e) j = i;
-  return j;
+// acc += f * v, v being a unit's sums (block-scaled weights).
+__device__ inline void add_scaled(floatx4& acc, float f, floatx4 v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = __builtin_fmaf(f, v[j], acc[j]);
 }
 
 // ---------------------------------------------------------------------------
 // Gate and up.
 // ---------------------------------------------------------------------------
-// Sums of the wave's share of the columns: 16 tokens x 16 rows of G and of U.  SPLIT
-// (float16 X, microscaled weights that float16 does not hold): X as the sum of two
-// bfloat16 numbers.  Otherwise `inexact` gathers whether there are such weights.
-template <int WF, int XT, bool SPLIT>
-__device__ inline void up_sums(const MoeArgs& p, Row<WF> (&row)[2], const uint16_t* x, floatx4 (&acc)[2],
-                               uint32_t& inexact) {
-  constexpr int D = 2;
-  const int lane = (int)threadIdx.x & 63, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int units = (p.d + 127) >> 7, whole = p.d >> 7;
-  const int lo = units * wave / kWaves, hi = units * (wave + 1) / kWaves, last = min(hi, whole);
-  struct Unit {
-    Row<WF> w[2];
-    u32x4 x[4];
-  };
-  auto load = [&](int u, bool all, Unit& o) {
+// What a workgroup knows of the routes, in LDS.
+struct Routes {
+  uint64_t* masks;                           // tokens of each expert
+  int* first;                                // first slot of each expert
+  int* slot_expert;                          // with the slot's tokens in the upper half
+  uint32_t* slot_pairs;                      // as in the workspace
+};
+constexpr size_t routes_lds(int tokens, int experts, int k) {
+  const int pairs = tokens * k, slots = (experts < pairs ? experts : pairs) + pairs / kSlot;
+  return (size_t)experts * 12 + (size_t)slots * 4 * (1 + kSlot) + (size_t)pairs * 4;
+}
+
+// Routes all tokens; returns the number of slots.  Workgroup 0 writes what the
+// second launch needs.
+__device__ inline int route_all(const MoeArgs& p, unsigned char* lds, Routes& o) {
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool first = blockIdx.x == 0;
+  const int pairs = p.tokens * p.k, most = max_slots(p.tokens, p.experts, p.k);
+  __shared__ int count;
+  o.masks = reinterpret_cast<uint64_t*>(lds);
+  o.first = reinterpret_cast<int*>(o.masks + p.experts);
+  o.slot_expert = o.first + p.experts;
+  o.slot_pairs = reinterpret_cast<uint32_t*>(o.slot_expert + most);
+  int* ids = reinterpret_cast<int*>(o.slot_pairs + most * kSlot);
+  for (int e = tid; e < p.experts; e += kThreads) o.masks[e] = 0u;
+  __syncthreads();
+  route_tokens(p.logits, p.l_dtype, p.ld_logits, wave, p.tokens, kWaves, p.experts, p.k, first && !p.renormalize,
+               [&](int t, const Routed& r) {
+                 if (lane < p.k) {
+                   ids[t * p.k + lane] = r.id;
+                   atomicOr(reinterpret_cast<unsigned long long*>(o.masks + r.id), 1ull << t);
+                 }
+                 if (first) {
+                   const float w = route_weight(r, p.k, p.renormalize);
+                   if (lane < p.k) p.weights[t * p.k + lane] = w;
+                 }
+               });
+  __syncthreads();
+  if (wave == 0) {
+    int before = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 64) {
+      const int n = e0 + lane < p.experts ? __popcll(o.masks[e0 + lane]) : 0;
+      const int own = (n + kSlot - 1) / kSlot;
+      int upto = own;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      o.w[i].codes = row[i].codes;
-      o.w[i].scales = row[i].scales;
-      load_row(o.w[i], u, q, all, p.d);
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int k = 128 * u + step_col<WF>(s, q);
-      o.x[s] = all ? (u32x4)*reinterpret_cast<const u32x4_a2*>(x + k) : load_x8_tail(x, k, p.d);
-    }
-  };
-  auto multiply = [&](const Unit& o) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const u32x4 w = transposed(o.w[i]);
-      floatx4 v = floatx4{0.f, 0.f, 0.f, 0.f};
-      if constexpr (WF == kMxWeights) {
-        v = acc[i];
-        if constexpr (XT == GPTQ_F16 && !SPLIT) inexact |= f16_inexact4(o.w[i].s);
+      for (int x = 1; x < 64; x <<= 1) {
+        const int v = __shfl_up(upto, x, 64);
+        if (lane >= x) upto += v;
       }
+      const int at = before + upto - own;
+      if (own > 0) o.first[e0 + lane] = at;
+      for (int i = 0; i < own; ++i) o.slot_expert[at + i] = (e0 + lane) | min(n - i * kSlot, kSlot) << 16;
+      before += __shfl(upto, 63, 64);
+    }
+    if (lane == 0) count = before;
+  }
+  __syncthreads();
+  for (int i = tid; i < pairs; i += kThreads) {
+    const int e = ids[i], t = i / p.k;
+    const int at = __popcll(o.masks[e] & (((uint64_t)1 << t) - 1));
+    o.slot_pairs[o.first[e] * kSlot + at] = (uint32_t)(i | t << 16);
+  }
+  __syncthreads();
+  if (first) {
+    for (int i = tid; i < count; i += kThreads) p.slots[1 + i] = o.slot_expert[i];
+    for (int i = tid; i < count * kSlot; i += kThreads) p.slot_pairs[i] = o.slot_pairs[i];
+    if (tid == 0) p.slots[0] = count;
+    for (int i = tid; i < (p.d + kDownRows - 1) / kDownRows; i += kThreads) p.arrived[i] = 0u;
+  }
+  return __builtin_amdgcn_readfirstlane(count);
+}
+
+// Tiles [lo, hi) of the list: tile n has slot n / tiles, rows 16 (n % tiles) ...
+// SPLIT (float16 X, microscaled weights that float16 does not hold): X as the sum of
+// two bfloat16 numbers.  Otherwise the result says whether there are such weights.
+template <int WF, int XT, bool TAIL, bool SPLIT>
+__device__ inline bool up_tiles(const MoeArgs& p, const Routes& routes, int lo, int hi, floatx4* red) {
+  constexpr int D = 1, kCols = Row<WF>::kCols, kSteps = Row<WF>::kSteps;
+  const int tid = (int)threadIdx.x, lane = tid & 63, q = lane >> 4, c16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // The waves share a tile's whole units, and a step each the columns behind them.
+  const int tiles = (p.f + 15) / 16, units = p.d / kCols;
+  const int u0 = units * wave / kWaves, count = units * (wave + 1) / kWaves - u0;
+  const int steps = (count + D - 1) / D * D;                  // so that a tile starts in the ring's first place
+  struct Unit {
+    Row<WF> w[2];                            // of G and of U
+    u32x4 x[kSteps];
+  };
+  Unit ring[D];
+  floatx4 acc[2];
+  uint32_t inexact = 0u;
+
+  // Where a tile's operands are.
+  struct Place {
+    const char *codes[2], *scales[2];
+    uint32_t w_at[2], s_at[2], x_at;
+  };
+  auto place = [&](int tile, Place& o) {
+    const int slot = tile / tiles, f0 = (tile - slot * tiles) * 16, n = routes.slot_expert[slot] >> 16;
+    o.x_at = (routes.slot_pairs[slot * kSlot + min(c16, n - 1)] >> 16) * (uint32_t)p.ldx * 2u;
+    const int e = __builtin_amdgcn_readfirstlane(routes.slot_expert[slot] & 0xFFFF);
+    const char *c = matrix_codes<WF>(p.gate_up, e), *s = matrix_scales<WF>(p.gate_up, e);
+    const int r = min(c16, p.f - 1 - f0);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+    for (int i = 0; i < 2; ++i) {
+      const int row0 = f0 + i * p.f, block0 = WF == kMxWeights ? row0 : row0 & ~127;
+      o.codes[i] = c + row0 * p.gate_up.ld * (WF == kMxWeights ? 4 : 1);
+      o.scales[i] = s + (WF == kMxWeights ? row0 * p.gate_up.lds : (int64_t)(row0 >> 7) * p.gate_up.lds * 4);
+      o.w_at[i] = codes_at<WF>(p.gate_up, r);
+      o.s_at[i] = scales_at<WF>(p.gate_up, row0 - block0 + r);
+    }
+  };
+  // Of the loads.  The loop has no branch around one, or the compiler would wait for
+  // all that are in flight where the branches meet: padded steps repeat a unit, and
+  // past the last tile that tile is loaded again.
+  int at_tile = lo, at_step = 0;
+  Place at;
+  const char* x = static_cast<const char*>(p.X);
+  auto load = [&](Unit& o) {
+    if (at_step == 0) place(min(at_tile, hi - 1), at);
+    const int u = u0 + min(at_step, count - 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_row(o.w[i], at.codes[i], at.w_at[i], at.scales[i], at.s_at[i], u, q);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      o.x[s] = *reinterpret_cast<const u32x4_a2*>(x + (at.x_at + 2u * (kCols * u + step_col<WF>(s, q))));
+    if (++at_step == steps) {
+      at_step = 0;
+      ++at_tile;
+    }
+  };
+  auto multiply = [&](Unit& o) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      arrange(o.w[i]);
+      floatx4 v = WF == kMxWeights ? acc[i] : floatx4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (WF == kMxWeights && XT == GPTQ_F16 && !SPLIT)
+        inexact |= f16_inexact4(o.w[i].s[0]) | f16_inexact4(o.w[i].s[1]);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
         if constexpr (SPLIT) {
           u32x4 top, rest;
           split8(o.x[s], top, rest);
-          const u32x4 wv = widen<GPTQ_BF16>(o.w[i], w, s);
+          const u32x4 wv = widen<GPTQ_BF16>(o.w[i], s);
           v = mfma16<GPTQ_BF16>(top, wv, v);
           v = mfma16<GPTQ_BF16>(rest, wv, v);
         } else {
-          v = mfma16<XT>(o.x[s], widen<XT>(o.w[i], w, s), v);
+          v = mfma16<XT>(o.x[s], widen<XT>(o.w[i], s), v);
         }
       }
-      if constexpr (WF == kMxWeights) {
-        acc[i] = v;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(o.w[i].s, v[j], acc[i][j]);
-      }
+      if constexpr (WF == kMxWeights) acc[i] = v;
+      else add_scaled(acc[i], o.w[i].s, v);
     }
   };
-  if (lo < last) {
-    Unit ring[D];
+
+  if (steps > 0) {
 #pragma unroll
-    for (int i = 0; i < D; ++i) load(min(lo + i, last - 1), true, ring[i]);
-    for (int u = lo; u < last; u += D) {
+    for (int i = 0; i < D; ++i) load(ring[i]);
+  }
+  for (int n = lo; n < hi; ++n) {
+    acc[0] = acc[1] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < steps; s += D) {
 #pragma unroll
       for (int i = 0; i < D; ++i) {
-        if (u + i < last) multiply(ring[i]);
-        load(min(u + i + D, last - 1), true, ring[i]);
+        if (s + i < count) multiply(ring[i]);
+        load(ring[i]);
       }
     }
+    if (TAIL && wave < kSteps && kCols * units + step_col<WF>(wave, 0) < p.d) {
+      Place here;
+      place(n, here);
+      const u32x4 xv = load_x8_tail(reinterpret_cast<const uint16_t*>(x + here.x_at),
+                                    kCols * units + step_col<WF>(wave, q), p.d);
+      constexpr int T = SPLIT ? GPTQ_BF16 : XT;
+      u32x4 top = xv, rest;
+      if constexpr (SPLIT) split8(xv, top, rest);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        Row<WF> o;
+        const u32x4 wv =
+            load_step<T>(o, here.codes[i], here.w_at[i], here.scales[i], here.s_at[i], units, wave, q, p.d);
+        floatx4 v = mfma16<T>(top, wv, WF == kMxWeights ? acc[i] : floatx4{0.f, 0.f, 0.f, 0.f});
+        if constexpr (SPLIT) v = mfma16<T>(rest, wv, v);
+        if constexpr (WF == kMxWeights && XT == GPTQ_F16 && !SPLIT) inexact |= o.s[0] - kF16Lo < kF16Span ? 0u : 1u;
+        if constexpr (WF == kMxWeights) acc[i] = v;
+        else add_scaled(acc[i], o.s, v);
+      }
+    }
+    // Two buffers: a tile's sums are added while the next tile's come in.
+    floatx4* to = red + (n & 1) * kWaves * 2 * 64;
+    to[(wave * 2) * 64 + lane] = acc[0];
+    to[(wave * 2 + 1) * 64 + lane] = acc[1];
+    __syncthreads();
+    const int slot = n / tiles, tokens = routes.slot_expert[slot] >> 16;
+    if (tid < 16 * tokens) {
+      // Register j of lane l: token 4 (l / 16) + j, row l % 16.
+      const int col = tid >> 4, r = (n - slot * tiles) * 16 + (tid & 15);
+      const float* s = reinterpret_cast<const float*>(to) + ((col >> 2) * 16 + (tid & 15)) * 4 + (col & 3);
+      float g = s[0], u = s[256];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) {
+        g += s[w * 512];
+        u += s[w * 512 + 256];
+      }
+      float h = r < p.f ? g / (1.f + expf(-g)) * u : 0.f;
+      const int64_t plane = (int64_t)p.tokens * p.k * p.f_pad;
+      uint16_t* o = p.h + (int64_t)(routes.slot_pairs[slot * kSlot + col] & 0xFFFFu) * p.f_pad + r;
+#pragma unroll
+      for (int i = 0; i < kPlanes; ++i) {
+        const uint32_t top = __float_as_uint(h) & 0xFFFF0000u;                 // 8 bits, the rest exact
+        o[i * plane] = (uint16_t)(top >> 16);
+        h = (top & 0x7F800000u) != 0x7F800000u ? h - __uint_as_float(top) : 0.f;
+      }
+      // Behind the last tile zeros, as the second launch reads whole units.
+      if (n - slot * tiles == tiles - 1)
+        for (int c = r + 16; c < p.f_pad; c += 16)
+#pragma unroll
+          for (int i = 0; i < kPlanes; ++i) o[i * plane + c - r] = 0;
+    }
   }
-  if (lo < hi && whole < hi) {
-    Unit o;
-    load(whole, false, o);
-    multiply(o);
-  }
+  return inexact != 0u;
 }
 
-template <int WF, int XT>
-__global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs p) {
+// TAIL: d is no multiple of a unit.  Without it two workgroups fit a CU.
+template <int WF, int XT, bool TAIL>
+__global__ __launch_bounds__(kThreads, 4) void moe_up_kernel(MoeArgs p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  floatx4* red = reinterpret_cast<floatx4*>(smem);            // [wave][gate, up][64]
-  uint64_t* masks = reinterpret_cast<uint64_t*>(red + kWaves * 2 * 64);       // tokens of each expert
-  int* ids = reinterpret_cast<int*>(masks + p.experts);       // tokens x k
-  const int tid = (int)threadIdx.x, lane = tid & 63, q = lane >> 4, c16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tiles = p.f_pad / 16;
-  const int slot = (int)(blockIdx.x / tiles), f0 = (int)(blockIdx.x % tiles) * 16;
-  const bool first = blockIdx.x == 0;
-
-  for (int e = tid; e < p.experts; e += kThreads) masks[e] = 0u;
-  __syncthreads();
-  for (int t = wave; t < p.tokens; t += kWaves) {
-    const Routed r = route_token(p.logits, p.l_dtype, (int64_t)t * p.ld_logits, p.experts, p.k,
-                                 first && !p.renormalize);
-    if (lane < p.k) {
-      ids[t * p.k + lane] = r.id;
-      atomicOr(reinterpret_cast<unsigned long long*>(masks + r.id), 1ull << t);
-    }
-    if (first) {
-      const float w = route_weight(r, p.k, p.renormalize);
-      if (lane < p.k) {
-        p.ids[t * p.k + lane] = r.id;
-        p.weights[t * p.k + lane] = w;
-      }
-    }
-  }
-  if (first)
-    for (int i = tid; i < (p.d + kDownRows - 1) / kDownRows; i += kThreads) p.arrived[i] = 0u;
-  __syncthreads();
-
-  // The slot-th expert that has tokens.
-  int expert = -1, before = 0;
-  uint64_t mask = 0;
-  for (int e0 = 0; e0 < p.experts; e0 += 64) {
-    const uint64_t m = e0 + lane < p.experts ? masks[e0 + lane] : 0u;
-    const uint64_t has = __ballot(m != 0);
-    const int count = __popcll(has);
-    if (slot < before + count) {
-      expert = e0 + nth_bit(has, slot - before);
-      mask = masks[expert];
-      break;
-    }
-    before += count;
-  }
-  if (expert < 0) return;
-  expert = __builtin_amdgcn_readfirstlane(expert);
-  mask = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(mask >> 32)) << 32 |
-         (uint32_t)__builtin_amdgcn_readfirstlane((int)mask);
-  const int count = __popcll(mask);
-
-  Row<WF> row[2];
-  if (f0 < p.f) {
-    const int r = min(f0 + c16, p.f - 1);
-    point(row[0], p.gate_up, expert, r);
-    point(row[1], p.gate_up, expert, p.f + r);
-  }
-  for (int c0 = 0; c0 < count; c0 += 16) {   // tokens, sixteen at a time
-    if (f0 < p.f) {
-      const int t = nth_bit(mask, c0 + c16);
-      const uint16_t* x = static_cast<const uint16_t*>(p.X) + (int64_t)t * p.ldx;
-      floatx4 acc[2] = {floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
-      uint32_t inexact = 0u;
-      up_sums<WF, XT, false>(p, row, x, acc, inexact);
-      if constexpr (WF == kMxWeights && XT == GPTQ_F16) {
-        if (!__syncthreads_and(inexact == 0u)) {
-          acc[0] = acc[1] = floatx4{0.f, 0.f, 0.f, 0.f};
-          up_sums<WF, XT, true>(p, row, x, acc, inexact);
-        }
-      }
-      red[(wave * 2) * 64 + lane] = acc[0];
-      red[(wave * 2 + 1) * 64 + lane] = acc[1];
-    }
-    __syncthreads();
-    if (tid < 256) {
-      // Register j of lane l: token 4 (l / 16) + j, row l % 16.
-      const int l = tid >> 2, at = c0 + 4 * (l >> 4) + (tid & 3), r = f0 + (l & 15);
-      float h = 0.f;
-      if (r < p.f) {
-        const float* s = reinterpret_cast<const float*>(red) + tid;
-        float g = s[0], u = s[256];
-        for (int w = 1; w < kWaves; ++w) {
-          g += s[w * 512];
-          u += s[w * 512 + 256];
-        }
-        h = g / (1.f + expf(-g)) * u;
-      }
-      if (at < count) {
-        const int t = nth_bit(mask, at);
-        const int64_t pairs = (int64_t)p.tokens * p.k, pair = (int64_t)t * p.k + place_of(ids, t, p.k, expert);
-        uint16_t* o = p.h + pair * p.f_pad + r;
-#pragma unroll
-        for (int i = 0; i < kPlanes; ++i) {
-          const uint32_t top = __float_as_uint(h) & 0xFFFF0000u;               // 8 bits, the rest exact
-          o[i * pairs * p.f_pad] = (uint16_t)(top >> 16);
-          const bool finite = (top & 0x7F800000u) != 0x7F800000u;
-          h = finite ? h - __uint_as_float(top) : 0.f;
-        }
-      }
-    }
-    __syncthreads();
+  floatx4* red = reinterpret_cast<floatx4*>(smem);            // [2][wave][gate, up][64]
+  Routes routes;
+  const int slots = route_all(p, smem + 2 * kWaves * 2 * 64 * sizeof(floatx4), routes);
+  const int64_t all = (int64_t)slots * ((p.f + 15) / 16);
+  const int lo = (int)(all * blockIdx.x / gridDim.x), hi = (int)(all * (blockIdx.x + 1) / gridDim.x);
+  const bool inexact = up_tiles<WF, XT, TAIL, false>(p, routes, lo, hi, red);
+  if constexpr (WF == kMxWeights && XT == GPTQ_F16) {
+    if (__syncthreads_or(inexact)) up_tiles<WF, XT, TAIL, true>(p, routes, lo, hi, red);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Down.
 // ---------------------------------------------------------------------------
-template <int WF>
-__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs p) {
+// TAIL: f is no multiple of a unit.
+template <int WF, bool TAIL>
+__global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(MoeArgs p) {
+  constexpr int D = 1, kCols = Row<WF>::kCols, kSteps = Row<WF>::kSteps;
+  constexpr int kParts = (kSlot + kPart - 1) / kPart;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  const int pairs = p.tokens * p.k;
-  float* sums = reinterpret_cast<float*>(smem);               // [wave][token][64 rows]
-  uint64_t* masks = reinterpret_cast<uint64_t*>(sums + kWaves * p.tokens * kDownRows);
-  int* ids = reinterpret_cast<int*>(masks + p.experts);
-  float* weights = reinterpret_cast<float*>(ids + pairs);
-  int* items = reinterpret_cast<int*>(weights + pairs);       // experts and their sixteens of tokens
-  __shared__ int item_count, is_last;
+  const int pairs = p.tokens * p.k, most = max_slots(p.tokens, p.experts, p.k);
+  float* sums = reinterpret_cast<float*>(smem);               // [wave][token][32 rows]
+  float* weights = sums + kWaves * p.tokens * kDownRows;
+  int* slot_expert = reinterpret_cast<int*>(weights + pairs);
+  uint32_t* slot_pairs = reinterpret_cast<uint32_t*>(slot_expert + most);
+  __shared__ int is_last;
   const int tid = (int)threadIdx.x, lane = tid & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int groups = (p.d + kDownRows - 1) / kDownRows;
   const int group = (int)blockIdx.x % groups, split = (int)blockIdx.x / groups, r0 = group * kDownRows;
 
-  for (int e = tid; e < p.experts; e += kThreads) masks[e] = 0u;
-  for (int i = tid; i < pairs; i += kThreads) {
-    ids[i] = p.ids[i];
-    weights[i] = p.weights[i];
-  }
+  // All that there can be, in one round trip; what lies behind the last slot is not used.
+  const int slots = p.slots[0];
+  for (int i = tid; i < pairs; i += kThreads) weights[i] = p.weights[i];
+  for (int i = tid; i < most; i += kThreads) slot_expert[i] = p.slots[1 + i];
+  for (int i = tid; i < most * kSlot; i += kThreads) slot_pairs[i] = p.slot_pairs[i];
   for (int i = tid; i < kWaves * p.tokens * kDownRows; i += kThreads) sums[i] = 0.f;
   __syncthreads();
-  for (int i = tid; i < pairs; i += kThreads)
-    atomicOr(reinterpret_cast<unsigned long long*>(masks + ids[i]), 1ull << (i / p.k));
-  __syncthreads();
-  if (wave == 0) {
-    int before = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 64) {
-      const int own = e0 + lane < p.experts ? (__popcll(masks[e0 + lane]) + 15) / 16 : 0;
-      int upto = own;
-#pragma unroll
-      for (int x = 1; x < 64; x <<= 1) {
-        const int o = __shfl_up(upto, x, 64);
-        if (lane >= x) upto += o;
-      }
-      for (int i = 0; i < own; ++i) items[before + upto - own + i] = (e0 + lane) | i << 16;
-      before += __shfl(upto, 63, 64);
-    }
-    if (lane == 0) item_count = before;
-  }
-  __syncthreads();
 
-  const int per_item = p.f_pad / 128, whole = p.f >> 7;
-  const int64_t total = (int64_t)item_count * per_item, parts = (int64_t)p.splits * kWaves, part = split * kWaves + wave;
-  const int lo = (int)(total * part / parts), hi = (int)(total * (part + 1) / parts);
-  const int64_t plane = (int64_t)pairs * p.f_pad;
+  const int per_slot = p.f / kCols;          // whole units
+  const int64_t total = (int64_t)slots * per_slot, shares = (int64_t)p.splits * kWaves, share = split * kWaves + wave;
+  const int lo = (int)(total * share / shares), hi = (int)(total * (share + 1) / shares);
+  const uint32_t plane = (uint32_t)pairs * (uint32_t)p.f_pad * 2u;
   float* mine = sums + wave * p.tokens * kDownRows;
+  const int third = c16 / 3;                 // this lane's token of a part, and its number of the three
+  const uint32_t in_plane = (uint32_t)(c16 - 3 * third) * plane;
 
-  // Lane c16's pair of an item (clamped to the last), and whether it is one.
-  auto pair_of = [&](int item, bool& there) {
-    const int e = items[item] & 0xFFFF, c = (items[item] >> 16) * 16 + c16;
-    const uint64_t mask = masks[e];
-    const int t = nth_bit((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(mask >> 32)) << 32 |
-                              (uint32_t)__builtin_amdgcn_readfirstlane((int)mask),
-                          c);
-    there = c < __popcll(mask);
-    return t * p.k + place_of(ids, t, p.k, e);
-  };
-
-  constexpr int D = 2;
   struct Unit {
     Row<WF> w[kDownTiles];
-    u32x4 x[kPlanes][4];
+    u32x4 x[kSteps];                         // of the first part
   };
-  int at_item = -1;                          // of the loads
-  const uint16_t* h = p.h;
-  Row<WF> row[kDownTiles];
-  auto load = [&](int n, Unit& o) {
-    const int item = n / per_item, u = n - item * per_item;
-    if (item != at_item) {
-      at_item = item;
-      const int e = __builtin_amdgcn_readfirstlane(items[item] & 0xFFFF);
-#pragma unroll
-      for (int i = 0; i < kDownTiles; ++i) point(row[i], p.down, e, min(r0 + 16 * i + c16, p.d - 1));
-      bool there;
-      h = p.h + (int64_t)pair_of(item, there) * p.f_pad;
-    }
-    const bool all = u < whole;
-#pragma unroll
-    for (int i = 0; i < kDownTiles; ++i) {
-      o.w[i].codes = row[i].codes;
-      o.w[i].scales = row[i].scales;
-      load_row(o.w[i], u, q, all, p.f);
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < kPlanes; ++i)
-        o.x[i][s] = *reinterpret_cast<const u32x4*>(h + i * plane + 128 * u + step_col<WF>(s, q));
+  // Where this lane's h of part i of a slot lies (lane 15 and lanes without a token
+  // repeat another's).
+  auto part_at = [&](int slot, int i) {
+    const int n = slot_expert[slot] >> 16;
+    return in_plane + (slot_pairs[slot * kSlot + min(min(third, kPart - 1) + kPart * i, n - 1)] & 0xFFFFu) *
+                          (uint32_t)p.f_pad * 2u;
   };
-  floatx4 acc[kDownTiles];
+  auto load_h = [&](uint32_t at, int u, u32x4 (&x)[kSteps]) {
+    const char* h = reinterpret_cast<const char*>(p.h);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      x[s] = *reinterpret_cast<const u32x4*>(h + (at + 2u * (kCols * u + step_col<WF>(s, q))));
+  };
+  uint32_t w_at[kDownTiles], s_at[kDownTiles];
+#pragma unroll
+  for (int i = 0; i < kDownTiles; ++i) {
+    const int r = min(16 * i + c16, p.d - 1 - r0);
+    w_at[i] = codes_at<WF>(p.down, r);
+    s_at[i] = WF == kMxWeights ? scales_at<WF>(p.down, r) : 0u;               // 32 rows lie in one block
+  }
+  struct Place {
+    const char *codes, *scales;
+    uint32_t h_at;
+  };
+  auto place = [&](int slot, Place& o) {
+    const int e = __builtin_amdgcn_readfirstlane(slot_expert[slot] & 0xFFFF);
+    o.codes = matrix_codes<WF>(p.down, e) + r0 * p.down.ld * (WF == kMxWeights ? 4 : 1);
+    o.scales = matrix_scales<WF>(p.down, e) +
+               (WF == kMxWeights ? r0 * p.down.lds : (int64_t)(r0 >> 7) * p.down.lds * 4);
+    o.h_at = part_at(slot, 0);
+  };
+  // Of the loads; past the last unit that unit is loaded again (no branch, as above).
+  int at_slot = 0, at_unit = 0, left = 0;
+  Place at;
+  auto load = [&](Unit& o) {
+#pragma unroll
+    for (int i = 0; i < kDownTiles; ++i) load_row(o.w[i], at.codes, w_at[i], at.scales, s_at[i], at_unit, q);
+    load_h(at.h_at, at_unit, o.x);
+    if (--left > 0 && ++at_unit == per_slot) {
+      at_unit = 0;
+      place(++at_slot, at);
+    }
+  };
+  floatx4 acc[kParts][kDownTiles];
   auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < kDownTiles; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < kParts; ++j)
+#pragma unroll
+      for (int i = 0; i < kDownTiles; ++i) acc[j][i] = floatx4{0.f, 0.f, 0.f, 0.f};
   };
-  auto multiply = [&](const Unit& o) {
+  auto multiply = [&](Unit& o, int slot, int u, int parts) {
 #pragma unroll
-    for (int i = 0; i < kDownTiles; ++i) {
-      const u32x4 w = transposed(o.w[i]);
-      floatx4 v = WF == kMxWeights ? acc[i] : floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < kDownTiles; ++i) arrange(o.w[i]);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const u32x4 wv = widen<GPTQ_BF16>(o.w[i], w, s);
-#pragma unroll
-        for (int j = 0; j < kPlanes; ++j) v = mfma16<GPTQ_BF16>(wv, o.x[j][s], v);
-      }
-      if constexpr (WF == kMxWeights) {
-        acc[i] = v;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(o.w[i].s, v[j], acc[i][j]);
-      }
-    }
-  };
-  // Register j of lane l: row 4 (l / 16) + j, the item's token l % 16.  A weight of 0
-  // leaves a token without the expert's product, whatever that is.
-  auto flush = [&](int item) {
-    bool there;
-    const int pair = pair_of(item, there);
-    const float w = weights[pair];
-    if (there && w != 0.f) {
-      float* to = mine + pair / p.k * kDownRows + 4 * q;
+    for (int j = 0; j < kParts; ++j) {
+      if (j >= parts) break;                 // the same for all lanes
+      if (j > 0) load_h(part_at(slot, j), u, o.x);
 #pragma unroll
       for (int i = 0; i < kDownTiles; ++i) {
-        floatx4 s = *reinterpret_cast<floatx4*>(to + 16 * i);
+        floatx4 v = WF == kMxWeights ? acc[j][i] : floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = __builtin_fmaf(w, acc[i][j], s[j]);
-        *reinterpret_cast<floatx4*>(to + 16 * i) = s;
+        for (int s = 0; s < kSteps; ++s) v = mfma16<GPTQ_BF16>(widen<GPTQ_BF16>(o.w[i], s), o.x[s], v);
+        if constexpr (WF == kMxWeights) acc[j][i] = v;
+        else add_scaled(acc[j][i], o.w[i].s, v);
       }
     }
   };
+  // Register i of lane l: row 4 (l / 16) + i, column l % 16.  A token's three columns
+  // are added; a weight of 0 leaves it without the expert's product, whatever that is.
+  auto flush = [&](int slot, int parts) {
+    const int n = slot_expert[slot] >> 16;
+#pragma unroll
+    for (int j = 0; j < kParts; ++j) {
+      if (j >= parts) break;
+      const int token = kPart * j + third;
+      const uint32_t pair = slot_pairs[slot * kSlot + min(token, n - 1)];
+      const float w = weights[pair & 0xFFFFu];
+      const bool there = c16 < 3 * kPart && c16 == 3 * third && token < n && w != 0.f;
+      float* to = mine + (pair >> 16) * kDownRows + 4 * q;
+#pragma unroll
+      for (int i = 0; i < kDownTiles; ++i) {
+        floatx4 v = acc[j][i];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += __shfl_down(acc[j][i][r], 1, 64) + __shfl_down(acc[j][i][r], 2, 64);
+        if (there) {
+          floatx4 s = *reinterpret_cast<floatx4*>(to + 16 * i);
+          add_scaled(s, w, v);
+          *reinterpret_cast<floatx4*>(to + 16 * i) = s;
+        }
+      }
+    }
+  };
+  auto parts_of = [&](int slot) {
+    return __builtin_amdgcn_readfirstlane(((slot_expert[slot] >> 16) + kPart - 1) / kPart);
+  };
   if (lo < hi) {
+    int slot = lo / per_slot, u = lo - slot * per_slot, parts = parts_of(slot);
+    at_slot = slot, at_unit = u, left = hi - lo;
+    place(slot, at);
     Unit ring[D];
 #pragma unroll
-    for (int i = 0; i < D; ++i) load(min(lo + i, hi - 1), ring[i]);
+    for (int i = 0; i < D; ++i) load(ring[i]);
     clear();
     for (int n = lo; n < hi; n += D) {
 #pragma unroll
       for (int i = 0; i < D; ++i) {
         if (n + i < hi) {
-          multiply(ring[i]);
-          if (n + i + 1 == hi || (n + i + 1) % per_item == 0) {
-            flush((n + i) / per_item);
+          multiply(ring[i], slot, u, parts);
+          ++u;
+          if (n + i + 1 == hi || u == per_slot) {
+            flush(slot, parts);
             clear();
+            u = 0;
+            ++slot;
+            if (n + i + 1 < hi) parts = parts_of(slot);
           }
         }
-        load(min(n + i + D, hi - 1), ring[i]);
+        load(ring[i]);
       }
+    }
+  }
+  // The columns behind the whole units, a slot at a time.
+  if constexpr (TAIL) {
+    const int s0 = (int)(slots * share / shares), s1 = (int)(slots * (share + 1) / shares);
+    for (int slot = s0; slot < s1; ++slot) {
+      Unit o;
+      place(slot, at);
+#pragma unroll
+      for (int i = 0; i < kDownTiles; ++i)
+        load_row_tail(o.w[i], at.codes, w_at[i], at.scales, s_at[i], per_slot, q, p.f);
+      load_h(at.h_at, per_slot, o.x);
+      clear();
+      multiply(o, slot, per_slot, parts_of(slot));
+      flush(slot, parts_of(slot));
     }
   }
   __syncthreads();
@@ -484,27 +627,42 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs p) {
   for (int i = tid; i < outputs; i += kThreads) {
     const int t = i / kDownRows, r = r0 + i % kDownRows;
     float v = sums[i];
+#pragma unroll
     for (int w = 1; w < kWaves; ++w) v += sums[w * outputs + i];
     if (r >= p.d) continue;
     if (p.splits == 1) store_y(p, (int64_t)t * p.ldy + r, v);
-    else p.part[((int64_t)split * p.tokens + t) * p.d + r] = v;
+    // Written through to where every workgroup of the device sees it.
+    else __hip_atomic_store(p.part + ((int64_t)split * p.tokens + t) * p.d + r, v, __ATOMIC_RELAXED,
+                            __HIP_MEMORY_SCOPE_AGENT);
   }
   if (p.splits == 1) return;
-  // The last workgroup of the group adds the parts, in order.
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+  // The last workgroup of the group adds the parts, in order.  The parts are stored
+  // and loaded past the caches of one XCD, and every wave waits for its own stores
+  // before its workgroup is counted, so whoever counts last finds all of them; an
+  // acquire and release of everything else would write back and drop the whole L2 (6
+  // to 9 us of 70 to 130).
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (tid == 0)
-    is_last = __hip_atomic_fetch_add(p.arrived + group, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+    is_last = __hip_atomic_fetch_add(p.arrived + group, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
               (uint32_t)p.splits - 1u;
   __syncthreads();
   if (!is_last) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   for (int i = tid; i < outputs; i += kThreads) {
     const int t = i / kDownRows, r = r0 + i % kDownRows;
     if (r >= p.d) continue;
+    // Eight loads in flight; past the last split its value again, not added.
     const float* at = p.part + (int64_t)t * p.d + r;
-    float v = at[0];
-    for (int s = 1; s < p.splits; ++s) v += at[(int64_t)s * p.tokens * p.d];
+    float v = 0.f;
+    for (int s = 0; s < p.splits; s += 8) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = __hip_atomic_load(at + (int64_t)min(s + j, p.splits - 1) * p.tokens * p.d, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v += s + j < p.splits ? x[j] : 0.f;
+    }
     store_y(p, (int64_t)t * p.ldy + r, v);
   }
 }
@@ -513,23 +671,24 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs p) {
 // Host.
 // ---------------------------------------------------------------------------
 struct Workspace {
-  size_t ids, weights, arrived, h, part, total;               // offsets in bytes
+  size_t slots, slot_pairs, arrived, h, part, total;          // offsets in bytes
 };
 constexpr int64_t kMaxSplits = 16;
 
 int down_splits(int64_t tokens, int64_t experts, int64_t topk, int64_t d, int64_t f) {
-  // Two workgroups a CU, a unit of 128 columns a wave at least.
+  // A workgroup a CU, a unit of 128 columns a wave at least.
   const int64_t groups = ceil_div(d, kDownRows), units = std::min(experts, tokens * topk) * ceil_div(f, 128);
-  return (int)std::max<int64_t>(1, std::min({kMaxSplits, 512 / groups, units / kWaves}));
+  return (int)std::max<int64_t>(1, std::min({kMaxSplits, 256 / groups, units / kWaves}));
 }
 
 Workspace workspace(int64_t tokens, int64_t experts, int64_t topk, int64_t d, int64_t f) {
-  const size_t pairs = (size_t)(tokens * topk), f_pad = (size_t)round_up(f, 128);
+  const size_t pairs = (size_t)(tokens * topk), f_pad = (size_t)round_up(f, kPadCols);
+  const size_t slots = (size_t)max_slots((int)tokens, (int)experts, (int)topk);
   const int splits = down_splits(tokens, experts, topk, d, f);
-  Workspace w;
-  w.ids = 0;
-  w.weights = align256(pairs * 4);
-  w.arrived = w.weights + align256(pairs * 4);
+  Workspace w;                               // the pairs' weights first
+  w.slots = align256(pairs * 4);
+  w.slot_pairs = w.slots + align256((slots + 1) * 4);
+  w.arrived = w.slot_pairs + align256(slots * kSlot * 4);
   w.h = w.arrived + align256((size_t)ceil_div(d, kDownRows) * 4);
   w.part = w.h + align256(kPlanes * pairs * f_pad * 2);
   w.total = w.part + (splits > 1 ? align256((size_t)splits * (size_t)(tokens * d) * 4) : 0);
@@ -541,16 +700,18 @@ bool sizes_fit(int64_t tokens, int64_t experts, int64_t topk, int64_t d, int64_t
          f <= kMxMaxCols / 2;
 }
 
+// Rows of a tile, and of X, are addressed with 32 bits.
+constexpr int64_t kMaxLd = (int64_t)1 << 23;
+
 // One stack of weights of `rows` x `cols`: words (bytes) and scales to a row, rows of
 // scales.
 gptq_status check_weights(const Weights& w, int64_t experts, int64_t rows, int64_t words, int64_t scale_rows,
                           int64_t scales) {
-  constexpr int64_t kMaxLd = (int64_t)1 << 40;
   if (w.codes == nullptr || w.scales == nullptr || w.ld < words || w.lds < scales) return GPTQ_ERR_INVALID_ARG;
   if (w.ld > kMaxLd || w.lds > kMaxLd) return GPTQ_ERR_UNSUPPORTED;
   if (experts == 1) return GPTQ_OK;
   if (w.stride < rows * w.ld || w.s_stride < scale_rows * w.lds) return GPTQ_ERR_INVALID_ARG;
-  return w.stride > (kMaxLd << 10) || w.s_stride > (kMaxLd << 10) ? GPTQ_ERR_UNSUPPORTED : GPTQ_OK;
+  return w.stride > (kMaxLd << 22) || w.s_stride > (kMaxLd << 22) ? GPTQ_ERR_UNSUPPORTED : GPTQ_OK;
 }
 
 template <int WF>
@@ -561,8 +722,7 @@ gptq_status layer(MoeArgs p, int64_t experts, int64_t d, int64_t f, int x_dtype,
     return GPTQ_ERR_INVALID_ARG;
   if (!sizes_fit(tokens, experts, topk, d, f)) return GPTQ_ERR_UNSUPPORTED;
   if (p.ldx < d || p.ldy < d || p.ld_logits < experts) return GPTQ_ERR_INVALID_ARG;
-  constexpr int64_t kMaxLd = (int64_t)1 << 40;
-  if (p.ldx > kMaxLd || p.ldy > kMaxLd || p.ld_logits > kMaxLd) return GPTQ_ERR_UNSUPPORTED;
+  if (p.ldx > kMaxLd || p.ldy > (kMaxLd << 17) || p.ld_logits > (kMaxLd << 17)) return GPTQ_ERR_UNSUPPORTED;
   if (tokens == 0 || d == 0) return GPTQ_OK;
   if (p.X == nullptr || p.logits == nullptr || p.Y == nullptr) return GPTQ_ERR_INVALID_ARG;
   constexpr bool MX = WF == kMxWeights;
@@ -576,8 +736,9 @@ gptq_status layer(MoeArgs p, int64_t experts, int64_t d, int64_t f, int x_dtype,
   if (ws == nullptr || ws_bytes < w.total) return GPTQ_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0) return GPTQ_ERR_INVALID_ARG;
   char* base = static_cast<char*>(ws);
-  p.ids = reinterpret_cast<int32_t*>(base + w.ids);
-  p.weights = reinterpret_cast<float*>(base + w.weights);
+  p.weights = reinterpret_cast<float*>(base);
+  p.slots = reinterpret_cast<int*>(base + w.slots);
+  p.slot_pairs = reinterpret_cast<uint32_t*>(base + w.slot_pairs);
   p.arrived = reinterpret_cast<uint32_t*>(base + w.arrived);
   p.h = reinterpret_cast<uint16_t*>(base + w.h);
   p.part = reinterpret_cast<float*>(base + w.part);
@@ -586,21 +747,24 @@ gptq_status layer(MoeArgs p, int64_t experts, int64_t d, int64_t f, int x_dtype,
   p.k = topk;
   p.d = (int)d;
   p.f = (int)f;
-  p.f_pad = (int)round_up(f, 128);
+  p.f_pad = (int)round_up(f, kPadCols);
   p.splits = down_splits(tokens, experts, topk, d, f);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int64_t pairs = tokens * topk, slots = std::min<int64_t>(experts, pairs);
+  const int64_t pairs = tokens * topk, slots = max_slots(p.tokens, p.experts, topk);
 
-  const size_t up_lds = kWaves * 2 * 64 * sizeof(floatx4) + experts * 8 + pairs * 4;
-  const unsigned up_grid = (unsigned)(slots * (p.f_pad / 16));
-  if (x_dtype == GPTQ_F16) moe_up_kernel<WF, GPTQ_F16><<<up_grid, kThreads, up_lds, st>>>(p);
-  else moe_up_kernel<WF, GPTQ_BF16><<<up_grid, kThreads, up_lds, st>>>(p);
+  const bool tail = d % Row<WF>::kCols != 0;
+  const int up_lds = (int)(2 * kWaves * 2 * 64 * sizeof(floatx4) + routes_lds(p.tokens, p.experts, topk));
+  const unsigned up_grid = (unsigned)std::min<int64_t>(slots * ceil_div(f, 16), 512);
+  const auto up = x_dtype == GPTQ_F16 ? (tail ? moe_up_kernel<WF, GPTQ_F16, true> : moe_up_kernel<WF, GPTQ_F16, false>)
+                                      : (tail ? moe_up_kernel<WF, GPTQ_BF16, true> : moe_up_kernel<WF, GPTQ_BF16, false>);
+  if (up_lds > 65536)
+    GPTQ_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(up), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                     up_lds));
+  up<<<up_grid, kThreads, up_lds, st>>>(p);
   GPTQ_TRY_LAUNCH();
 
-  // An item for every expert with tokens and every sixteen tokens more.
-  const size_t items = (size_t)(slots + pairs / 16);
-  const int down_lds = (int)(kWaves * tokens * kDownRows * 4 + experts * 8 + pairs * 8 + items * 4);
-  const auto k = moe_down_kernel<WF>;
+  const int down_lds = (int)(kWaves * tokens * kDownRows * 4 + pairs * 4 + slots * 4 * (1 + kSlot));
+  const auto k = f % Row<WF>::kCols != 0 ? moe_down_kernel<WF, true> : moe_down_kernel<WF, false>;
   if (down_lds > 65536)
     GPTQ_TRY_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                      down_lds));

@@ -9,6 +9,7 @@
 // kept between the launches, and no order depends on timing.  Up to 64 tokens
 // take one workgroup for all of it: a launch less.
 #include "moe.h"
+#include "mx.h"
 
 namespace gptq {
 namespace {
@@ -24,45 +25,54 @@ struct RouteArgs {
   int32_t* order;                            // tokens * k
 };
 
-__device__ inline int choose(const RouteArgs& p, int t) {
+__device__ inline void put(const RouteArgs& p, int t, const Routed& r) {
   const int lane = (int)threadIdx.x & 63;
-  const Routed r = route_token(p.logits, p.dtype, (int64_t)t * p.ld, p.experts, p.k, !p.renormalize);
   const float w = route_weight(r, p.k, p.renormalize);
   if (lane < p.k) {
     p.ids[(int64_t)t * p.k + lane] = r.id;
     p.weights[(int64_t)t * p.k + lane] = w;
   }
-  return r.id;
 }
 
 __global__ __launch_bounds__(256) void moe_choose_kernel(RouteArgs p) {
-  const int t = (int)(blockIdx.x * 4 + (threadIdx.x >> 6));
-  if (t < p.tokens) choose(p, t);
+  const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
+  route_tokens(p.logits, p.dtype, p.ld, t, min(t + 1, p.tokens), 1, p.experts, p.k, !p.renormalize,
+               [&](int token, const Routed& r) { put(p, token, r); });
 }
 
-// Sixteen waves, each with every sixteenth part of the pairs, 256 at a time (four
-// neighbouring ones a lane).
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+// Sixteen waves, each with every sixteenth part of the pairs, 1024 at a time: four
+// loads in flight, four neighbouring pairs a lane and load.
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortLoads = 4, kSortStep = 256 * kSortLoads;
 __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(RouteArgs p) {
   __shared__ int below[kSortWaves], equal[kSortWaves];
   const int e = (int)blockIdx.x, lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int pairs = p.tokens * p.k;
-  const int per = ((pairs + kSortWaves - 1) / kSortWaves + 255) / 256 * 256;
+  const int per = ((pairs + kSortWaves - 1) / kSortWaves + kSortStep - 1) / kSortStep * kSortStep;
   const int lo = min(wave * per, pairs), hi = min(lo + per, pairs);
-  auto load4 = [&](int at, int (&v)[4]) {
+  u32x4 v[kSortLoads];
+  auto load = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = at + i < hi ? p.ids[at + i] : 0x7FFFFFFF;
+    for (int j = 0; j < kSortLoads; ++j) {
+      const int at = b + 256 * j + 4 * lane;
+      if (b + kSortStep <= hi) {             // the same for all lanes
+        v[j] = *reinterpret_cast<const u32x4_a4*>(p.ids + at);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = at + i < hi ? (uint32_t)p.ids[at + i] : 0x7FFFFFFFu;
+      }
+    }
   };
   int less = 0, same = 0;
-  for (int b = lo; b < hi; b += 256) {
-    int v[4];
-    load4(b + 4 * lane, v);
+  for (int b = lo; b < hi; b += kSortStep) {
+    load(b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      less += v[i] < e;
-      same += v[i] == e;
-    }
+    for (int j = 0; j < kSortLoads; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        less += (int)v[j][i] < e;
+        same += (int)v[j][i] == e;
+      }
   }
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) {
@@ -84,20 +94,24 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(RouteArgs p) {
     p.offsets[e] = first;
     if (e == p.experts - 1) p.offsets[p.experts] = first + all;
   }
+  if (equal[wave] == 0) return;
   int at = first + mine;
   const uint64_t before = ((uint64_t)1 << lane) - 1;
-  for (int b = lo; b < hi; b += 256) {
-    int v[4], mark = at;
-    load4(b + 4 * lane, v);
+  for (int b = lo; b < hi; b += kSortStep) {
+    load(b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t hit = __ballot(v[i] == e);
-      mark += __popcll(hit & before);
-      at += __popcll(hit);
+    for (int j = 0; j < kSortLoads; ++j) {
+      int mark = at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t hit = __ballot((int)v[j][i] == e);
+        mark += __popcll(hit & before);
+        at += __popcll(hit);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((int)v[j][i] == e) p.order[mark++] = b + 256 * j + 4 * lane + i;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (v[i] == e) p.order[mark++] = b + 4 * lane + i;
   }
 }
 
@@ -107,10 +121,11 @@ __global__ __launch_bounds__(kSortThreads) void moe_route_kernel(RouteArgs p) {
   __shared__ int ids[kSmallTokens * kMoeMaxTopk];
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  for (int t = wave; t < p.tokens; t += kSortWaves) {
-    const int id = choose(p, t);
-    if (lane < p.k) ids[t * p.k + lane] = id;
-  }
+  route_tokens(p.logits, p.dtype, p.ld, wave, p.tokens, kSortWaves, p.experts, p.k, !p.renormalize,
+               [&](int t, const Routed& r) {
+                 put(p, t, r);
+                 if (lane < p.k) ids[t * p.k + lane] = r.id;
+               });
   __syncthreads();
   const int pairs = p.tokens * p.k;
   const uint64_t before = ((uint64_t)1 << lane) - 1;
