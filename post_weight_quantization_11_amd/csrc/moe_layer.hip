@@ -286,6 +286,7 @@ __device__ inline int route_all(const MoeArgs& p, unsigned char* lds, Routes& o)
 template <int WF, int XT, bool TAIL, bool SPLIT>
 __device__ inline bool up_tiles(const MoeArgs& p, const Routes& routes, int lo, int hi, floatx4* red) {
   constexpr int D = 1, kCols = Row<WF>::kCols, kSteps = Row<WF>::kSteps;
+  if (lo >= hi) return false;                // there are more workgroups than tiles: no tile to clamp loads to
   const int tid = (int)threadIdx.x, lane = tid & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // The waves share a tile's whole units, and a step each the columns behind them.
