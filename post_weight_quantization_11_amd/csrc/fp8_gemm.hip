@@ -546,22 +546,29 @@ constexpr TileShape kWideTileShapes[] = {
 // 9.8 us, 12 on tiles; 54 x 430 x 6080: 8.2 and 11; 64 x 4096 x 4096: 15 and 13).
 // Two tiles of W a workgroup read X half as often, one gives more workgroups (16 x
 // 4096 x 4096 9.5 and 9.8; 24 x 4096 x 4096 12.2 and 9.6; 2 x 3463 x 8368 13 and 15;
-// 1 x 49152 x 12288 161 and 110).
-Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool wide) {
+// 1 x 49152 x 12288 161 and 110).  `odd`: rows that do not start at whole 32-bit words,
+// which their 16-byte loads take twice as long for (77 x 4096 x 11008 on them 52 and
+// 130 us, on tiles 27 and 33): they take up to 2^25 weights (16 x 4099 x 4097 15.7 us,
+// 17.4 on tiles; 1 x 4099 x 11007 33 and 27; 64 experts' 256 x 1025 x 2047 80 and 48).
+constexpr int64_t kOddWeights = (int64_t)1 << 25;
+Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool wide, bool odd) {
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
   if (grouped) {
     // By the rows that an expert has on average (8 experts of 11008 x 4096 with 8
     // rows each: 92 us, 97 on tiles, with 64 373 and 155; 4 of 500 x 9000 with 10: 13
     // and 47; 100 of 512 x 512 with 20: 29 and 14).
-    if (rows < 8 * experts || (rows < 16 * experts && products <= 300000000))
-      return Plan{std::min(experts, rows) * ceil_div(m, 32) < 256 ? kRows1 : kRows2, 1};
-  } else if (rows <= 16 || products <= 600000000) {
-    if (rows <= 4 && m >= 2048 && m <= 6144 && n >= 6144) return Plan{kRows1Pinned, 1};
+    const int64_t touched = std::min(experts, rows);
+    if (odd ? rows < 16 * experts && touched * m * n <= kOddWeights
+            : rows < 8 * experts || (rows < 16 * experts && products <= 300000000))
+      return Plan{touched * ceil_div(m, 32) < 256 ? kRows1 : kRows2, 1};
+  } else if (odd ? m * n <= kOddWeights && products <= 300000000 : rows <= 16 || products <= 600000000) {
+    if (!odd && rows <= 4 && m >= 2048 && m <= 6144 && n >= 6144) return Plan{kRows1Pinned, 1};
     return Plan{outputs <= 65536 && m < 8192 ? kRows1 : kRows2, 1};
   }
-  const int64_t e = grouped ? experts : 0;
-  const TileChoice c = wide ? choose_tiles(kWideTileShapes, m, n, rows, e, 4.0, 0.2e-6)
-                            : choose_tiles(kTileShapes, m, n, rows, e, 4.0, 0.2e-6);
+  // Experts with fewer rows than a tile take a whole one each.
+  const int64_t e = grouped ? experts : 0, least = grouped ? std::min(experts, rows) : 0;
+  const TileChoice c = wide ? choose_tiles(kWideTileShapes, m, n, rows, e, 4.0, 0.2e-6, least)
+                            : choose_tiles(kTileShapes, m, n, rows, e, 4.0, 0.2e-6, least);
   return Plan{(Kind)c.kind, c.splits};
 }
 
@@ -613,11 +620,15 @@ gptq_status launch_tile(const Fp8Operands& p, const Plan& pl, void* ws, hipStrea
   return GPTQ_OK;
 }
 
+// What the addresses of all rows have in common: the low bits that are 0.
+uint64_t row_starts(const Fp8Operands& p) {
+  return reinterpret_cast<uintptr_t>(p.X) | reinterpret_cast<uintptr_t>(p.W) | (uint64_t)(p.rows > 1 ? p.ldx : 0) |
+         (uint64_t)(p.m > 1 ? p.ldw : 0) | (uint64_t)p.w_stride;
+}
+
 template <bool WIDE, int WR, int WC, int RB, int CB, int NB>
 gptq_status launch_tiles(const Fp8Operands& p, const Plan& pl, void* ws, hipStream_t st) {
-  const uint64_t starts = reinterpret_cast<uintptr_t>(p.X) | reinterpret_cast<uintptr_t>(p.W) | (uint64_t)p.ldx |
-                          (uint64_t)p.ldw | (uint64_t)p.w_stride;
-  if ((starts & 15) == 0) return launch_tile<WIDE, WR, WC, RB, CB, NB, true>(p, pl, ws, st);
+  if ((row_starts(p) & 15) == 0) return launch_tile<WIDE, WR, WC, RB, CB, NB, true>(p, pl, ws, st);
   return launch_tile<WIDE, WR, WC, RB, CB, 2, false>(p, pl, ws, st);
 }
 
@@ -633,7 +644,8 @@ gptq_status launch_rows(const Fp8Operands& p, hipStream_t st) {
 
 template <bool WIDE>
 gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, hipStream_t st) {
-  Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, WIDE);
+  const uint64_t starts = row_starts(p);
+  Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, WIDE, (starts & 3) != 0);
   // The tile kernels address the rows of a tile with 32 bits; rows further apart
   // take the row kernel.
   constexpr int64_t kMaxPitch = (int64_t)1 << 22;
@@ -685,10 +697,14 @@ extern "C" size_t gptq_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, i
   if (m <= 0 || n < 0 || rows <= 0 || experts <= 0 || n > kFp8MaxCols || m > GPTQ_MX_MAX_ROWS ||
       rows > GPTQ_MX_MAX_ROWS || experts > GPTQ_MX_MAX_EXPERTS)
     return 0;
-  // Of one matrix with either kind of Y; products grouped by expert need none.
+  // Of one matrix with either kind of Y and rows of any alignment; products grouped
+  // by expert need none.
   if (experts > 1) return 0;
-  return std::max(plan_ws(make_plan(m, n, rows, 1, false, false), m, rows),
-                  plan_ws(make_plan(m, n, rows, 1, false, true), m, rows));
+  size_t need = 0;
+  for (int wide = 0; wide < 2; ++wide)
+    for (int odd = 0; odd < 2; ++odd)
+      need = std::max(need, plan_ws(make_plan(m, n, rows, 1, false, wide != 0, odd != 0), m, rows));
+  return need;
 }
 
 extern "C" gptq_status gptq_block_gemm(const uint8_t* codes, int64_t m, int64_t n, int64_t ld_codes, const float* scales,

@@ -185,7 +185,7 @@ inline int64_t max_tiles(int64_t rows, int64_t experts, bool grouped, int tile) 
 // (a launch, and the bytes that they move).  A round's time grows from `one` (a
 // workgroup a CU) to `full` along a square root (a few CUs with two already hold
 // the rest up).  Grouped by expert (experts > 0): half a tile more for every expert
-// that can have rows, and no splits.
+// that can have rows, `least_tiles` of X rows at least, and no splits.
 struct TileShape {
   int kind;                                  // of the caller
   int bm, bn, per_cu;                        // rows of W and of X, workgroups a CU holds
@@ -197,14 +197,14 @@ struct TileChoice {
 constexpr int kSplitCols = 256;              // a split is a multiple of this
 template <size_t N>
 TileChoice choose_tiles(const TileShape (&shapes)[N], int64_t m, int64_t n, int64_t rows, int64_t experts,
-                        double join, double join_bytes) {
+                        double join, double join_bytes, int64_t least_tiles = 0) {
   const int max_splits = experts > 0 ? 1 : 16;
   TileChoice best{shapes[0].kind, 1};
   double least = std::numeric_limits<double>::infinity();
   const double parts = (double)m * (double)rows * 8.0;       // bytes that a split's sums move
   for (const TileShape& s : shapes) {
     const int64_t partial = (std::min(experts, rows) + 1) / 2, held = 256 * s.per_cu;
-    const int64_t tiles = ceil_div(m, s.bm) * (ceil_div(rows, s.bn) + partial);
+    const int64_t tiles = ceil_div(m, s.bm) * std::max(ceil_div(rows, s.bn) + partial, least_tiles);
     for (int splits = 1; splits <= max_splits && (splits == 1 || n >= (int64_t)splits * kSplitCols); ++splits) {
       const int64_t groups = tiles * splits, rest = groups % held;
       double t = (double)(groups / held) * s.full;
