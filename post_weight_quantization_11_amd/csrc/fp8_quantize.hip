@@ -5,18 +5,19 @@
 //   code  = the e4m3 value nearest to the quotient w / scale, ties to the even code
 //
 // The quotient is not a float32 number, and rounding it to one first would put
-// those within 2^-24 of a border between two codes on the border.  It is rounded
-// to odd instead: the nearest float32 t, moved, where it is even and not exact,
-// to the odd neighbour on the side of the remainder w - t scale (exact in one
-// fused multiply-add).  Borders are even float32 numbers, so the conversion
-// instruction, which rounds to the nearest even code, sees every quotient on its
-// own side.  Scale and values are first multiplied by the power of two that
-// brings the scale to [1, 2), so that no remainder is lost to underflow.
+// those within 2^-24 of a border between two codes on the border.  Instead w times
+// the reciprocal, a few units off, is rounded to 20 bits: t.  Borders have at most 5
+// bits, so the only one that can lie between t and the quotient is t itself, and
+// the sign of the remainder w - t scale, exact in one fused multiply-add, says on
+// which side: t is moved one unit there.  The conversion instruction, which rounds
+// to the nearest even code, then sees every quotient on its own side of a border.
+// The remainder is a multiple of 2^-46 |w| (nearly): under scales below 2^-80 values
+// and scale are multiplied by 2^60 first, so that it is not lost to underflow.
 //
-// One pass.  Blocks of a row: a thread takes 8 columns, sixteen neighbouring
-// threads a block, its maximum in four steps across the lanes.  Blocks of 128 x
-// 128: a workgroup takes one, 64 values a thread in registers between the
-// maximum and the codes.  Reads, codes and Wq are contiguous.
+// One pass.  Blocks of a row: a thread takes 16 columns, eight neighbouring threads
+// a block, its maximum in three steps across the lanes.  Blocks of 128 x 128: a
+// workgroup takes one or four neighbouring ones, 64 values a thread in registers
+// between the maximum and the codes.  Reads, codes and Wq are contiguous.
 #include "fp8.h"
 
 namespace gptq {
@@ -60,38 +61,34 @@ template <int DT> __device__ inline float block_scale(uint32_t amax) {
   return fmaxf(top / kFp8Max, 0x1p-126f);
 }
 
-// What the codes of a block need of its scale: 2^exp scale in [1, 2).
+// What the codes of a block need of its scale.
 struct Divisor {
-  float s, r;                                // and (nearly) its reciprocal
-  int exp;
+  float up, s, r;                            // 1 or 2^60, the scale times that, nearly its reciprocal
 };
 __device__ inline Divisor divisor(float scale) {
-  const int exp = 127 - (int)(__float_as_uint(scale) >> 23);
-  const float s = ldexpf(scale, exp);
-  return Divisor{s, __builtin_amdgcn_rcpf(s), exp};
+  const float up = scale < 0x1p-80f ? 0x1p60f : 1.f;
+  return Divisor{up, scale * up, __builtin_amdgcn_rcpf(scale * up)};
 }
 
-// w / scale rounded to odd.
+// w / scale on its side of every border between two codes.
 __device__ inline float quotient(float w, const Divisor& d) {
-  const float a = ldexpf(fabsf(w), d.exp);
-  float t = a * d.r;
-  t = __builtin_fmaf(__builtin_fmaf(-t, d.s, a), d.r, t);      // the nearest float32
-  const float rest = __builtin_fmaf(-t, d.s, a);
-  uint32_t b = __float_as_uint(t);
-  b = (rest < 0.f ? b - 1u : b) | (rest != 0.f ? 1u : 0u);     // even b: b - 1 is odd; odd b: b - 1 | 1 is b
-  return __builtin_copysignf(__uint_as_float(b), w);
+  const float a = fabsf(w) * d.up;
+  const uint32_t t = (__float_as_uint(a * d.r) + 8u) & ~15u;
+  const int rest = (int)__float_as_uint(__builtin_fmaf(-__uint_as_float(t), d.s, a));
+  int side;                                  // -1, 0 or 1 (of min and max the compiler makes compares and selects)
+  asm("v_med3_i32 %0, %1, -1, 1" : "=v"(side) : "v"(rest));
+  return __builtin_copysignf(__uint_as_float(t + (uint32_t)side), w);
 }
 
 template <int DT>
 __device__ inline u32x2 encode(const typename Fp8x8<DT>::Vec& v, const Divisor& d) {
+  auto at = [&](int i) { return quotient(Fp8x8<DT>::at(v, i), d); };
   u32x2 c;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     int w = 0;
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(Fp8x8<DT>::at(v, 4 * i), d), quotient(Fp8x8<DT>::at(v, 4 * i + 1), d),
-                                        w, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(Fp8x8<DT>::at(v, 4 * i + 2), d),
-                                        quotient(Fp8x8<DT>::at(v, 4 * i + 3), d), w, true);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(at(4 * i), at(4 * i + 1), w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(at(4 * i + 2), at(4 * i + 3), w, true);
     c[i] = (uint32_t)w;
   }
   return c;
@@ -187,84 +184,105 @@ __device__ inline void finish8(const QuantArgs<DT>& p, int64_t e, int64_t r, int
   }
 }
 
-// groups: threads with columns, `per_row` (a multiple of 16: whole blocks) to a row.
+// Sixteen columns a thread.  groups: threads with columns, `per_row` (a multiple of 8:
+// whole blocks) to a row.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void fp8_quantize_rows_kernel(QuantArgs<DT> p, uint32_t groups, uint32_t per_row,
                                                                      GroupDiv div) {
   const uint32_t g = blockIdx.x * kThreads + threadIdx.x;
-  // groups is a multiple of 16, so a block's lanes leave together.
+  // groups is a multiple of 8, so a block's lanes leave together.
   if (g >= groups) return;
   const int64_t e = blockIdx.y, r = (int64_t)(((uint64_t)g * div.mul) >> div.shift);
-  const int k0 = (int)(g - (uint32_t)r * per_row) * 8;
-  typename Fp8x8<DT>::Vec v;
-  load8<DT>(p.W + e * p.w_stride + r * p.ldw + k0, p.n - k0, v);
-  uint32_t a = Fp8x8<DT>::amax(v);
+  const int k0 = (int)(g - (uint32_t)r * per_row) * 16;
+  typename Fp8x8<DT>::Vec v[2];
 #pragma unroll
-  for (int x = 1; x < 16; x <<= 1) a = max(a, (uint32_t)__shfl_xor((int)a, x, 64));
+  for (int i = 0; i < 2; ++i) load8<DT>(p.W + e * p.w_stride + r * p.ldw + k0 + 8 * i, p.n - k0 - 8 * i, v[i]);
+  uint32_t a = max(Fp8x8<DT>::amax(v[0]), Fp8x8<DT>::amax(v[1]));
+#pragma unroll
+  for (int x = 1; x < 8; x <<= 1) a = max(a, (uint32_t)__shfl_xor((int)a, x, 64));
   const float scale = block_scale<DT>(a);
-  if ((threadIdx.x & 15) == 0) p.scales[e * p.s_stride + r * p.lds + (k0 >> 7)] = scale;
-  finish8<DT>(p, e, r, k0, scale, divisor(scale), v);
+  if ((threadIdx.x & 7) == 0) p.scales[e * p.s_stride + r * p.lds + (k0 >> 7)] = scale;
+  const Divisor d = divisor(scale);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) finish8<DT>(p, e, r, k0 + 8 * i, scale, d, v[i]);
 }
 
-// One block of 128 x 128 a workgroup; m: rows from the launch's first on.
-template <int DT>
-__global__ __launch_bounds__(kThreads) void fp8_quantize_blocks_kernel(QuantArgs<DT> p, int64_t m, uint32_t per_row) {
-  constexpr int kRows = kThreads / 16, kPasses = kFp8Block / kRows;
-  __shared__ uint32_t tops[kThreads / 64];
+// BLOCKS neighbouring blocks of 128 x 128 a workgroup, sixteen rows at a time.  Four
+// read 512 columns of a row in one go (49152 x 12288 float16 with Wq 560 us, 600 one by
+// one); one gives small matrices more workgroups.  m: rows from the launch's first on;
+// per_row: such groups of blocks.
+template <int DT, int BLOCKS>
+__global__ __launch_bounds__(256 * BLOCKS, DT == GPTQ_F32 ? 4 : 8) void fp8_quantize_blocks_kernel(
+    QuantArgs<DT> p, int64_t m, uint32_t per_row) {
+  constexpr int kRows = 16, kPasses = kFp8Block / kRows;
+  __shared__ uint32_t tops[BLOCKS][kRows];
+  const int at = (int)threadIdx.x % (16 * BLOCKS), row = (int)threadIdx.x / (16 * BLOCKS), l16 = at & 15;
   const int64_t e = blockIdx.y, rb = blockIdx.x / per_row;
-  const int cb = (int)(blockIdx.x - (uint32_t)rb * per_row);
-  const int k0 = cb * kFp8Block + (int)(threadIdx.x & 15) * 8;
-  const int64_t r0 = rb * kFp8Block + (threadIdx.x >> 4);
+  const int k0 = (int)(blockIdx.x - (uint32_t)rb * per_row) * (kFp8Block * BLOCKS) + at * 8;
+  const int64_t r0 = rb * kFp8Block + row;
   typename Fp8x8<DT>::Vec v[kPasses];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int64_t r = r0 + i * kRows;
-    load8<DT>(p.W + e * p.w_stride + min(r, m - 1) * p.ldw + k0, p.n - k0, v[i]);
-  }
+  for (int i = 0; i < kPasses; ++i)
+    load8<DT>(p.W + e * p.w_stride + min(r0 + i * kRows, m - 1) * p.ldw + k0, p.n - k0, v[i]);
   uint32_t a = 0u;                           // rows past the last repeat it
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) a = max(a, Fp8x8<DT>::amax(v[i]));
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) a = max(a, (uint32_t)__shfl_xor((int)a, x, 64));
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = a;
+  for (int x = 1; x < 16; x <<= 1) a = max(a, (uint32_t)__shfl_xor((int)a, x, 64));
+  if (l16 == 0) tops[at >> 4][row] = a;
   __syncthreads();
-  a = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+  a = tops[at >> 4][l16];
+#pragma unroll
+  for (int x = 1; x < 16; x <<= 1) a = max(a, (uint32_t)__shfl_xor((int)a, x, 64));
   const float scale = block_scale<DT>(a);
-  if (threadIdx.x == 0) p.scales[e * p.s_stride + rb * p.lds + cb] = scale;
+  if (row == 0 && l16 == 0 && k0 < p.n) p.scales[e * p.s_stride + rb * p.lds + (k0 >> 7)] = scale;
   const Divisor d = divisor(scale);
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int64_t r = r0 + i * kRows;
-    if (r < m) finish8<DT>(p, e, r, k0, scale, d, v[i]);
-  }
+  for (int i = 0; i < kPasses; ++i)
+    if (r0 + i * kRows < m) finish8<DT>(p, e, r0 + i * kRows, k0, scale, d, v[i]);
 }
 
-template <int DT>
-gptq_status launch(QuantArgs<DT> p, int64_t experts, int64_t m, int block_rows, hipStream_t st) {
-  const int64_t blocks = ceil_div(p.n, kFp8Block);
-  const int64_t per_row = block_rows == 1 ? blocks * 16 : blocks;
-  // Rows a launch: a multiple of the block's.
-  const int64_t slab = block_rows == 1 ? std::max<int64_t>(1, kMaxSlab / per_row)
-                                       : std::max<int64_t>(1, kMaxSlab / kThreads / per_row) * kFp8Block;
+// Calls part(rows of the launch, its operands) for as many rows at a time as one launch
+// takes: `per` threads to a unit of `unit` rows.
+template <int DT, typename Part>
+gptq_status in_parts(const QuantArgs<DT>& p, int64_t m, int block_rows, int64_t unit, int64_t per, Part part) {
+  const int64_t slab = std::max<int64_t>(1, kMaxSlab / per) * unit;
   for (int64_t r0 = 0; r0 < m; r0 += slab) {
-    const int64_t rows = std::min(slab, m - r0);
     QuantArgs<DT> q = p;
     q.W += r0 * p.ldw;
     q.codes += r0 * p.ldc;
     q.scales += r0 / block_rows * p.lds;
     if (q.Wq != nullptr) q.Wq += r0 * p.ldq;
-    if (block_rows == 1) {
-      const uint32_t groups = (uint32_t)(rows * per_row);
-      fp8_quantize_rows_kernel<DT><<<dim3((unsigned)ceil_div(groups, kThreads), (unsigned)experts), kThreads, 0, st>>>(
-          q, groups, (uint32_t)per_row, group_div((uint32_t)per_row));
-    } else {
-      fp8_quantize_blocks_kernel<DT>
-          <<<dim3((unsigned)(ceil_div(rows, kFp8Block) * per_row), (unsigned)experts), kThreads, 0, st>>>(
-              q, rows, (uint32_t)per_row);
-    }
+    part(std::min(slab, m - r0), q);
     GPTQ_TRY_LAUNCH();
   }
   return GPTQ_OK;
+}
+
+template <int DT, int BLOCKS>
+gptq_status launch_blocks(const QuantArgs<DT>& p, int64_t experts, int64_t m, hipStream_t st) {
+  const int64_t per_row = ceil_div(p.n, kFp8Block * BLOCKS);
+  return in_parts<DT>(p, m, kFp8Block, kFp8Block, per_row * 256 * BLOCKS, [&](int64_t rows, const QuantArgs<DT>& q) {
+    fp8_quantize_blocks_kernel<DT, BLOCKS>
+        <<<dim3((unsigned)(ceil_div(rows, kFp8Block) * per_row), (unsigned)experts), 256 * BLOCKS, 0, st>>>(
+            q, rows, (uint32_t)per_row);
+  });
+}
+
+template <int DT>
+gptq_status launch(const QuantArgs<DT>& p, int64_t experts, int64_t m, int block_rows, hipStream_t st) {
+  const int64_t blocks = ceil_div(p.n, kFp8Block);
+  if (block_rows != 1) {
+    // Four blocks a workgroup where that still gives two workgroups a CU.
+    if (ceil_div(m, kFp8Block) * blocks * experts >= 4 * 512) return launch_blocks<DT, 4>(p, experts, m, st);
+    return launch_blocks<DT, 1>(p, experts, m, st);
+  }
+  const int64_t per_row = blocks * 8;
+  return in_parts<DT>(p, m, 1, 1, per_row, [&](int64_t rows, const QuantArgs<DT>& q) {
+    const uint32_t groups = (uint32_t)(rows * per_row);
+    fp8_quantize_rows_kernel<DT><<<dim3((unsigned)ceil_div(groups, kThreads), (unsigned)experts), kThreads, 0, st>>>(
+        q, groups, (uint32_t)per_row, group_div((uint32_t)per_row));
+  });
 }
 
 template <int DT>

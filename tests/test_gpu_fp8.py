@@ -554,3 +554,17 @@ def test_binding_refusals(g):
     with pytest.raises(g.GptqError):
         g.gptq_block_gemm(W, S, X, XS, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     g.gptq_block_gemm(W, S, X, XS, ws=torch.empty(need, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_quantize_many_blocks(g, dtype):
+    # Enough blocks that a workgroup takes four; three strips of rows of them, the
+    # last one partial, and the last columns of all.
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    W = (torch.randn((20010, 1800), device="cuda", generator=gen) * 0.05).to(_dt(dtype))
+    q = g.gptq_block_quantize(W, 128, want_wq=True)
+    for strip in (0, 77, 156):
+        rows = slice(128 * strip, 128 * strip + 128)
+        part = {k: q[k][slice(strip, strip + 1) if k == "scales" else rows] for k in q}
+        _check_quantized(part, W[rows].double().cpu().numpy(), 128, dtype)
