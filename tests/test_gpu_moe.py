@@ -173,6 +173,7 @@ LAYERS = [
     (1, 1, 1, 1, 1), (1, 2, 1, 16, 16), (1, 8, 2, 256, 384), (2, 5, 5, 70, 33), (3, 70, 4, 130, 100), (7, 4, 2, 515, 300),
     (16, 64, 6, 256, 128), (17, 3, 1, 200, 257), (33, 6, 3, 129, 65), (64, 2, 2, 100, 140), (64, 1, 1, 130, 70),
     (5, 300, 16, 64, 40), (2, 1024, 3, 24, 24), (4, 3, 2, 1100, 1030), (64, 9, 3, 320, 520),
+    (6, 4, 2, 512, 768),
 ]
 
 
