@@ -51,23 +51,26 @@ __device__ inline float route_exp(float l, float m) { return l == m ? 1.f : expf
 template <int L> struct RouteKeys {
   uint32_t keys[L];
 };
-template <int L>
-__device__ inline void route_load(RouteKeys<L>& o, const void* logits, int dtype, int64_t row, int experts) {
+// F32: of float32 logits.  (Chosen at run time, every load stood behind a branch of
+// its own, and the compiler waited for each before the next.)
+template <int L, bool F32>
+__device__ inline void route_load(RouteKeys<L>& o, const void* logits, int64_t row, int experts) {
   const int lane = (int)threadIdx.x & 63;
 #pragma unroll
   for (int j = 0; j < L; ++j) {
     const int64_t at = row + min(64 * j + lane, experts - 1);
-    o.keys[j] = dtype == GPTQ_F32 ? static_cast<const uint32_t*>(logits)[at] : static_cast<const uint16_t*>(logits)[at];
+    if constexpr (F32) o.keys[j] = static_cast<const uint32_t*>(logits)[at];
+    else o.keys[j] = static_cast<const uint16_t*>(logits)[at];
   }
 }
 
-template <int L>
+template <int L, bool F32>
 __device__ inline Routed route_choose(RouteKeys<L> o, int dtype, int experts, int k, bool want_sum) {
   const int lane = (int)threadIdx.x & 63;
   uint32_t (&keys)[L] = o.keys;
 #pragma unroll
   for (int j = 0; j < L; ++j) {
-    const float l = dtype == GPTQ_F32   ? __uint_as_float(keys[j])
+    const float l = F32                 ? __uint_as_float(keys[j])
                     : dtype == GPTQ_F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)keys[j])
                                         : __uint_as_float(keys[j] << 16);
     keys[j] = 64 * j + lane < experts ? route_key(l) : 0u;
@@ -106,25 +109,32 @@ __device__ inline Routed route_choose(RouteKeys<L> o, int dtype, int experts, in
 }
 
 // Tokens t, t + step, ... below `tokens`, one after the other; the next one's logits
-// are on their way meanwhile.  done(t, Routed).
-template <int L, typename Done>
+// are on their way meanwhile.  done(t, Routed); want_sum(t): whether it is to have the
+// sum over all experts.
+template <int L, bool F32, typename Want, typename Done>
 __device__ inline void route_some(const void* logits, int dtype, int64_t ld, int t, int tokens, int step, int experts,
-                                  int k, bool want_sum, Done done) {
+                                  int k, Want want_sum, Done done) {
   if (t >= tokens) return;
   RouteKeys<L> next;
-  route_load(next, logits, dtype, (int64_t)t * ld, experts);
+  route_load<L, F32>(next, logits, (int64_t)t * ld, experts);
   for (; t < tokens; t += step) {
     const RouteKeys<L> now = next;
-    route_load(next, logits, dtype, (int64_t)min(t + step, tokens - 1) * ld, experts);
-    done(t, route_choose(now, dtype, experts, k, want_sum));
+    route_load<L, F32>(next, logits, (int64_t)min(t + step, tokens - 1) * ld, experts);
+    done(t, route_choose<L, F32>(now, dtype, experts, k, want_sum(t)));
   }
 }
-template <typename Done>
+template <bool F32, typename Want, typename Done>
+__device__ inline void route_typed(const void* logits, int dtype, int64_t ld, int t, int tokens, int step, int experts,
+                                   int k, Want want_sum, Done done) {
+  if (experts <= 64) route_some<1, F32>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
+  else if (experts <= 256) route_some<4, F32>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
+  else route_some<kMoeMaxExperts / 64, F32>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
+}
+template <typename Want, typename Done>
 __device__ inline void route_tokens(const void* logits, int dtype, int64_t ld, int t, int tokens, int step, int experts,
-                                    int k, bool want_sum, Done done) {
-  if (experts <= 64) route_some<1>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
-  else if (experts <= 256) route_some<4>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
-  else route_some<kMoeMaxExperts / 64>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
+                                    int k, Want want_sum, Done done) {
+  if (dtype == GPTQ_F32) route_typed<true>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
+  else route_typed<false>(logits, dtype, ld, t, tokens, step, experts, k, want_sum, done);
 }
 
 // Lane i's probability of the i-th expert.  A token whose logits are all -inf (or
@@ -140,5 +150,9 @@ __device__ inline float route_weight(const Routed& r, int k, bool renormalize) {
   }
   return w / sum;
 }
+
+// Launches the choice alone: ids and weights of tokens >= 1.
+gptq_status moe_choose(const void* logits, int dtype, int64_t ld, int tokens, int experts, int k, bool renormalize,
+                       int32_t* ids, float* weights, hipStream_t stream);
 
 }  // namespace gptq

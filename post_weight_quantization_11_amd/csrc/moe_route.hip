@@ -6,8 +6,8 @@
 // experts) and takes the maximum k times.  Sorting: one workgroup an expert reads
 // all pairs' experts, 4 bytes each, counts those of lower experts (its first
 // place) and places its own in their order: nothing but the pairs themselves is
-// kept between the launches, and no order depends on timing.  Up to 64 tokens
-// take one workgroup for all of it: a launch less.
+// kept between the launches, and no order depends on timing.  Few tokens take one
+// workgroup for all of it: a launch less.
 #include "moe.h"
 #include "mx.h"
 
@@ -36,7 +36,7 @@ __device__ inline void put(const RouteArgs& p, int t, const Routed& r) {
 
 __global__ __launch_bounds__(256) void moe_choose_kernel(RouteArgs p) {
   const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
-  route_tokens(p.logits, p.dtype, p.ld, t, min(t + 1, p.tokens), 1, p.experts, p.k, !p.renormalize,
+  route_tokens(p.logits, p.dtype, p.ld, t, min(t + 1, p.tokens), 1, p.experts, p.k, [&](int) { return !p.renormalize; },
                [&](int token, const Routed& r) { put(p, token, r); });
 }
 
@@ -115,40 +115,57 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(RouteArgs p) {
   }
 }
 
-// Both for at most kSmallTokens tokens.
+// Both for few tokens: an expert's tokens are the bits of a 64-bit
+// number in LDS, whichever wave sets them, and its places a prefix sum, a thread an
+// expert.
 constexpr int kSmallTokens = 64;
+static_assert(kSortThreads >= kMoeMaxExperts && kSortThreads >= kSmallTokens * kMoeMaxTopk);
 __global__ __launch_bounds__(kSortThreads) void moe_route_kernel(RouteArgs p) {
-  __shared__ int ids[kSmallTokens * kMoeMaxTopk];
-  const int lane = (int)threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  route_tokens(p.logits, p.dtype, p.ld, wave, p.tokens, kSortWaves, p.experts, p.k, !p.renormalize,
+  __shared__ int ids[kSmallTokens * kMoeMaxTopk], first[kMoeMaxExperts], sums[kSortWaves];
+  __shared__ unsigned long long masks[kMoeMaxExperts];
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  masks[tid] = 0u;
+  __syncthreads();
+  route_tokens(p.logits, p.dtype, p.ld, wave, p.tokens, kSortWaves, p.experts, p.k, [&](int) { return !p.renormalize; },
                [&](int t, const Routed& r) {
                  put(p, t, r);
-                 if (lane < p.k) ids[t * p.k + lane] = r.id;
+                 if (lane < p.k) {
+                   ids[t * p.k + lane] = r.id;
+                   atomicOr(masks + r.id, 1ull << t);
+                 }
                });
   __syncthreads();
-  const int pairs = p.tokens * p.k;
-  const uint64_t before = ((uint64_t)1 << lane) - 1;
-  for (int e = wave; e < p.experts; e += kSortWaves) {
-    int at = 0, same = 0;
-    for (int b = 0; b < pairs; b += 64) {
-      const int v = b + lane < pairs ? ids[b + lane] : 0x7FFFFFFF;
-      at += __popcll(__ballot(v < e));
-      same += __popcll(__ballot(v == e));
-    }
-    if (lane == 0) {
-      p.offsets[e] = at;
-      if (e == p.experts - 1) p.offsets[p.experts] = at + same;
-    }
-    for (int b = 0; same > 0 && b < pairs; b += 64) {
-      const uint64_t hit = __ballot(b + lane < pairs && ids[b + lane] == e);
-      if (hit >> lane & 1) p.order[at + __popcll(hit & before)] = b + lane;
-      at += __popcll(hit);
-    }
+  const int own = __popcll(masks[tid]);
+  int upto = own;
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) {
+    const int v = __shfl_up(upto, x, 64);
+    if (lane >= x) upto += v;
+  }
+  if (lane == 63) sums[wave] = upto;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) upto += sums[w];
+  first[tid] = upto - own;
+  if (tid < p.experts) p.offsets[tid + 1] = upto;
+  if (tid == 0) p.offsets[0] = 0;
+  __syncthreads();
+  if (tid < p.tokens * p.k) {
+    const int e = ids[tid], t = tid / p.k;
+    p.order[first[e] + __popcll(masks[e] & ((1ull << t) - 1))] = tid;
   }
 }
 
 }  // namespace
+
+gptq_status moe_choose(const void* logits, int dtype, int64_t ld, int tokens, int experts, int k, bool renormalize,
+                       int32_t* ids, float* weights, hipStream_t stream) {
+  const RouteArgs p{logits, dtype, ld, tokens, experts, k, renormalize, ids, weights, nullptr, nullptr};
+  moe_choose_kernel<<<(unsigned)ceil_div(tokens, 4), 256, 0, stream>>>(p);
+  GPTQ_TRY_LAUNCH();
+  return GPTQ_OK;
+}
+
 }  // namespace gptq
 
 using namespace gptq;
@@ -166,13 +183,16 @@ extern "C" gptq_status gptq_moe_route(const void* logits, int l_dtype, int64_t t
   const RouteArgs p{logits, l_dtype, ld_logits, (int)tokens, (int)experts, topk, renormalize != 0,
                     ids, weights, offsets, order};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (offsets != nullptr && tokens <= kSmallTokens) {
+  // One workgroup up to a token a wave, or few experts (us, one against two launches: 32
+  // x 64 6.7 / 7.6, 64 x 8 7.1 / 7.1; 64 x 64 9.8 / 7.8, 32 x 256 11.2 / 8.8).
+  if (offsets != nullptr && (tokens <= kSortWaves || (tokens <= kSmallTokens && tokens * experts <= 2048))) {
     moe_route_kernel<<<1, kSortThreads, 0, st>>>(p);
     GPTQ_TRY_LAUNCH();
     return GPTQ_OK;
   }
-  moe_choose_kernel<<<(unsigned)ceil_div(tokens, 4), 256, 0, st>>>(p);
-  GPTQ_TRY_LAUNCH();
+  const gptq_status rc = moe_choose(logits, l_dtype, ld_logits, (int)tokens, (int)experts, topk, renormalize != 0, ids,
+                                    weights, st);
+  if (rc != GPTQ_OK) return rc;
   if (offsets != nullptr) {
     moe_sort_kernel<<<(unsigned)experts, kSortThreads, 0, st>>>(p);
     GPTQ_TRY_LAUNCH();

@@ -60,24 +60,25 @@ def test_gpu_tests_reach_every_kernel(recorder):
     calls += [_layer(fmt, *s, dtype) for s in sizes.LAYERS for fmt in ("mx", "block") for dtype in (F16, BF16)]
     reached = set()
     for rc, launches in _record(recorder, calls):
-        assert rc == 0 and 1 <= len(launches) <= 2
+        assert rc == 0 and 1 <= len(launches) <= 3
         reached |= {k for k, _ in launches}
     assert reached == held
 
 
-def test_a_layer_is_two_launches_within_their_limits(recorder):
+def test_a_layer_is_two_launches_three_for_many_tokens_within_their_limits(recorder):
     sizes = [(64, 1024, 16, 1 << 20, 1 << 19), (64, 1024, 16, 64, 64), (1, 1, 1, 1 << 20, 1), (64, 1, 1, 1, 1 << 19),
              (1, 8, 2, 4096, 11008), (16, 64, 6, 2048, 1024)]
     calls = [_layer(fmt, *s, dtype) for s in sizes for fmt in ("mx", "block") for dtype in (F16, BF16)]
     for call, (rc, launches) in zip(calls, _record(recorder, calls)):
-        assert rc == 0 and len(launches) == 2, call
+        assert rc == 0 and len(launches) == (3 if call[1][-13] > 16 else 2), call
         for _, k in launches:
             assert k[0] >= 1 and k[0] * k[3] < 1 << 32 and k[1:3] == [1, 1] and k[6] <= LDS - 64, (call, k)
 
 
-def test_up_to_64_tokens_route_in_one_launch(recorder):
-    for tokens, want in ((1, 1), (64, 1), (65, 2), (1 << 20, 2)):
-        rc, launches = _record(recorder, [_route(tokens, 100, 4)])[0]
-        assert rc == 0 and len(launches) == want
+def test_few_tokens_route_in_one_launch(recorder):
+    for tokens, experts, want in ((1, 100, 1), (16, 1024, 1), (17, 120, 1), (64, 32, 1), (64, 33, 2), (17, 121, 2), (65, 4, 2),
+                                  (1 << 20, 100, 2)):
+        rc, launches = _record(recorder, [_route(tokens, experts, 4)])[0]
+        assert rc == 0 and len(launches) == want, (tokens, experts)
         for _, k in launches:
             assert k[0] * k[3] < 1 << 32
