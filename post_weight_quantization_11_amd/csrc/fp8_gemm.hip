@@ -63,18 +63,18 @@ __device__ inline floatx4 mfma16(bf16x8 w, bf16x8 x, floatx4 c) {
 // ---------------------------------------------------------------------------
 // Few rows of X: the waves of a workgroup share RT tiles of 16 rows of W and one
 // of X, take every eighth quad of blocks (512 columns) and add their sums through
-// LDS in wave order.  Both operands come straight from memory, D blocks in
-// flight a wave; a quad's four scales are one load.  The compiler moves loads
-// towards their products and so keeps to few registers and eight waves a SIMD,
-// which many workgroups want (16 x 11008 x 4096 20 us, 27 with PIN); PIN keeps
-// them in their places: few workgroups with long rows depend on what each has in
-// flight (1 x 4096 x 11008 19.5 -> 15.8 us).
+// LDS in wave order.  Both operands come straight from memory, D blocks in flight a
+// wave, along their rows, and are exchanged between lanes (loaded in the matrix
+// instruction's order they cost the CU's cache four times the accesses: 1 x 49152 x
+// 12288 139 us for 108, with rows at odd addresses 1 x 12288 x 12288 93 for 45); a
+// quad's four scales are one load.  Measured: 1 x 4096 x 4096 6.7 us,
+// 1 x 12288 x 12288 37 us, 1 x 49152 x 12288 108 us (5.6 TB/s), 16 x 49152 x 12288 131.
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
-template <int RT, int D, bool PIN>
+template <int RT, int D>
 __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p) {
   static_assert(D == 1 || D == 2 || D == 4, "the ring's slots are the same in every quad");
-  extern __shared__ floatx4 red[];           // [wave][RT][64]
+  extern __shared__ floatx4 red[];           // [wave][RT][64], and the waves' exchanges
   const int row_tiles = (p.m + 16 * RT - 1) / (16 * RT);
   const int slot = (int)(blockIdx.x / row_tiles), r0 = (int)(blockIdx.x % row_tiles) * 16 * RT;
   const TokenTile tile = find_tile(p, slot, 16);
@@ -84,17 +84,17 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
   const uint8_t* wrow[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
-    wrow[rt] = p.W + (int64_t)tile.expert * p.w_stride + (int64_t)min(r0 + 16 * rt + c16, p.m - 1) * p.ldw;
+    wrow[rt] = p.W + (int64_t)tile.expert * p.w_stride + (int64_t)min(r0 + 16 * rt + (lane >> 2), p.m - 1) * p.ldw;
   // 16 RT divides 128: the tiles lie in one block of rows.
   const float* wsrow = p.S + (int64_t)tile.expert * p.s_stride + (int64_t)(r0 >> 7) * p.lds;
-  const int64_t t = min(tile.begin + c16, tile.end - 1);
-  const uint8_t* xrow = p.X + t * p.ldx;
-  const float* xsrow = p.XS + t * p.ldxs;
+  const uint8_t* xrow = p.X + (int64_t)min(tile.begin + (lane >> 2), tile.end - 1) * p.ldx;
+  const float* xsrow = p.XS + (int64_t)min(tile.begin + c16, tile.end - 1) * p.ldxs;
+  u32x4* swap = reinterpret_cast<u32x4*>(red + kRowWaves * RT * 64) + wave * (kExchange / 16);
   floatx4 acc[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) acc[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  // Lane quarter q holds bytes 16 q .. + 15 of both halves of a block.
+  // Lane quarter q is to hold bytes 16 q .. + 15 of both halves of a block.
   struct Unit {
     u32x4 w[RT][2], x[2];
   };
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
   const int quads = p.n >> 9;                // whole ones
   // Past the last quad that quad is loaded again (and not used).
   auto load_unit = [&](int quad, int d, Unit& u) {
-    const int at = 128 * (4 * min(quad, quads - 1) + d) + 16 * q;
+    const int at = 128 * (4 * min(quad, quads - 1) + d) + 16 * (lane & 3);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -117,9 +117,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
     s.w = *reinterpret_cast<const floatx4_a4*>(wsrow + at);
     s.x = *reinterpret_cast<const floatx4_a4*>(xsrow + at);
   };
-  auto multiply = [&](const Unit& u, float f) {
+  auto multiply = [&](Unit& u, float f) {
+    exchange(u.x, swap, lane);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
+      exchange(u.w[rt], swap, lane);
       floatx4 v = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < 4; ++s) v = mfma16(fp8_widen8(u.w[rt][s >> 1], s & 1), fp8_widen8(u.x[s >> 1], s & 1), v);
@@ -133,14 +135,12 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
     load_scales(wave, cur);
 #pragma unroll
     for (int d = 0; d < D; ++d) load_unit(wave, d, u[d]);
-    if constexpr (PIN) __builtin_amdgcn_sched_barrier(0);     // all loads are issued before the first product
     for (int quad = wave; quad < quads; quad += kRowWaves) {
       load_scales(quad + kRowWaves, nxt);
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         multiply(u[d % D], cur.w[d] * cur.x[d]);
         load_unit(d + D < 4 ? quad : quad + kRowWaves, (d + D) % 4, u[d % D]);
-        if constexpr (PIN) __builtin_amdgcn_sched_barrier(0);
       }
       cur = nxt;
     }
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
     Unit u;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = 128 * b + 64 * h + 16 * q;
+      const int k = 128 * b + 64 * h + 16 * (lane & 3);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) u.w[rt][h] = fp8_load16_tail(wrow[rt], k, p.n);
       u.x[h] = fp8_load16_tail(xrow, k, p.n);
@@ -514,7 +514,7 @@ __global__ __launch_bounds__(kJoinCols / 4) void fp8_join_kernel(Fp8Operands p, 
 
 // What a product runs on, from its sizes alone.
 enum Kind {
-  kRows1, kRows1Pinned, kRows2,              // fp8_rows_kernel: one tile or two of W's rows
+  kRows1, kRows2,                            // fp8_rows_kernel: one tile or two of W's rows
   kTile128x32, kTile128x64, kTile128x128, kTile256x256,     // W rows x X rows of a tile
 };
 struct Plan {
@@ -542,27 +542,25 @@ constexpr TileShape kWideTileShapes[] = {
     {kTile128x128, 128, 128, 2, 4.8, 2.2, 4.0},
 };
 
-// The row kernels take up to 16 rows of X and whatever is small (32 x 4096 x 4096:
-// 9.8 us, 12 on tiles; 54 x 430 x 6080: 8.2 and 11; 64 x 4096 x 4096: 15 and 13).
-// Two tiles of W a workgroup read X half as often, one gives more workgroups (16 x
-// 4096 x 4096 9.5 and 9.8; 24 x 4096 x 4096 12.2 and 9.6; 2 x 3463 x 8368 13 and 15;
-// 1 x 49152 x 12288 161 and 110).  `odd`: rows that do not start at whole 32-bit words,
-// which their 16-byte loads take twice as long for (77 x 4096 x 11008 on them 52 and
-// 130 us, on tiles 27 and 33): they take up to 2^25 weights (16 x 4099 x 4097 15.7 us,
-// 17.4 on tiles; 1 x 4099 x 11007 33 and 27; 64 experts' 256 x 1025 x 2047 80 and 48).
-constexpr int64_t kOddWeights = (int64_t)1 << 25;
-Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool wide, bool odd) {
+// The row kernels take up to 16 rows of X and whatever is small (us, against tiles: 16
+// x 12288 x 12288 43 / 45, 24 x 12288 x 12288 51 / 42; 96 x 4096 x 4096 14 / 15; 48 x
+// 11008 x 4096 23 / 27, 64 x 11008 x 4096 27 / 24; 128 x 1030 x 2044 8.0 / 11.4; rows at
+// odd addresses 96 x 4096 x 4096 20 / 21, 24 x 4099 x 11007 31 / 29), unless short rows
+// leave their many workgroups little each (256 x 1030 x 2044 10 / 17, 256 x 2048 x 2048
+// 9.5 / 8.4, 512 x 1024 x 1024 8.0 / 6.0, 256 x 8192 x 512 23 / 6.3).  Two tiles of W a
+// workgroup read X half as often, one gives more workgroups (16 x 4096 x 4096 7.9 and
+// 7.2; 24 x 4096 x 4096 7.4 and 9.6; 16 x 49152 x 12288 131 and 159).
+Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool wide) {
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
   if (grouped) {
-    // By the rows that an expert has on average (8 experts of 11008 x 4096 with 8
-    // rows each: 92 us, 97 on tiles, with 64 373 and 155; 4 of 500 x 9000 with 10: 13
-    // and 47; 100 of 512 x 512 with 20: 29 and 14).
+    // By the rows that an expert has on average, and rows long enough for the eight
+    // waves (us, against tiles: 8 experts of 11008 x 4096 with 12 rows each 71 / 94, with
+    // 24 103 / 95; 64 of 1030 x 2044 with 12 44 / 45; 64 of 2048 x 1024 with 4 40 / 32;
+    // 100 of 512 x 512 with 1 17 / 10; one of 512 x 512 3.4 / 4.2).
     const int64_t touched = std::min(experts, rows);
-    if (odd ? rows < 16 * experts && touched * m * n <= kOddWeights
-            : rows < 8 * experts || (rows < 16 * experts && products <= 300000000))
+    if (rows <= 12 * experts && (n > 1024 || touched * m * n <= ((int64_t)1 << 22)))
       return Plan{touched * ceil_div(m, 32) < 256 ? kRows1 : kRows2, 1};
-  } else if (odd ? m * n <= kOddWeights && products <= 300000000 : rows <= 16 || products <= 600000000) {
-    if (!odd && rows <= 4 && m >= 2048 && m <= 6144 && n >= 6144) return Plan{kRows1Pinned, 1};
+  } else if (rows <= 16 || (products <= 1500000000 && outputs <= 160 * n)) {
     return Plan{outputs <= 65536 && m < 8192 ? kRows1 : kRows2, 1};
   }
   // Experts with fewer rows than a tile take a whole one each.
@@ -632,20 +630,19 @@ gptq_status launch_tiles(const Fp8Operands& p, const Plan& pl, void* ws, hipStre
   return launch_tile<WIDE, WR, WC, RB, CB, 2, false>(p, pl, ws, st);
 }
 
-template <int RT, int D, bool PIN>
+template <int RT, int D>
 gptq_status launch_rows(const Fp8Operands& p, hipStream_t st) {
   constexpr int threads = 64 * kRowWaves;
   const int64_t slots = max_tiles(p.rows, p.experts, p.offsets != nullptr, 16);
   return in_row_parts(p, 16 * RT, slots, threads, [&](const Fp8Operands& q) {
-    fp8_rows_kernel<RT, D, PIN>
-        <<<(unsigned)(ceil_div(q.m, 16 * RT) * slots), threads, kRowWaves * RT * 64 * sizeof(floatx4), st>>>(q);
+    fp8_rows_kernel<RT, D>
+        <<<(unsigned)(ceil_div(q.m, 16 * RT) * slots), threads, kRowWaves * (RT * 64 * sizeof(floatx4) + kExchange), st>>>(q);
   });
 }
 
 template <bool WIDE>
 gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, hipStream_t st) {
-  const uint64_t starts = row_starts(p);
-  Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, WIDE, (starts & 3) != 0);
+  Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, WIDE);
   // The tile kernels address the rows of a tile with 32 bits; rows further apart
   // take the row kernel.
   constexpr int64_t kMaxPitch = (int64_t)1 << 22;
@@ -660,9 +657,8 @@ gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, hipStream_t 
     case kTile128x128: return launch_tiles<WIDE, 2, 2, 2, 2, 2>(p, pl, ws, st);
     case kTile128x64: return launch_tiles<WIDE, 4, 1, 1, 2, 3>(p, pl, ws, st);
     case kTile128x32: return launch_tiles<WIDE, 4, 1, 1, 1, 4>(p, pl, ws, st);
-    case kRows1: return launch_rows<1, 4, false>(p, st);
-    case kRows1Pinned: return launch_rows<1, 4, true>(p, st);
-    default: return launch_rows<2, 2, false>(p, st);
+    case kRows1: return launch_rows<1, 4>(p, st);
+    default: return launch_rows<2, 2>(p, st);
   }
 }
 
@@ -697,13 +693,11 @@ extern "C" size_t gptq_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, i
   if (m <= 0 || n < 0 || rows <= 0 || experts <= 0 || n > kFp8MaxCols || m > GPTQ_MX_MAX_ROWS ||
       rows > GPTQ_MX_MAX_ROWS || experts > GPTQ_MX_MAX_EXPERTS)
     return 0;
-  // Of one matrix with either kind of Y and rows of any alignment; products grouped
-  // by expert need none.
+  // Of one matrix with either kind of Y; products grouped by expert need none.
   if (experts > 1) return 0;
   size_t need = 0;
   for (int wide = 0; wide < 2; ++wide)
-    for (int odd = 0; odd < 2; ++odd)
-      need = std::max(need, plan_ws(make_plan(m, n, rows, 1, false, wide != 0, odd != 0), m, rows));
+    need = std::max(need, plan_ws(make_plan(m, n, rows, 1, false, wide != 0), m, rows));
   return need;
 }
 

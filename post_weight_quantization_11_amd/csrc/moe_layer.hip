@@ -226,27 +226,6 @@ template <int WF> __device__ inline int step_col(int s, int q) {
   return WF == kMxWeights ? 32 * s + 8 * q : 64 * (s >> 1) + 16 * q + 8 * (s & 1);
 }
 
-// What the lanes loaded, row lane / 4 and quarter lane % 4 of its 64 bytes, into the
-// order of the matrix instruction, row lane % 16 and quarter lane / 16, through the
-// wave's own kExchange bytes of LDS (its accesses are done in their order).  Loaded in
-// the instruction's order, every lane beside another's row, a load takes 64 accesses
-// of the cache for 16 (16 tokens, 64 experts 2048 x 1024 in 8 bits 71 us for 68; 1 token,
-// 8 of 4096 x 11008 in 4 bits 46 for 43).
-constexpr int kExchange = 2 * 64 * 16;
-__device__ inline void wave_fence() {        // for the compiler alone
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-}
-__device__ inline void exchange(u32x4 (&w)[2], u32x4* lds, int lane) {
-  wave_fence();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) lds[64 * h + ((lane & 60) | ((lane & 3) ^ (lane >> 4)))] = w[h];
-  wave_fence();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) w[h] = lds[64 * h + (4 * (lane & 15) | ((lane >> 4) ^ (lane >> 2 & 3)))];
-}
-
 // Codes in the order of the steps.
 __device__ inline void arrange(Row<kMxWeights>& o) {
 #pragma unroll

@@ -217,14 +217,14 @@ def _check(Y, res, n, out, what, keep=None):
 
 
 GEMM = [
-    # m, n, batch: row kernels, then tiles (more than 16 rows, 6e8 products), each with rows that are 16-byte
+    # m, n, batch: row kernels, then tiles (more than 16 rows, 1.5e9 products), each with rows that are 16-byte
     # aligned and with rows that are not
     (1, 1, 1), (16, 128, 1), (17, 33, 2), (40, 7, 3), (70, 1000, 5), (33, 31, 16), (64, 4096, 1), (100, 2049, 17),
     (256, 256, 64), (130, 640, 33), (515, 515, 130), (300, 1031, 259), (1040, 256, 7), (2060, 6200, 3),
     (2060, 6203, 3), (8200, 520, 12), (8200, 515, 12),
     (2100, 8208, 40), (2100, 8201, 40), (4200, 1040, 140), (4200, 1031, 140), (1100, 4112, 300), (1100, 4099, 300),
     (2700, 768, 700), (2700, 775, 700), (1300, 1920, 530), (1300, 1925, 530), (4100, 1056, 1100), (4100, 1030, 1100),
-    (6200, 400, 2100), (6200, 393, 2100),
+    (6200, 400, 2100), (6200, 393, 2100), (2100, 8208, 100), (2100, 8201, 100),
 ]
 
 
@@ -482,18 +482,18 @@ def test_side_stream(g, batch):
 
 
 def test_graphs_replayed_in_turn(g):
-    """Two graphs over the operators, replayed several times in turn with new
+    """Graphs over the operators, replayed several times in turn with new
     inputs and eager calls between, each replay against the eager result."""
     import torch
     rng = _rng(53)
     E, m, n = 4, 300, 8200
     layers = []
-    for batch in (3, 290):
+    for batch in (3, 290, 640):
         (W, S), _ = _stack(rng, E, m, n)
         X, _ = _to(rng.standard_normal((batch, n)), "bf16")
         off = torch.tensor([0, 1, 1, batch // 2, batch], dtype=torch.int32, device="cuda")
         layers.append(dict(W=W, S=S, X=X, off=off, Yg=torch.zeros((batch, m), device="cuda")))
-    assert g.load().gptq_block_gemm_ws_bytes(m, n, 290, 1) > 0              # split columns: a workspace each
+    assert g.load().gptq_block_gemm_ws_bytes(m, n, 640, 1) > 0              # split columns: a workspace each
 
     def step(L):
         q = g.gptq_block_quantize(L["X"])
