@@ -71,35 +71,42 @@ __device__ inline floatx4 mfma16(bf16x8 w, bf16x8 x, floatx4 c) {
 // 1 x 12288 x 12288 37 us, 1 x 49152 x 12288 108 us (5.6 TB/s), 16 x 49152 x 12288 131.
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
-template <int RT, int D>
+template <int RT, int CT, int D>
 __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p) {
   static_assert(D == 1 || D == 2 || D == 4, "the ring's slots are the same in every quad");
-  extern __shared__ floatx4 red[];           // [wave][RT][64], and the waves' exchanges
+  extern __shared__ floatx4 red[];           // [wave][CT][RT][64], and the waves' exchanges
   const int row_tiles = (p.m + 16 * RT - 1) / (16 * RT);
   const int slot = (int)(blockIdx.x / row_tiles), r0 = (int)(blockIdx.x % row_tiles) * 16 * RT;
-  const TokenTile tile = find_tile(p, slot, 16);
+  const TokenTile tile = find_tile(p, slot, 16 * CT);
   if (!tile.valid) return;
   const int lane = (int)threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const uint8_t* wrow[RT];
+  // Rows past the last repeat it: what they give is not stored.
+  const uint8_t *wrow[RT], *xrow[CT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
     wrow[rt] = p.W + (int64_t)tile.expert * p.w_stride + (int64_t)min(r0 + 16 * rt + (lane >> 2), p.m - 1) * p.ldw;
   // 16 RT divides 128: the tiles lie in one block of rows.
   const float* wsrow = p.S + (int64_t)tile.expert * p.s_stride + (int64_t)(r0 >> 7) * p.lds;
-  const uint8_t* xrow = p.X + (int64_t)min(tile.begin + (lane >> 2), tile.end - 1) * p.ldx;
-  const float* xsrow = p.XS + (int64_t)min(tile.begin + c16, tile.end - 1) * p.ldxs;
-  u32x4* swap = reinterpret_cast<u32x4*>(red + kRowWaves * RT * 64) + wave * (kExchange / 16);
-  floatx4 acc[RT];
+  const float* xsrow[CT];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) acc[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int ct = 0; ct < CT; ++ct) {
+    xrow[ct] = p.X + (int64_t)min(tile.begin + 16 * ct + (lane >> 2), tile.end - 1) * p.ldx;
+    xsrow[ct] = p.XS + (int64_t)min(tile.begin + 16 * ct + c16, tile.end - 1) * p.ldxs;
+  }
+  u32x4* swap = reinterpret_cast<u32x4*>(red + kRowWaves * RT * CT * 64) + wave * (kExchange / 16);
+  floatx4 acc[CT][RT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   // Lane quarter q is to hold bytes 16 q .. + 15 of both halves of a block.
   struct Unit {
-    u32x4 w[RT][2], x[2];
+    u32x4 w[RT][2], x[CT][2];
   };
   struct Scales {
-    floatx4 w, x;                            // a quad's
+    floatx4 w, x[CT];                        // a quad's
   };
   const int quads = p.n >> 9;                // whole ones
   // Past the last quad that quad is loaded again (and not used).
@@ -109,24 +116,35 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) u.w[rt][h] = *reinterpret_cast<const u32x4_a1*>(wrow[rt] + at + 64 * h);
-      u.x[h] = *reinterpret_cast<const u32x4_a1*>(xrow + at + 64 * h);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) u.x[ct][h] = *reinterpret_cast<const u32x4_a1*>(xrow[ct] + at + 64 * h);
     }
   };
   auto load_scales = [&](int quad, Scales& s) {
     const int at = 4 * min(quad, quads - 1);
     s.w = *reinterpret_cast<const floatx4_a4*>(wsrow + at);
-    s.x = *reinterpret_cast<const floatx4_a4*>(xsrow + at);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) s.x[ct] = *reinterpret_cast<const floatx4_a4*>(xsrow[ct] + at);
   };
-  auto multiply = [&](Unit& u, float f) {
-    exchange(u.x, swap, lane);
+  auto multiply = [&](Unit& u, const float (&f)[CT]) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) exchange(u.x[ct], swap, lane);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       exchange(u.w[rt], swap, lane);
-      floatx4 v = floatx4{0.f, 0.f, 0.f, 0.f};
+      floatx4 v[CT];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) v = mfma16(fp8_widen8(u.w[rt][s >> 1], s & 1), fp8_widen8(u.x[s >> 1], s & 1), v);
+      for (int ct = 0; ct < CT; ++ct) v[ct] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[rt][i] = __builtin_fmaf(f, v[i], acc[rt][i]);
+      for (int s = 0; s < 4; ++s) {
+        const bf16x8 w = fp8_widen8(u.w[rt][s >> 1], s & 1);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) v[ct] = mfma16(w, fp8_widen8(u.x[ct][s >> 1], s & 1), v[ct]);
+      }
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[ct][rt][i] = __builtin_fmaf(f[ct], v[ct][i], acc[ct][rt][i]);
     }
   };
   if (wave < quads) {
@@ -139,7 +157,10 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
       load_scales(quad + kRowWaves, nxt);
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        multiply(u[d % D], cur.w[d] * cur.x[d]);
+        float f[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) f[ct] = cur.w[d] * cur.x[ct][d];
+        multiply(u[d % D], f);
         load_unit(d + D < 4 ? quad : quad + kRowWaves, (d + D) % 4, u[d % D]);
       }
       cur = nxt;
@@ -149,22 +170,27 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
   const int blocks = (p.n + 127) >> 7;
   for (int b = 4 * quads + (wave + kRowWaves - quads % kRowWaves) % kRowWaves; b < blocks; b += kRowWaves) {
     Unit u;
+    float f[CT];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = 128 * b + 64 * h + 16 * (lane & 3);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) u.w[rt][h] = fp8_load16_tail(wrow[rt], k, p.n);
-      u.x[h] = fp8_load16_tail(xrow, k, p.n);
-    }
-    multiply(u, wsrow[b] * xsrow[b]);
-  }
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) red[(wave * RT + rt) * 64 + lane] = acc[rt];
+      for (int ct = 0; ct < CT; ++ct) u.x[ct][h] = fp8_load16_tail(xrow[ct], k, p.n);
+    }
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) f[ct] = wsrow[b] * xsrow[ct][b];
+    multiply(u, f);
+  }
+  constexpr int kTiles = RT * CT;
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) red[(wave * kTiles + i) * 64 + lane] = acc[i / RT][i % RT];
   __syncthreads();
-  if (wave < RT) {
+  if (wave < kTiles) {
     floatx4 v = red[wave * 64 + lane];
-    for (int w = 1; w < kRowWaves; ++w) v += red[(w * RT + wave) * 64 + lane];
-    const int x = tile.begin + c16, r = r0 + 16 * wave + 4 * q;
+    for (int w = 1; w < kRowWaves; ++w) v += red[(w * kTiles + wave) * 64 + lane];
+    const int x = tile.begin + 16 * (wave / RT) + c16, r = r0 + 16 * (wave % RT) + 4 * q;
     if (x < tile.end) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -514,7 +540,7 @@ __global__ __launch_bounds__(kJoinCols / 4) void fp8_join_kernel(Fp8Operands p, 
 
 // What a product runs on, from its sizes alone.
 enum Kind {
-  kRows1, kRows2,                            // fp8_rows_kernel: one tile or two of W's rows
+  kRows1, kRows2, kRows4x2,                  // fp8_rows_kernel: 16 or 32 rows of W, 64 with 32 of X
   kTile128x32, kTile128x64, kTile128x128, kTile256x256,     // W rows x X rows of a tile
 };
 struct Plan {
@@ -550,7 +576,7 @@ constexpr TileShape kWideTileShapes[] = {
 // 9.5 / 8.4, 512 x 1024 x 1024 8.0 / 6.0, 256 x 8192 x 512 23 / 6.3).  Two tiles of W a
 // workgroup read X half as often, one gives more workgroups (16 x 4096 x 4096 7.9 and
 // 7.2; 24 x 4096 x 4096 7.4 and 9.6; 16 x 49152 x 12288 131 and 159).
-Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool wide) {
+Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool wide, bool direct) {
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
   if (grouped) {
     // By the rows that an expert has on average, and rows long enough for the eight
@@ -560,6 +586,11 @@ Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped
     const int64_t touched = std::min(experts, rows);
     if (rows <= 12 * experts && (n > 1024 || touched * m * n <= ((int64_t)1 << 22)))
       return Plan{touched * ceil_div(m, 32) < 256 ? kRows1 : kRows2, 1};
+    // Thirty-two rows of X a workgroup: the weights once (8 of 11008 x 4096 with 32 92 /
+    // 112, with 48 128 / 112; 64 of 1030 x 2044 with 24 56 / 60, with 32 58 / 69; where
+    // tiles take rows straight to LDS 64 of 1408 x 2048 with 24 59 / 45).
+    if (rows > 12 * experts && rows <= 32 * experts && touched * ceil_div(m, 64) >= 256 && n >= (direct ? 4096 : 2000))
+      return Plan{kRows4x2, 1};
   } else if (rows <= 16 || (products <= 1500000000 && outputs <= 160 * n)) {
     return Plan{outputs <= 65536 && m < 8192 ? kRows1 : kRows2, 1};
   }
@@ -630,19 +661,20 @@ gptq_status launch_tiles(const Fp8Operands& p, const Plan& pl, void* ws, hipStre
   return launch_tile<WIDE, WR, WC, RB, CB, 2, false>(p, pl, ws, st);
 }
 
-template <int RT, int D>
+template <int RT, int CT, int D>
 gptq_status launch_rows(const Fp8Operands& p, hipStream_t st) {
   constexpr int threads = 64 * kRowWaves;
-  const int64_t slots = max_tiles(p.rows, p.experts, p.offsets != nullptr, 16);
+  const int64_t slots = max_tiles(p.rows, p.experts, p.offsets != nullptr, 16 * CT);
   return in_row_parts(p, 16 * RT, slots, threads, [&](const Fp8Operands& q) {
-    fp8_rows_kernel<RT, D>
-        <<<(unsigned)(ceil_div(q.m, 16 * RT) * slots), threads, kRowWaves * (RT * 64 * sizeof(floatx4) + kExchange), st>>>(q);
+    fp8_rows_kernel<RT, CT, D>
+        <<<(unsigned)(ceil_div(q.m, 16 * RT) * slots), threads, kRowWaves * (RT * CT * 64 * sizeof(floatx4) + kExchange), st>>>(q);
   });
 }
 
 template <bool WIDE>
 gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, hipStream_t st) {
-  Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, WIDE);
+  const bool direct = (row_starts(p) & 15) == 0;
+  Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, WIDE, direct);
   // The tile kernels address the rows of a tile with 32 bits; rows further apart
   // take the row kernel.
   constexpr int64_t kMaxPitch = (int64_t)1 << 22;
@@ -657,8 +689,9 @@ gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, hipStream_t 
     case kTile128x128: return launch_tiles<WIDE, 2, 2, 2, 2, 2>(p, pl, ws, st);
     case kTile128x64: return launch_tiles<WIDE, 4, 1, 1, 2, 3>(p, pl, ws, st);
     case kTile128x32: return launch_tiles<WIDE, 4, 1, 1, 1, 4>(p, pl, ws, st);
-    case kRows1: return launch_rows<1, 4>(p, st);
-    default: return launch_rows<2, 2>(p, st);
+    case kRows1: return launch_rows<1, 1, 4>(p, st);
+    case kRows4x2: return launch_rows<4, 2, 1>(p, st);
+    default: return launch_rows<2, 1, 2>(p, st);
   }
 }
 
@@ -697,7 +730,7 @@ extern "C" size_t gptq_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, i
   if (experts > 1) return 0;
   size_t need = 0;
   for (int wide = 0; wide < 2; ++wide)
-    need = std::max(need, plan_ws(make_plan(m, n, rows, 1, false, wide != 0), m, rows));
+    need = std::max(need, plan_ws(make_plan(m, n, rows, 1, false, wide != 0, false), m, rows));
   return need;
 }
 

@@ -69,6 +69,17 @@ def test_the_plan_takes_the_kernel_that_measured_faster(recorder, rows, m, n, ou
     assert rc == 0 and _kind(launches[0][0]) == want
 
 
+@pytest.mark.parametrize("experts,rows,m,n,ld,want", [
+    (64, 256, 2048, 4096, 4096, ("rows", 2)), (4, 4, 512, 512, 512, ("rows", 1)), (64, 256, 2048, 1024, 1024, "tiles"),
+    (8, 256, 11008, 4096, 4096, ("rows", 4)), (64, 1536, 1408, 2048, 2048, "tiles"),
+    (64, 1536, 1408, 2048, 2052, ("rows", 4)), (8, 512, 11008, 4096, 4096, "tiles"),
+])
+def test_the_plan_of_grouped_products(recorder, experts, rows, m, n, ld, want):
+    rc, launches = _record(recorder, [_grouped(experts, m, n, rows, BF16, ld)])[0]
+    kind = _kind(launches[0][0])
+    assert rc == 0 and len(launches) == 1 and (kind == want or (want == "tiles" and kind[0] != "rows"))
+
+
 def test_a_launch_has_fewer_than_2_to_the_32_threads(recorder):
     calls = [_grouped(2048, 131072, 8, 8191, F32), _grouped(65536, 4096, 32, 196608, BF16),
              _grouped(65536, 1 << 20, 1, 1 << 20, F16), _gemm(4096, 32, 1 << 20, F32, ldx=1 << 23),
@@ -84,7 +95,7 @@ def test_gpu_tests_reach_every_kernel(recorder):
 
     held = {_kernel(w[1]) for w in launch_recorder._run(recorder, []) if w[0] == "kernel"}
     held = {k for k in held if k[0].startswith("fp8_") and "quantize" not in k[0]}
-    assert len(held) == 17
+    assert len(held) == 18
     calls = [_gemm(*s, out) for s in sizes.GEMM for out in (F32, F16, BF16)]
     calls += [_grouped(e, m, n, rows, out, ld) for e, m, n, _, rows in sizes.GROUPED for out in (F32, BF16)
               for ld in (n, _up(n, 16) * 16)]

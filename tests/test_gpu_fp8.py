@@ -383,6 +383,8 @@ GROUPED = [
     (6, 640, 256, [0, 60, 130, 190, 250, 320, 400], 400),
     (6, 640, 250, [0, 60, 130, 190, 250, 320, 400], 400),
     (20, 132, 300, [33 * i for i in range(21)], 660),
+    (20, 833, 2003, [0, 0, 40, 56, 89, 90, 110, 141, 173, 190, 205, 269, 274, 304, 316, 336, 356, 364, 392, 396, 402],
+     410),
 ]
 
 
