@@ -610,7 +610,8 @@ gptq_status gptq_moe_route(const void* logits, int l_dtype, int64_t tokens, int6
                            int32_t* order, void* stream);
 
 /* A layer of experts for up to GPTQ_MOE_MAX_TOKENS tokens (more take
- * gptq_moe_route and the products grouped by expert), in two launches:
+ * gptq_moe_route and the products grouped by expert), in two launches (three with
+ * more than 16 tokens):
  *   Y[t] = sum_j weights[t, j] D_e (silu(G_e X[t]) * (U_e X[t])),  e = ids[t, j],
  * with ids and weights as gptq_moe_route gives them for the logits, and
  * silu(a) = a / (1 + exp(-a)).
@@ -628,10 +629,10 @@ gptq_status gptq_moe_route(const void* logits, int l_dtype, int64_t tokens, int6
  *   ws        device workspace of gptq_moe_ws_bytes bytes, 16-byte aligned, in use until
  *             the call's work on `stream` is done: calls that may run at the same time
  *             (two streams, two captured graphs) need one each.
- * Products are exact and sums float32; between the two launches values keep their
+ * Products are exact and sums float32; between the two products values keep their
  * 24 bits.  The same call gives the same bits.  A pair whose weight is 0 adds
- * nothing, whatever its product.  d <= 2^20, f <= 2^19, f >= 1; experts and topk as
- * for gptq_moe_route. */
+ * nothing, whatever its product.  d <= 2^20, f <= 2^19, f >= 1; leading dimensions of
+ * weights, scales and X <= 2^23; experts and topk as for gptq_moe_route. */
 size_t gptq_moe_ws_bytes(int64_t tokens, int64_t experts, int topk, int64_t d, int64_t f);
 gptq_status gptq_mx_moe(const uint32_t* gate_up, int64_t ld_gate_up, int64_t stride_gate_up,
                         const uint8_t* gate_up_scales, int64_t ld_gate_up_scales, int64_t stride_gate_up_scales,
