@@ -71,10 +71,13 @@ __device__ inline floatx4 mfma16(bf16x8 w, bf16x8 x, floatx4 c) {
 // 1 x 12288 x 12288 37 us, 1 x 49152 x 12288 108 us (5.6 TB/s), 16 x 49152 x 12288 131.
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
+template <int RT, int CT> constexpr int rows_lds() {
+  return kRowWaves * std::max(RT * CT * 64 * (int)sizeof(floatx4), kExchange);
+}
 template <int RT, int CT, int D>
 __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p) {
   static_assert(D == 1 || D == 2 || D == 4, "the ring's slots are the same in every quad");
-  extern __shared__ floatx4 red[];           // [wave][CT][RT][64], and the waves' exchanges
+  extern __shared__ floatx4 red[];           // a wave's exchanges, then its sums [CT][RT][64]
   const int row_tiles = (p.m + 16 * RT - 1) / (16 * RT);
   const int slot = (int)(blockIdx.x / row_tiles), r0 = (int)(blockIdx.x % row_tiles) * 16 * RT;
   const TokenTile tile = find_tile(p, slot, 16 * CT);
@@ -94,7 +97,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
     xrow[ct] = p.X + (int64_t)min(tile.begin + 16 * ct + (lane >> 2), tile.end - 1) * p.ldx;
     xsrow[ct] = p.XS + (int64_t)min(tile.begin + 16 * ct + c16, tile.end - 1) * p.ldxs;
   }
-  u32x4* swap = reinterpret_cast<u32x4*>(red + kRowWaves * RT * CT * 64) + wave * (kExchange / 16);
+  constexpr int kTiles = RT * CT, kMine = rows_lds<RT, CT>() / kRowWaves / 16;
+  u32x4* swap = reinterpret_cast<u32x4*>(red + wave * kMine);
   floatx4 acc[CT][RT];
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct)
@@ -183,13 +187,13 @@ __global__ __launch_bounds__(64 * kRowWaves) void fp8_rows_kernel(Fp8Operands p)
     for (int ct = 0; ct < CT; ++ct) f[ct] = wsrow[b] * xsrow[ct][b];
     multiply(u, f);
   }
-  constexpr int kTiles = RT * CT;
+  wave_fence();
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) red[(wave * kTiles + i) * 64 + lane] = acc[i / RT][i % RT];
+  for (int i = 0; i < kTiles; ++i) red[wave * kMine + i * 64 + lane] = acc[i / RT][i % RT];
   __syncthreads();
   if (wave < kTiles) {
     floatx4 v = red[wave * 64 + lane];
-    for (int w = 1; w < kRowWaves; ++w) v += red[(w * kTiles + wave) * 64 + lane];
+    for (int w = 1; w < kRowWaves; ++w) v += red[w * kMine + wave * 64 + lane];
     const int x = tile.begin + 16 * (wave / RT) + c16, r = r0 + 16 * (wave % RT) + 4 * q;
     if (x < tile.end) {
 #pragma unroll
@@ -667,7 +671,7 @@ gptq_status launch_rows(const Fp8Operands& p, hipStream_t st) {
   const int64_t slots = max_tiles(p.rows, p.experts, p.offsets != nullptr, 16 * CT);
   return in_row_parts(p, 16 * RT, slots, threads, [&](const Fp8Operands& q) {
     fp8_rows_kernel<RT, CT, D>
-        <<<(unsigned)(ceil_div(q.m, 16 * RT) * slots), threads, kRowWaves * (RT * CT * 64 * sizeof(floatx4) + kExchange), st>>>(q);
+        <<<(unsigned)(ceil_div(q.m, 16 * RT) * slots), threads, rows_lds<RT, CT>(), st>>>(q);
   });
 }
 
