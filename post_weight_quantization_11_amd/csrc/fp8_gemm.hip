@@ -572,36 +572,54 @@ constexpr TileShape kWideTileShapes[] = {
     {kTile128x128, 128, 128, 2, 4.8, 2.2, 4.0},
 };
 
+// Rows through registers (kTile256x256 took 155 us for 2048 x 4099 x 4097, 128 x 128 108).
+// Fitted to 16 sizes from 24 x 8200 x 8201 to 2048 x 4099 x 4097: 1.01 times the fastest in
+// the mean, 1.1 at worst.
+constexpr TileShape kRaggedTileShapes[] = {
+    {kTile128x32, 128, 32, 2, 1.3, 2.1, 2.4},
+    {kTile128x64, 128, 64, 2, 1.2, 2.4, 3.1},
+    {kTile128x128, 128, 128, 2, 0.3, 3.3, 5.0},
+};
+constexpr TileShape kWideRaggedTileShapes[] = {
+    {kTile128x32, 128, 32, 2, 3.3, 2.2, 2.5},
+    {kTile128x64, 128, 64, 2, 3.3, 2.9, 3.4},
+    {kTile128x128, 128, 128, 2, 3.1, 3.5, 5.2},
+};
+
 // The row kernels take up to 16 rows of X and whatever is small (us, against tiles: 16
 // x 12288 x 12288 43 / 45, 24 x 12288 x 12288 51 / 42; 96 x 4096 x 4096 14 / 15; 48 x
-// 11008 x 4096 23 / 27, 64 x 11008 x 4096 27 / 24; 128 x 1030 x 2044 8.0 / 11.4; rows at
-// odd addresses 96 x 4096 x 4096 20 / 21, 24 x 4099 x 11007 31 / 29), unless short rows
-// leave their many workgroups little each (256 x 1030 x 2044 10 / 17, 256 x 2048 x 2048
-// 9.5 / 8.4, 512 x 1024 x 1024 8.0 / 6.0, 256 x 8192 x 512 23 / 6.3).  Two tiles of W a
-// workgroup read X half as often, one gives more workgroups (16 x 4096 x 4096 7.9 and
-// 7.2; 24 x 4096 x 4096 7.4 and 9.6; 16 x 49152 x 12288 131 and 159).
+// 11008 x 4096 23 / 27, 64 x 11008 x 4096 27 / 24; 128 x 2048 x 2048 5.8 / 10), unless
+// short rows leave their many workgroups little each (256 x 2048 x 2048 9.5 / 8.4, 512 x
+// 1024 x 1024 8.0 / 6.0, 256 x 8192 x 512 23 / 6.3).  Of rows that are not 16-byte
+// aligned they take less (16 x 4099 x 4097 13 / 15, 24 x 4099 x 4097 17 / 15; 128 x 1030 x
+// 2044 8.4 / 11, 256 x 1030 x 2043 13 / 13; 16 x 8200 x 8201 33 / 29, but up to 16 rows
+// are promised widened codes).  Two tiles of W a workgroup read X half as often, one
+// gives more workgroups (16 x 4096 x 4096 7.9 and 7.2; 24 x 4096 x 4096 7.4 and 9.6; 16 x
+// 49152 x 12288 131 and 159).
 Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool wide, bool direct) {
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
   if (grouped) {
     // By the rows that an expert has on average, and rows long enough for the eight
     // waves (us, against tiles: 8 experts of 11008 x 4096 with 12 rows each 71 / 94, with
-    // 24 103 / 95; 64 of 1030 x 2044 with 12 44 / 45; 64 of 2048 x 1024 with 4 40 / 32;
+    // 24 103 / 95; 64 of 1030 x 2044 with 8 43 / 44; 64 of 2048 x 1024 with 4 40 / 32;
     // 100 of 512 x 512 with 1 17 / 10; one of 512 x 512 3.4 / 4.2).
     const int64_t touched = std::min(experts, rows);
-    if (rows <= 12 * experts && (n > 1024 || touched * m * n <= ((int64_t)1 << 22)))
+    if (rows <= 12 * experts && (rows <= 16 || n >= 2000 || touched * m * n <= ((int64_t)1 << 22)))
       return Plan{touched * ceil_div(m, 32) < 256 ? kRows1 : kRows2, 1};
     // Thirty-two rows of X a workgroup: the weights once (8 of 11008 x 4096 with 32 92 /
     // 112, with 48 128 / 112; 64 of 1030 x 2044 with 24 56 / 60, with 32 58 / 69; where
     // tiles take rows straight to LDS 64 of 1408 x 2048 with 24 59 / 45).
     if (rows > 12 * experts && rows <= 32 * experts && touched * ceil_div(m, 64) >= 256 && n >= (direct ? 4096 : 2000))
       return Plan{kRows4x2, 1};
-  } else if (rows <= 16 || (products <= 1500000000 && outputs <= 160 * n)) {
+  } else if (rows <= 16 || (direct ? products <= 1500000000 && outputs <= 160 * n : products <= 400000000)) {
     return Plan{outputs <= 65536 && m < 8192 ? kRows1 : kRows2, 1};
   }
   // Experts with fewer rows than a tile take a whole one each.
   const int64_t e = grouped ? experts : 0, least = grouped ? std::min(experts, rows) : 0;
-  const TileChoice c = wide ? choose_tiles(kWideTileShapes, m, n, rows, e, 4.0, 0.2e-6, least)
-                            : choose_tiles(kTileShapes, m, n, rows, e, 4.0, 0.2e-6, least);
+  const TileChoice c = direct ? wide ? choose_tiles(kWideTileShapes, m, n, rows, e, 4.0, 0.2e-6, least)
+                                     : choose_tiles(kTileShapes, m, n, rows, e, 4.0, 0.2e-6, least)
+                       : wide ? choose_tiles(kWideRaggedTileShapes, m, n, rows, e, 6.0, 0.14e-6, least)
+                              : choose_tiles(kRaggedTileShapes, m, n, rows, e, 6.0, 0.14e-6, least);
   return Plan{(Kind)c.kind, c.splits};
 }
 
@@ -688,7 +706,7 @@ gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, hipStream_t 
   if (need > 0 && (reinterpret_cast<uintptr_t>(ws) & 3) != 0) return GPTQ_ERR_INVALID_ARG;
   switch (pl.kind) {
     case kTile256x256:
-      if constexpr (!WIDE) return launch_tiles<WIDE, 4, 2, 2, 4, 2>(p, pl, ws, st);
+      if constexpr (!WIDE) return launch_tile<WIDE, 4, 2, 2, 4, 2, true>(p, pl, ws, st);
       [[fallthrough]];
     case kTile128x128: return launch_tiles<WIDE, 2, 2, 2, 2, 2>(p, pl, ws, st);
     case kTile128x64: return launch_tiles<WIDE, 4, 1, 1, 2, 3>(p, pl, ws, st);
@@ -730,11 +748,13 @@ extern "C" size_t gptq_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, i
   if (m <= 0 || n < 0 || rows <= 0 || experts <= 0 || n > kFp8MaxCols || m > GPTQ_MX_MAX_ROWS ||
       rows > GPTQ_MX_MAX_ROWS || experts > GPTQ_MX_MAX_EXPERTS)
     return 0;
-  // Of one matrix with either kind of Y; products grouped by expert need none.
+  // Of one matrix with either kind of Y and rows of any alignment; products grouped
+  // by expert need none.
   if (experts > 1) return 0;
   size_t need = 0;
   for (int wide = 0; wide < 2; ++wide)
-    need = std::max(need, plan_ws(make_plan(m, n, rows, 1, false, wide != 0, false), m, rows));
+    for (int direct = 0; direct < 2; ++direct)
+      need = std::max(need, plan_ws(make_plan(m, n, rows, 1, false, wide != 0, direct != 0), m, rows));
   return need;
 }
 
