@@ -248,6 +248,45 @@ def test_layer_non_finite_tokens_stay_alone(g, fmt):
     assert np.isnan(Y[3]).all() and not np.isfinite(Y[18]).all()
 
 
+@pytest.mark.parametrize("tokens,E,k,d,f", [
+    (18, 3, 2, 4500, 40), (3, 2, 1, 8200, 33),              # more columns than the waves hold of X
+    (17, 3, 2, 1030, 515), (46, 2, 2, 777, 1029),           # partial units, strided; slots of fifteen tokens and one
+    (2, 2, 2, 1030, 8200), (20, 2, 1, 4600, 4100),          # several tiles of a slot a workgroup
+])
+@pytest.mark.parametrize("fmt", ["mx", "block"])
+def test_layer_long_and_partial_rows(g, fmt, tokens, E, k, d, f):
+    rng = _rng(tokens, d)
+    args, gu64, dn64, call = _layer(g, fmt, rng, E, d, f, pad=3)
+    L, L64 = _to(rng.standard_normal((tokens, E)), "bf16")
+    for dtype in ("bf16", "f16"):
+        X, X64 = _to(rng.standard_normal((tokens, d)), dtype, d + 5)
+        _check(call(*args, X, L, k), gu64, dn64, X64, L64, k, True, _units(fmt, d, f), "f32",
+               f"{fmt} layer {tokens} tokens {E} x {d} x {f} {dtype}")
+
+
+@pytest.mark.parametrize("d", [1, 9, 200, 301, 1030])
+@pytest.mark.parametrize("fmt", ["mx", "block"])
+def test_layer_infinity_in_the_last_columns(g, fmt, d):
+    """Loads that end at the rows' end repeat nothing: an infinite X in one of the last
+    columns times positive weights is an infinite h, not a NaN."""
+    import torch
+    rng = _rng(37, d)
+    tokens, f = 3, 5
+    quantize = g.gptq_mx_quantize if fmt == "mx" else lambda w: g.gptq_block_quantize(w, 128)
+    call, names = (g.gptq_mx_moe, ("packed", "scales")) if fmt == "mx" else (g.gptq_block_moe, ("codes", "scales"))
+    gu, dn = _to(rng.uniform(0.5, 1, size=(2 * f, d)), "f32")[0], _to(rng.uniform(0.5, 1, size=(d, f)), "f32")[0]
+    args = [q[n] for q in (quantize(gu[None]), quantize(dn[None])) for n in names]
+    L = torch.zeros((tokens, 1), device="cuda")
+    for dtype in ("bf16", "f16"):
+        X, _ = _to(rng.uniform(0.1, 1, size=(tokens, d)), dtype)
+        Y0 = call(*args, X, L, 1).clone()
+        for c in {d - 1, max(d - 3, 0), max(d - 9, 0), d // 2}:
+            Z = X.clone()
+            Z[1, c] = float("inf")
+            Y = call(*args, Z, L, 1)
+            assert (Y[1] == float("inf")).all() and torch.equal(Y[0], Y0[0]) and torch.equal(Y[2], Y0[2])
+
+
 @pytest.mark.parametrize("lo,hi", [(90, 100), (104, 104), (103, 103), (128, 140)])
 def test_microscaled_layer_with_scales_beyond_float16(g, lo, hi):
     # Weights that float16 X cannot meet in float16: X is split in two.
@@ -259,6 +298,17 @@ def test_microscaled_layer_with_scales_beyond_float16(g, lo, hi):
     X, X64 = _to(rng.standard_normal((tokens, d)) * 2.0 ** (110 - lo if lo > 104 else 0), "f16")
     Y = g.gptq_mx_moe(gu, gus, dn, dns, X, L, k)
     _check(Y, gu64, dn64, X64, L64, k, True, _units("mx", d, f, True), "f32", f"mx layer, scales {lo} .. {hi}")
+
+
+def test_microscaled_layer_with_scales_beyond_float16_and_many_tiles(g):
+    rng = _rng(41)
+    tokens, E, k, d, f = 5, 2, 2, 1030, 8200
+    (gu, gus), gu64 = _mx_stack(rng, E, 2 * f, d, 90, 100)
+    (dn, dns), dn64 = _mx_stack(rng, E, d, f, 100, 140)
+    L, L64 = _to(rng.standard_normal((tokens, E)), "f32")
+    X, X64 = _to(rng.standard_normal((tokens, d)), "f16")
+    _check(g.gptq_mx_moe(gu, gus, dn, dns, X, L, k), gu64, dn64, X64, L64, k, True, _units("mx", d, f, True), "f32",
+           "mx layer, split X, many tiles")
 
 
 @pytest.mark.parametrize("fmt", ["mx", "block"])
