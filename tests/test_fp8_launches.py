@@ -72,8 +72,8 @@ def test_the_plan_takes_the_kernel_that_measured_faster(recorder, rows, m, n, ou
 
 @pytest.mark.parametrize("experts,rows,m,n,ld,want", [
     (64, 256, 2048, 4096, 4096, ("rows", 2)), (4, 4, 512, 512, 512, ("rows", 1)), (64, 256, 2048, 1024, 1024, "tiles"),
-    (8, 256, 11008, 4096, 4096, ("rows", 4)), (64, 1536, 1408, 2048, 2048, "tiles"),
-    (64, 16, 2048, 1024, 1024, ("rows", 2)), (64, 1536, 1408, 2048, 2052, ("rows", 4)),
+    (8, 256, 11008, 4096, 4096, ("rows", 4)), (64, 1600, 1300, 2048, 2048, "tiles"),
+    (64, 16, 2048, 1024, 1024, ("rows", 2)), (64, 1600, 1300, 2048, 2052, ("rows", 4)),
     (8, 512, 11008, 4096, 4096, "tiles"),
 ])
 def test_the_plan_of_grouped_products(recorder, experts, rows, m, n, ld, want):

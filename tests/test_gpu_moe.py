@@ -53,6 +53,7 @@ ROUTES = [
     # tokens, experts, topk: one workgroup up to 64 tokens, then two launches; one, four and sixteen registers of logits
     (1, 1, 1), (1, 2, 2), (3, 64, 6), (16, 64, 6), (64, 65, 16), (5, 256, 8), (64, 257, 3), (7, 1024, 16), (65, 8, 2),
     (257, 16, 16), (1000, 200, 4), (515, 1000, 8), (4099, 63, 1), (8192, 128, 8),
+    (20011, 40, 7),                                         # several steps of the sort a wave
 ]
 
 
