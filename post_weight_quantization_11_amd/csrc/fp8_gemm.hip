@@ -8,18 +8,16 @@
 // row of X and, inside a tile's 32 or 64 rows of W, to one block of W: their
 // factor xs * ws is one number a lane.
 //
-// The matrix instructions on 8-bit operands (v_mfma_f32_32x32x64_f8f6f4) have
-// twice the rate of those on 16-bit ones, but not float32's precision: probed,
-// they cut each product at 2^-13 of the largest power of two among the eight that
-// they add at a time (5e-5 of the result for codes of all magnitudes, 1.4e-5 for
-// quantized normal data), where the 16-bit ones cut at 2^-24.  A 16-bit Y, which
-// rounds to 2^-8 or 2^-11 anyway, takes the former.  A float32 Y takes the latter
-// on codes widened to bfloat16, which holds them exactly; so do products with few
-// rows of X, bound by W's bytes.
+// The matrix instructions on 8-bit operands, of either generation
+// (v_mfma_f32_32x32x64_f8f6f4 at twice the rate of the 16-bit ones, v_mfma_f32_32x32x16_fp8_fp8
+// at theirs), do not sum in float32: probed, they cut each product at 2^-13 of the
+// largest power of two among the eight that they add at a time (5e-5 of the result for
+// codes of all magnitudes, any part of it where large terms cancel), where the 16-bit
+// ones cut at 2^-24.  So codes are widened to bfloat16, which holds them exactly.
 //
-// Operand layout (checked with an in-bounds probe): lane l holds 32 codes (8
-// 16-bit elements) of row l % 32 (l % 16); the order of the summed columns is free
-// as long as both operands agree.  Accumulator register i of lane l is row 8 (i /
+// Operand layout (checked with an in-bounds probe): lane l holds 8 elements of row l
+// % 32 (l % 16); the order of the summed columns is free as long as both operands
+// agree.  Accumulator register i of lane l is row 8 (i /
 // 4) + 4 (l / 32) + i % 4 (4 (l / 16) + i) of the first operand and row l % 32 (l %
 // 16) of the second.
 #include "fp8.h"
@@ -44,15 +42,6 @@ struct Fp8Operands {
   int y_dtype;
 };
 
-__device__ inline intx8 operand(u32x4 lo, u32x4 hi) {
-  return intx8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
-__device__ inline floatx16 mfma32(intx8 w, intx8 x, floatx16 c) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, 0, 0, 0, 0, 0);
-}
-__device__ inline floatx4 mfma16(intx8 w, intx8 x) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, floatx4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-}
 __device__ inline floatx16 mfma32(bf16x8 w, bf16x8 x, floatx16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x, c, 0, 0, 0);
 }
@@ -230,8 +219,8 @@ constexpr int tile_lds() {
 
 // Stores a workgroup's sums.  Each wave passes its own through LDS (the stages are
 // no longer read), 32 rows of X x 64 (32) rows of W at a time, so that a lane
-// stores eight neighbouring ones.
-template <bool T16, int WR, int WC, int RB, int CB>
+// stores eight neighbouring ones.  Y16: a 16-bit Y, otherwise float32.
+template <bool Y16, int WR, int WC, int RB, int CB>
 __device__ inline void store_tile(const Fp8Operands& p, const TileGrid& tg, const TokenTile& tile, int r0, int split,
                                   const floatx16 (&acc)[RB][CB], unsigned char* smem) {
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
@@ -247,8 +236,7 @@ __device__ inline void store_tile(const Fp8Operands& p, const TileGrid& tg, cons
       for (int b = 0; b < RP; ++b)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<floatx4*>(my + (T16 ? 16 * (g & 1) + (lane & 15) : l32) * kPitch + 32 * b +
-                                      (T16 ? 16 * (g >> 1) + 4 * (lane >> 4) : 8 * g + 4 * h)) =
+          *reinterpret_cast<floatx4*>(my + l32 * kPitch + 32 * b + 8 * g + 4 * h) =
               floatx4{acc[r2 + b][cb][4 * g], acc[r2 + b][cb][4 * g + 1], acc[r2 + b][cb][4 * g + 2],
                       acc[r2 + b][cb][4 * g + 3]};
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
@@ -264,7 +252,7 @@ __device__ inline void store_tile(const Fp8Operands& p, const TileGrid& tg, cons
         if (x < tile.end && r < p.m) {
           if (tg.splits > 1)
             store8<GPTQ_F32>(tg.part, ((int64_t)split * p.rows + x) * p.m + r, p.m - r, lo, hi);
-          else if (p.y_dtype == GPTQ_F32)
+          else if (!Y16)
             store8<GPTQ_F32>(p.Y, (int64_t)x * p.ldy + r, p.m - r, lo, hi);
           else if (p.y_dtype == GPTQ_F16)
             store8<GPTQ_F16>(p.Y, (int64_t)x * p.ldy + r, p.m - r, lo, hi);
@@ -277,12 +265,11 @@ __device__ inline void store_tile(const Fp8Operands& p, const TileGrid& tg, cons
     }
 }
 
-// WIDE: on codes widened to bfloat16 (float32 Y), otherwise as stored.
 // DIRECT: rows of both operands are 16-byte aligned and go from memory to LDS
 // without passing through registers, NB - 1 stages ahead.  Otherwise one stage
 // ahead, through registers, any alignment.
-template <bool WIDE, int WR, int WC, int RB, int CB, int NB, bool DIRECT>
-__global__ __launch_bounds__(64 * WR * WC, RB * CB <= 8 ? 2 : 1) void fp8_tile_kernel(Fp8Operands p, TileGrid tg) {
+template <bool Y16, int WR, int WC, int RB, int CB, int NB, bool DIRECT>
+__global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Operands p, TileGrid tg) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   constexpr int kThreads = 64 * WR * WC, kWaves = WR * WC;
   constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB, kRows = BM + BN;        // X rows first, then W rows
@@ -293,7 +280,6 @@ __global__ __launch_bounds__(64 * WR * WC, RB * CB <= 8 ? 2 : 1) void fp8_tile_k
   static_assert(kRows % (8 * kWaves) == 0 && kWaves % 2 == 0, "a wave stages eight rows at a time, all even or all odd");
   static_assert(32 * RB <= kFp8Block && BM % kFp8Block == 0, "a wave's rows of W lie in one block");
   static_assert(DIRECT || NB == 2, "through registers one stage is ahead");
-  constexpr bool T16 = !WIDE && RB * CB > 4;
   int split, r0;
   TokenTile tile;
   if (!tile_of_workgroup(p, tg, BM, BN, split, tile, r0)) return;
@@ -390,109 +376,42 @@ __global__ __launch_bounds__(64 * WR * WC, RB * CB <= 8 ? 2 : 1) void fp8_tile_k
   uint32_t frag_at[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) frag_at[j] = (uint32_t)(l32 * kRow + (((4 * (j >> 1) + 2 * h + (j & 1)) ^ swizzle(l32)) << 4));
-  auto load_frag = [&](const unsigned char* rows, intx8 (&o)[2]) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-      o[s] = operand(*reinterpret_cast<const u32x4*>(rows + frag_at[2 * s]),
-                     *reinterpret_cast<const u32x4*>(rows + frag_at[2 * s + 1]));
-  };
   auto fold = [&](floatx16& to, const floatx16& sum, float f) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) to[i] = __builtin_fmaf(f, sum[i], to[i]);
   };
-  // One stage.
+  // One stage: W's part widened once, then 32 rows of X at a time.  (All sums at once
+  // would need as many registers again as acc.)
   auto compute = [&](int buf) {
     const unsigned char* xs = smem + buf * kBuf + wc * CB * 32 * kRow;
     const unsigned char* ws = smem + buf * kBuf + (BN + wr * RB * 32) * kRow;
     const float* sc = scale_lds + buf * kSlots;
     const float wscale = sc[kSlots - 64 + ((wr * RB * 32) >> 7)];
-    constexpr int XR = 3;
-    float f[CB];
-    if constexpr (WIDE) {
-      floatx16 sum[RB][CB];
+    bf16x8 w[RB][8];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        u32x4 w[RB], x[CB];
+        const u32x4 v = *reinterpret_cast<const u32x4*>(ws + rb * 32 * kRow + frag_at[j]);
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) w[rb] = *reinterpret_cast<const u32x4*>(ws + rb * 32 * kRow + frag_at[j]);
+        for (int s = 0; s < 2; ++s) w[rb][2 * j + s] = fp8_widen8(v, s);
+      }
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) x[cb] = *reinterpret_cast<const u32x4*>(xs + cb * 32 * kRow + frag_at[j]);
+    for (int cb = 0; cb < CB; ++cb) {
+      floatx16 sum[RB];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(xs + cb * 32 * kRow + frag_at[j]);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          bf16x8 wv[RB];
+          const bf16x8 x = fp8_widen8(v, s);
 #pragma unroll
-          for (int rb = 0; rb < RB; ++rb) wv[rb] = fp8_widen8(w[rb], s);
-#pragma unroll
-          for (int cb = 0; cb < CB; ++cb) {
-            const bf16x8 xv = fp8_widen8(x[cb], s);
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) sum[rb][cb] = mfma32(wv[rb], xv, j + s == 0 ? floatx16{} : sum[rb][cb]);
-          }
+          for (int rb = 0; rb < RB; ++rb) sum[rb] = mfma32(w[rb][2 * j + s], x, j + s == 0 ? floatx16{} : sum[rb]);
         }
       }
+      const float f = sc[(wc * CB + cb) * 32 + l32] * wscale;
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) f[cb] = sc[(wc * CB + cb) * 32 + l32] * wscale;
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) fold(acc[rb][cb], sum[rb][cb], f[cb]);
-    } else if constexpr (T16) {
-      const int l16 = lane & 15, q = lane >> 4;
-      uint32_t at[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) at[j] = (uint32_t)(l16 * kRow + (((2 * q + j) ^ swizzle(l16)) << 4));
-      auto load16 = [&](const unsigned char* rows) {
-        return operand(*reinterpret_cast<const u32x4*>(rows + at[0]), *reinterpret_cast<const u32x4*>(rows + at[1]));
-      };
-      intx8 w[2 * RB], x[XR];
-#pragma unroll
-      for (int r = 0; r < 2 * RB; ++r) w[r] = load16(ws + r * 16 * kRow);
-#pragma unroll
-      for (int c = 0; c < XR - 1; ++c) x[c] = load16(xs + c * 16 * kRow);
-      float g[2 * CB];
-#pragma unroll
-      for (int c = 0; c < 2 * CB; ++c) g[c] = sc[(wc * 2 * CB + c) * 16 + l16] * wscale;
-      floatx4 sum[2][2 * RB];
-      auto fold4 = [&](int c, int r) {
-        floatx16& to = acc[r >> 1][c >> 1];
-        const int s = 4 * (2 * (r & 1) + (c & 1));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[s + i] = __builtin_fmaf(g[c], sum[c & 1][r][i], to[s + i]);
-      };
-#pragma unroll
-      for (int c = 0; c < 2 * CB; ++c) {
-        if (c + XR - 1 < 2 * CB) x[(c + XR - 1) % XR] = load16(xs + (c + XR - 1) * 16 * kRow);
-#pragma unroll
-        for (int r = 0; r < 2 * RB; ++r) {
-          sum[c & 1][r] = mfma16(w[r], x[c % XR]);
-          if (c > 0) fold4(c - 1, r);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 2 * RB; ++r) fold4(2 * CB - 1, r);
-    } else {
-      // A tile's sums of the block are added while the next tile's are multiplied.
-      constexpr int XB = RB * CB > 4 ? 1 : 2;
-      intx8 w[RB][2], x[XB][2];
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb) load_frag(ws + rb * 32 * kRow, w[rb]);
-      load_frag(xs, x[0]);
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) f[cb] = sc[(wc * CB + cb) * 32 + l32] * wscale;
-      floatx16 sum[2];
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        if (XB == 1 ? cb > 0 : cb + 1 < CB)
-          load_frag(xs + (XB == 1 ? cb : cb + 1) * 32 * kRow, x[XB == 1 ? 0 : (cb + 1) & 1]);
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          const int at = cb * RB + rb;
-          sum[at & 1] = mfma32(w[rb][0], x[cb % XB][0], floatx16{});
-          sum[at & 1] = mfma32(w[rb][1], x[cb % XB][1], sum[at & 1]);
-          if (at > 0) fold(acc[(at - 1) % RB][(at - 1) / RB], sum[(at - 1) & 1], f[(at - 1) / RB]);
-        }
-      }
-      fold(acc[RB - 1][CB - 1], sum[(RB * CB - 1) & 1], f[CB - 1]);
+      for (int rb = 0; rb < RB; ++rb) fold(acc[rb][cb], sum[rb], f);
     }
   };
 
@@ -537,7 +456,7 @@ __global__ __launch_bounds__(64 * WR * WC, RB * CB <= 8 ? 2 : 1) void fp8_tile_k
     compute(0);
   }
   lds_barrier();
-  store_tile<T16, WR, WC, RB, CB>(p, tg, tile, r0, split, acc, smem);
+  store_tile<Y16, WR, WC, RB, CB>(p, tg, tile, r0, split, acc, smem);
 }
 
 __global__ __launch_bounds__(kJoinCols / 4) void fp8_join_kernel(Fp8Operands p, TileGrid tg) { join_splits(p, tg); }
@@ -552,39 +471,36 @@ struct Plan {
   int splits;                                // of the columns, tiles only
 };
 
-// Fitted to 60 sizes from 4 x 67 x 304 to 4096 x 12288 x 12288: what the model
-// chooses takes 1.03 times the fastest shape's time in the mean, 1.4 at worst (40 x
-// 11008 x 4096: 25 us with three splits, 19 with one).  Some of the measured pairs,
-// the chosen first, codes as stored: 16 x 12288 x 12288 on 128 x 32 with two splits
-// 39.5, with one 51; 77 x 4096 x 11008 on 128 x 64 with four 20, 128 x 128 with
-// four 24; 512 x 4096 x 4096 on 128 x 64 23, 128 x 128 33; 2048 x 4096 x 4096 on
-// 128 x 128 51, 256 x 256 63; 2146 x 21057 x 4480 on 256 x 256 218, 128 x 128 268.
+// Fitted to 95 sizes from 20 x 91 x 1824 to 4096 x 12288 x 12288: what the model chooses
+// takes 1.005 times the fastest shape's time in the mean, 1.1 at worst (24 x 12288 x
+// 12288: 45 us, 41 on 128 x 64).  Some of the measured pairs, the chosen first: 40 x
+// 11008 x 4096 on 128 x 64 with two splits (172 workgroups) 20.8, with three (258, two
+// CUs with two each) 25.9, with one 27.2; 77 x 4096 x 11008 on 128 x 64 with four 25.9,
+// 128 x 128 with four 34; 512 x 4096 x 4096 on 128 x 64 28, 128 x 128 40; 2048 x 4096 x
+// 4096 on 128 x 128 71, 256 x 256 116.
 constexpr TileShape kTileShapes[] = {
-    {kTile128x32, 128, 32, 2, 3.2, 0.97, 3.4},
-    {kTile128x64, 128, 64, 2, 3.4, 1.2, 3.0},
-    {kTile128x128, 128, 128, 2, 3.9, 1.8, 3.3},
-    {kTile256x256, 256, 256, 1, 5.0, 3.8, 3.8},
+    {kTile128x32, 128, 32, 2, 3.58, 1.11, 2.6},
+    {kTile128x64, 128, 64, 2, 4.29, 1.3, 2.78},
+    {kTile128x128, 128, 128, 2, 4.55, 2.41, 3.72},
 };
-// Codes widened.
-constexpr TileShape kWideTileShapes[] = {
-    {kTile128x32, 128, 32, 2, 3.6, 1.1, 3.5},
-    {kTile128x64, 128, 64, 2, 4.0, 1.5, 3.1},
-    {kTile128x128, 128, 128, 2, 4.8, 2.2, 4.0},
+// Of a 16-bit Y (4096 x 4096 x 4096 on 256 x 256 124 us, 128 x 128 132; 4096 x 12288 x
+// 12288 1051 and 1147; 2100 x 6200 x 400 26 and 29).
+constexpr TileShape kTileShapes16[] = {
+    {kTile128x32, 128, 32, 2, 3.58, 1.11, 2.6},
+    {kTile128x64, 128, 64, 2, 4.29, 1.3, 2.78},
+    {kTile128x128, 128, 128, 2, 4.55, 2.41, 3.72},
+    {kTile256x256, 256, 256, 1, 4.72, 7.01, 7.01},
 };
+constexpr double kJoin = 3.4, kJoinBytes = 0.27e-6;
 
-// Rows through registers (kTile256x256 took 155 us for 2048 x 4099 x 4097, 128 x 128 108).
-// Fitted to 16 sizes from 24 x 8200 x 8201 to 2048 x 4099 x 4097: 1.01 times the fastest in
-// the mean, 1.1 at worst.
+// Rows through registers.  Fitted to 27 sizes from 17 x 4099 x 4097 to 2048 x 4099 x
+// 4097: 1.02 times the fastest in the mean, 1.1 at worst.
 constexpr TileShape kRaggedTileShapes[] = {
-    {kTile128x32, 128, 32, 2, 1.3, 2.1, 2.4},
-    {kTile128x64, 128, 64, 2, 1.2, 2.4, 3.1},
-    {kTile128x128, 128, 128, 2, 0.3, 3.3, 5.0},
+    {kTile128x32, 128, 32, 2, 1.88, 2.22, 2.62},
+    {kTile128x64, 128, 64, 2, 2.49, 2.75, 3.22},
+    {kTile128x128, 128, 128, 2, 1.95, 3.63, 4.67},
 };
-constexpr TileShape kWideRaggedTileShapes[] = {
-    {kTile128x32, 128, 32, 2, 3.3, 2.2, 2.5},
-    {kTile128x64, 128, 64, 2, 3.3, 2.9, 3.4},
-    {kTile128x128, 128, 128, 2, 3.1, 3.5, 5.2},
-};
+constexpr double kRaggedJoin = 4.6, kRaggedJoinBytes = 0.16e-6;
 
 // The row kernels take up to 16 rows of X and whatever is small (us, against tiles: 16
 // x 12288 x 12288 43 / 45, 24 x 12288 x 12288 51 / 42; 96 x 4096 x 4096 14 / 15; 48 x
@@ -592,11 +508,10 @@ constexpr TileShape kWideRaggedTileShapes[] = {
 // short rows leave their many workgroups little each (256 x 2048 x 2048 9.5 / 8.4, 512 x
 // 1024 x 1024 8.0 / 6.0, 256 x 8192 x 512 23 / 6.3).  Of rows that are not 16-byte
 // aligned they take less (16 x 4099 x 4097 13 / 15, 24 x 4099 x 4097 17 / 15; 128 x 1030 x
-// 2044 8.4 / 11, 256 x 1030 x 2043 13 / 13; 16 x 8200 x 8201 33 / 29, but up to 16 rows
-// are promised widened codes).  Two tiles of W a workgroup read X half as often, one
+// 2044 8.4 / 11, 256 x 1030 x 2043 13 / 13).  Two tiles of W a workgroup read X half as often, one
 // gives more workgroups (16 x 4096 x 4096 7.9 and 7.2; 24 x 4096 x 4096 7.4 and 9.6; 16 x
 // 49152 x 12288 131 and 159).
-Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool wide, bool direct) {
+Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool y16, bool direct) {
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
   if (grouped) {
     // By the rows that an expert has on average, and rows long enough for the eight
@@ -616,10 +531,10 @@ Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped
   }
   // Experts with fewer rows than a tile take a whole one each.
   const int64_t e = grouped ? experts : 0, least = grouped ? std::min(experts, rows) : 0;
-  const TileChoice c = direct ? wide ? choose_tiles(kWideTileShapes, m, n, rows, e, 4.0, 0.2e-6, least)
-                                     : choose_tiles(kTileShapes, m, n, rows, e, 4.0, 0.2e-6, least)
-                       : wide ? choose_tiles(kWideRaggedTileShapes, m, n, rows, e, 6.0, 0.14e-6, least)
-                              : choose_tiles(kRaggedTileShapes, m, n, rows, e, 6.0, 0.14e-6, least);
+  const TileChoice c =
+      !direct ? choose_tiles(kRaggedTileShapes, m, n, rows, e, kRaggedJoin, kRaggedJoinBytes, least, true)
+      : y16   ? choose_tiles(kTileShapes16, m, n, rows, e, kJoin, kJoinBytes, least, true)
+              : choose_tiles(kTileShapes, m, n, rows, e, kJoin, kJoinBytes, least, true);
   return Plan{(Kind)c.kind, c.splits};
 }
 
@@ -647,10 +562,10 @@ gptq_status in_row_parts(const Fp8Operands& p, int bm, int64_t slots, int thread
   return GPTQ_OK;
 }
 
-template <bool WIDE, int WR, int WC, int RB, int CB, int NB, bool DIRECT>
+template <bool Y16, int WR, int WC, int RB, int CB, int NB, bool DIRECT>
 gptq_status launch_tile(const Fp8Operands& p, const Plan& pl, void* ws, hipStream_t st) {
   constexpr int BM = 32 * WR * RB, BN = 32 * WC * CB, lds = tile_lds<WR, WC, RB, CB, NB>();
-  const auto k = fp8_tile_kernel<WIDE, WR, WC, RB, CB, NB, DIRECT>;
+  const auto k = fp8_tile_kernel<Y16, WR, WC, RB, CB, NB, DIRECT>;
   const int64_t cols = round_up(std::max<int64_t>(ceil_div(p.n, pl.splits), 1), kSplitCols);
   // Whole splits can leave fewer of them than were asked for.
   const int splits = (int)std::max<int64_t>(ceil_div(p.n, cols), 1);
@@ -677,10 +592,10 @@ uint64_t row_starts(const Fp8Operands& p) {
          (uint64_t)(p.m > 1 ? p.ldw : 0) | (uint64_t)p.w_stride;
 }
 
-template <bool WIDE, int WR, int WC, int RB, int CB, int NB>
+template <bool Y16, int WR, int WC, int RB, int CB, int NB>
 gptq_status launch_tiles(const Fp8Operands& p, const Plan& pl, void* ws, hipStream_t st) {
-  if ((row_starts(p) & 15) == 0) return launch_tile<WIDE, WR, WC, RB, CB, NB, true>(p, pl, ws, st);
-  return launch_tile<WIDE, WR, WC, RB, CB, 2, false>(p, pl, ws, st);
+  if ((row_starts(p) & 15) == 0) return launch_tile<Y16, WR, WC, RB, CB, NB, true>(p, pl, ws, st);
+  return launch_tile<Y16, WR, WC, RB, CB, 2, false>(p, pl, ws, st);
 }
 
 template <int RT, int CT, int D>
@@ -693,10 +608,10 @@ gptq_status launch_rows(const Fp8Operands& p, hipStream_t st) {
   });
 }
 
-template <bool WIDE>
+template <bool Y16>
 gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, hipStream_t st) {
   const bool direct = (row_starts(p) & 15) == 0;
-  Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, WIDE, direct);
+  Plan pl = make_plan(p.m, p.n, p.rows, p.experts, p.offsets != nullptr, Y16, direct);
   // The tile kernels address the rows of a tile with 32 bits; rows further apart
   // take the row kernel.
   constexpr int64_t kMaxPitch = (int64_t)1 << 22;
@@ -706,11 +621,11 @@ gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, hipStream_t 
   if (need > 0 && (reinterpret_cast<uintptr_t>(ws) & 3) != 0) return GPTQ_ERR_INVALID_ARG;
   switch (pl.kind) {
     case kTile256x256:
-      if constexpr (!WIDE) return launch_tile<WIDE, 4, 2, 2, 4, 2, true>(p, pl, ws, st);
+      if constexpr (Y16) return launch_tile<Y16, 4, 2, 2, 4, 2, true>(p, pl, ws, st);
       [[fallthrough]];
-    case kTile128x128: return launch_tiles<WIDE, 2, 2, 2, 2, 2>(p, pl, ws, st);
-    case kTile128x64: return launch_tiles<WIDE, 4, 1, 1, 2, 3>(p, pl, ws, st);
-    case kTile128x32: return launch_tiles<WIDE, 4, 1, 1, 1, 4>(p, pl, ws, st);
+    case kTile128x128: return launch_tiles<Y16, 2, 2, 2, 2, 2>(p, pl, ws, st);
+    case kTile128x64: return launch_tiles<Y16, 4, 1, 1, 2, 3>(p, pl, ws, st);
+    case kTile128x32: return launch_tiles<Y16, 4, 1, 1, 1, 4>(p, pl, ws, st);
     case kRows1: return launch_rows<1, 1, 4>(p, st);
     case kRows4x2: return launch_rows<4, 2, 1>(p, st);
     default: return launch_rows<2, 1, 2>(p, st);
@@ -719,7 +634,7 @@ gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, hipStream_t 
 
 gptq_status launch(const Fp8Operands& p, void* ws, size_t ws_bytes, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return p.y_dtype == GPTQ_F32 ? launch<true>(p, ws, ws_bytes, st) : launch<false>(p, ws, ws_bytes, st);
+  return p.y_dtype == GPTQ_F32 ? launch<false>(p, ws, ws_bytes, st) : launch<true>(p, ws, ws_bytes, st);
 }
 
 constexpr int64_t kMaxLd = (int64_t)1 << 40; // products of strides and indexes stay below 2^62
@@ -752,9 +667,9 @@ extern "C" size_t gptq_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t rows, i
   // by expert need none.
   if (experts > 1) return 0;
   size_t need = 0;
-  for (int wide = 0; wide < 2; ++wide)
+  for (int y16 = 0; y16 < 2; ++y16)
     for (int direct = 0; direct < 2; ++direct)
-      need = std::max(need, plan_ws(make_plan(m, n, rows, 1, false, wide != 0, direct != 0), m, rows));
+      need = std::max(need, plan_ws(make_plan(m, n, rows, 1, false, y16 != 0, direct != 0), m, rows));
   return need;
 }
 

@@ -205,7 +205,7 @@ inline int64_t max_tiles(int64_t rows, int64_t experts, bool grouped, int tile) 
 // round with as many as the CUs hold at once, and the join with its splits' sums
 // (a launch, and the bytes that they move).  A round's time grows from `one` (a
 // workgroup a CU) to `full` along a square root (a few CUs with two already hold
-// the rest up).  Grouped by expert (experts > 0): half a tile more for every expert
+// the rest up), or at_once: it is `full` as soon as one CU has two.  Grouped by expert (experts > 0): half a tile more for every expert
 // that can have rows, `least_tiles` of X rows at least, and no splits.
 struct TileShape {
   int kind;                                  // of the caller
@@ -218,7 +218,7 @@ struct TileChoice {
 constexpr int kSplitCols = 256;              // a split is a multiple of this
 template <size_t N>
 TileChoice choose_tiles(const TileShape (&shapes)[N], int64_t m, int64_t n, int64_t rows, int64_t experts,
-                        double join, double join_bytes, int64_t least_tiles = 0) {
+                        double join, double join_bytes, int64_t least_tiles = 0, bool at_once = false) {
   const int max_splits = experts > 0 ? 1 : 16;
   TileChoice best{shapes[0].kind, 1};
   double least = std::numeric_limits<double>::infinity();
@@ -229,7 +229,7 @@ TileChoice choose_tiles(const TileShape (&shapes)[N], int64_t m, int64_t n, int6
     for (int splits = 1; splits <= max_splits && (splits == 1 || n >= (int64_t)splits * kSplitCols); ++splits) {
       const int64_t groups = tiles * splits, rest = groups % held;
       double t = (double)(groups / held) * s.full;
-      if (rest > 256) t += s.one + (s.full - s.one) * std::sqrt((double)(rest - 256) * (1.0 / 256));
+      if (rest > 256) t += at_once ? s.full : s.one + (s.full - s.one) * std::sqrt((double)(rest - 256) * (1.0 / 256));
       else if (rest > 0) t += s.one;
       t = s.launch + t * (double)ceil_div(ceil_div(n, splits), kSplitCols);
       if (splits > 1) t += join + join_bytes * splits * parts;
