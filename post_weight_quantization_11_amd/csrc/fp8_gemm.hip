@@ -502,15 +502,19 @@ constexpr TileShape kRaggedTileShapes[] = {
 };
 constexpr double kRaggedJoin = 4.6, kRaggedJoinBytes = 0.16e-6;
 
-// The row kernels take up to 16 rows of X and whatever is small (us, against tiles: 16
-// x 12288 x 12288 43 / 45, 24 x 12288 x 12288 51 / 42; 96 x 4096 x 4096 14 / 15; 48 x
-// 11008 x 4096 23 / 27, 64 x 11008 x 4096 27 / 24; 128 x 2048 x 2048 5.8 / 10), unless
-// short rows leave their many workgroups little each (256 x 2048 x 2048 9.5 / 8.4, 512 x
-// 1024 x 1024 8.0 / 6.0, 256 x 8192 x 512 23 / 6.3).  Of rows that are not 16-byte
-// aligned they take less (16 x 4099 x 4097 13 / 15, 24 x 4099 x 4097 17 / 15; 128 x 1030 x
-// 2044 8.4 / 11, 256 x 1030 x 2043 13 / 13).  Two tiles of W a workgroup read X half as often, one
-// gives more workgroups (16 x 4096 x 4096 7.9 and 7.2; 24 x 4096 x 4096 7.4 and 9.6; 16 x
-// 49152 x 12288 131 and 159).
+// The row kernels take up to 16 rows of X and whatever is small: their time goes with
+// their workgroups' columns, of 32 rows of W and 16 of X each and about 700 more to
+// start (us, against tiles: 32 x 11008 x 4096 18.0 / 18.7, 34 x 11008 x 4096 21.8 / 20.5, 48
+// x 11008 x 4096 22.4 / 21.4; 96 x 4096 x 4096 14 / 17, 200 x 4096 x 4096 25 / 21; 17 x
+// 4096 x 11008 17 / 18, 33 x 4096 x 11008 23 / 20; 24 x 12288 x 12288 52 / 41; 256 x 2048 x
+// 2048 9.6 / 11.5, 512 x 2048 x 2048 17 / 12), unless short rows leave their many
+// workgroups little each (24 x 8192 x 512 4.4 / 5.5, 64 x 8192 x 512 7.1 / 5.5; 256 x 1024
+// x 1024 4.7 / 7.3, 512 x 1024 x 1024 7.9 / 7.6).  On the slower side are 128 x 4096 x 4096
+// (19.2 on tiles, 17.1) and 640 x 300 x 8208 (20.2 on rows, 17.5).  Of rows that are not
+// 16-byte aligned they take less (16 x 4099 x 4097 13 / 15, 24 x 4099 x 4097 15 / 14; 128 x
+// 1030 x 2044 8.3 / 12, 256 x 1030 x 2043 13 / 14).  Two tiles of W a workgroup read X
+// half as often, one gives more workgroups (16 x 4096 x 4096 7.9 and 7.2; 24 x 4096 x
+// 4096 7.5 and 10.3; 16 x 49152 x 12288 131 and 159).
 Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool y16, bool direct) {
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
   if (grouped) {
@@ -526,7 +530,8 @@ Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped
     // tiles take rows straight to LDS 64 of 1408 x 2048 with 24 59 / 45).
     if (rows > 12 * experts && rows <= 32 * experts && touched * ceil_div(m, 64) >= 256 && n >= (direct ? 4096 : 2000))
       return Plan{kRows4x2, 1};
-  } else if (rows <= 16 || (direct ? products <= 1500000000 && outputs <= 160 * n : products <= 400000000)) {
+  } else if (rows <= 16 || (direct ? ceil_div(m, 32) * ceil_div(rows, 16) * (n + 700) <= 4000000 && outputs <= 400 * n
+                                   : products <= 400000000)) {
     return Plan{outputs <= 65536 && m < 8192 ? kRows1 : kRows2, 1};
   }
   // Experts with fewer rows than a tile take a whole one each.

@@ -1,0 +1,44 @@
+"""Plans of the 8-bit products at sizes that were measured on several kernels,
+recorded without a GPU."""
+import pytest
+
+from tests import launch_recorder
+from tests.test_fp8_launches import BF16, F16, F32, _gemm, _kind, _record
+
+ROWS = "rows"
+
+
+@pytest.fixture(scope="module")
+def recorder(tmp_path_factory):
+    return launch_recorder.build(str(tmp_path_factory.mktemp("recorder")))
+
+
+# Rows of X, of W and columns, and the kernel that measured faster: rows, or a tile and
+# its splits of the columns.
+MEASURED = [
+    # us on rows and on the tiles: 17.8 / 18.3, then 21.8 / 20.5, 22.0 / 20.8, 22.4 / 21.4, 26.1 / 21.7, 26.8 / 22.1
+    (28, 11008, 4096, (ROWS, 1)), (34, 11008, 4096, (128, 64, 2)), (40, 11008, 4096, (128, 64, 2)),
+    (48, 11008, 4096, (128, 64, 2)), (56, 11008, 4096, (128, 64, 2)), (64, 11008, 4096, (128, 64, 2)),
+    # 13.5 / 16.2, 14.1 / 16.9, 17.0 / 18.0, 23.4 / 19.8
+    (77, 4096, 4096, (ROWS, 1)), (96, 4096, 4096, (ROWS, 1)), (17, 4096, 11008, (ROWS, 1)), (33, 4096, 11008, (128, 64, 8)),
+    # 4.7 / 7.3, 9.6 / 11.5, 16.9 / 11.9, 4.4 / 5.5, 7.1 / 5.5
+    (256, 1024, 1024, (ROWS, 1)), (256, 2048, 2048, (ROWS, 1)), (512, 2048, 2048, (128, 32, 1)), (24, 8192, 512, (ROWS, 1)),
+    (64, 8192, 512, (128, 32, 1)),
+    # 128 x 128 with four splits 101, 128 x 64 with two 122
+    (256, 12288, 12288, (128, 128, 4)), (1024, 11008, 4096, (128, 128, 1)),
+]
+
+
+@pytest.mark.parametrize("rows,m,n,want", MEASURED)
+@pytest.mark.parametrize("out", [F32, F16, BF16])
+def test_the_plan_is_the_faster_one(recorder, rows, m, n, want, out):
+    rc, launches = _record(recorder, [_gemm(m, n, rows, out)])[0]
+    kind = _kind(launches[0][0])
+    assert rc == 0
+    if kind[0] == ROWS:
+        got = (ROWS, len(launches))
+    else:
+        tiles = -(-m // kind[0]) * -(-rows // kind[1])
+        got = (*kind, max(s for s in range(1, 17) if -(-tiles * s // 8) * 8 == launches[0][1][0]))
+        assert len(launches) == (1 if got[2] == 1 else 2)
+    assert got == want
