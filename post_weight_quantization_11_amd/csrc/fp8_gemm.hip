@@ -472,35 +472,35 @@ struct Plan {
 };
 
 // Fitted to 95 sizes from 20 x 91 x 1824 to 4096 x 12288 x 12288: what the model chooses
-// takes 1.005 times the fastest shape's time in the mean, 1.1 at worst (24 x 12288 x
-// 12288: 45 us, 41 on 128 x 64).  Some of the measured pairs, the chosen first: 40 x
-// 11008 x 4096 on 128 x 64 with two splits (172 workgroups) 20.8, with three (258, two
-// CUs with two each) 25.9, with one 27.2; 77 x 4096 x 11008 on 128 x 64 with four 25.9,
-// 128 x 128 with four 34; 512 x 4096 x 4096 on 128 x 64 28, 128 x 128 40; 2048 x 4096 x
-// 4096 on 128 x 128 71, 256 x 256 116.
+// takes 1.005 times the fastest shape's time in the mean, 1.1 at worst (128 x 4096 x
+// 4096: 19.2 us on 128 x 64 with four splits, 17.6 on 128 x 32 with two).  Some of the
+// measured pairs, the chosen first: 40 x 11008 x 4096 on 128 x 64 with two splits (172
+// workgroups) 20.8, with three (258, two CUs with two each) 25.9, with one 27.2; 77 x
+// 4096 x 11008 on 128 x 64 with four 25.9, 128 x 128 with four 34; 512 x 4096 x 4096 on
+// 128 x 64 28, 128 x 128 40; 2048 x 4096 x 4096 on 128 x 128 71, 256 x 256 116.
 constexpr TileShape kTileShapes[] = {
-    {kTile128x32, 128, 32, 2, 3.58, 1.11, 2.6},
-    {kTile128x64, 128, 64, 2, 4.29, 1.3, 2.78},
-    {kTile128x128, 128, 128, 2, 4.55, 2.41, 3.72},
+    {kTile128x32, 128, 32, 2, 1.77, 1.07, 2.32, 3.0},
+    {kTile128x64, 128, 64, 2, 3.76, 1.31, 2.37, 0.84},
+    {kTile128x128, 128, 128, 2, 3.65, 2.37, 3.69, 0.49},
 };
 // Of a 16-bit Y (4096 x 4096 x 4096 on 256 x 256 124 us, 128 x 128 132; 4096 x 12288 x
 // 12288 1051 and 1147; 2100 x 6200 x 400 26 and 29).
 constexpr TileShape kTileShapes16[] = {
-    {kTile128x32, 128, 32, 2, 3.58, 1.11, 2.6},
-    {kTile128x64, 128, 64, 2, 4.29, 1.3, 2.78},
-    {kTile128x128, 128, 128, 2, 4.55, 2.41, 3.72},
-    {kTile256x256, 256, 256, 1, 4.72, 7.01, 7.01},
+    {kTile128x32, 128, 32, 2, 1.77, 1.07, 2.32, 3.0},
+    {kTile128x64, 128, 64, 2, 3.76, 1.31, 2.37, 0.84},
+    {kTile128x128, 128, 128, 2, 3.65, 2.37, 3.69, 0.49},
+    {kTile256x256, 256, 256, 1, 4.41, 6.97, 6.97, 0.72},
 };
-constexpr double kJoin = 3.4, kJoinBytes = 0.27e-6;
+constexpr double kJoin = 3.74, kJoinBytes = 0.25e-6;
 
 // Rows through registers.  Fitted to 27 sizes from 17 x 4099 x 4097 to 2048 x 4099 x
 // 4097: 1.02 times the fastest in the mean, 1.1 at worst.
 constexpr TileShape kRaggedTileShapes[] = {
-    {kTile128x32, 128, 32, 2, 1.88, 2.22, 2.62},
-    {kTile128x64, 128, 64, 2, 2.49, 2.75, 3.22},
-    {kTile128x128, 128, 128, 2, 1.95, 3.63, 4.67},
+    {kTile128x32, 128, 32, 2, 1.04, 1.97, 2.54, 0.1},
+    {kTile128x64, 128, 64, 2, 1.09, 2.98, 3.8, 0.32},
+    {kTile128x128, 128, 128, 2, 1.37, 4.05, 4.59, 0.1},
 };
-constexpr double kRaggedJoin = 4.6, kRaggedJoinBytes = 0.16e-6;
+constexpr double kRaggedJoin = 6.35, kRaggedJoinBytes = 0.16e-6;
 
 // The row kernels take up to 16 rows of X and whatever is small: their time goes with
 // their workgroups' columns, of 32 rows of W and 16 of X each and about 700 more to
@@ -517,29 +517,46 @@ constexpr double kRaggedJoin = 4.6, kRaggedJoinBytes = 0.16e-6;
 // 4096 7.5 and 10.3; 16 x 49152 x 12288 131 and 159).
 Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped, bool y16, bool direct) {
   const int64_t outputs = m * rows, products = outputs * std::max<int64_t>(n, 1);
+  // Tiles of bn rows of X that the experts' rows form: as a geometric distribution has
+  // them (all of an expert's rows in one tile where they are few, half a tile more where
+  // they are many).
+  const int64_t touched = std::min(experts, rows);
+  const auto expert_tiles = [&](int bn) {
+    return (double)touched / -std::expm1(-(double)bn * (double)touched / (double)rows);
+  };
   if (grouped) {
-    // By the rows that an expert has on average, and rows long enough for the eight
-    // waves (us, against tiles: 8 experts of 11008 x 4096 with 12 rows each 71 / 94, with
-    // 24 103 / 95; 64 of 1030 x 2044 with 8 43 / 44; 64 of 2048 x 1024 with 4 40 / 32;
-    // 100 of 512 x 512 with 1 17 / 10; one of 512 x 512 3.4 / 4.2).
-    const int64_t touched = std::min(experts, rows);
-    if (rows <= 12 * experts && (rows <= 16 || n >= 2000 || touched * m * n <= ((int64_t)1 << 22)))
+    // By the rows that an expert has on average, and more columns than a block for each of
+    // the eight waves (us, against tiles: 8 experts of 11008 x 4096 with 8 rows each 68 /
+    // 99, with 14 79 / 93; 64 of 1030 x 1024 with 8 25 / 23, 1030 x 1100 31 / 35, 1030 x 1300
+    // 34 / 39, 1030 x 1999 43 / 50; at odd addresses 28 / 27, 34 / 31, 37 / 37, 48 / 49 and
+    // 1408 x 1536 43 / 53; 64 of 2048 x 1024 with 4 40 / 32; 100 of 512 x 512 with 8 16 /
+    // 11; one of 512 x 512 3.4 / 4.2).
+    constexpr int64_t kColsAll = kRowWaves * kFp8Block;
+    if (rows <= 12 * experts && (rows <= 16 || n > kColsAll || touched * m * n <= ((int64_t)1 << 22)))
       return Plan{touched * ceil_div(m, 32) < 256 ? kRows1 : kRows2, 1};
-    // Thirty-two rows of X a workgroup: the weights once (8 of 11008 x 4096 with 32 92 /
-    // 112, with 48 128 / 112; 64 of 1030 x 2044 with 24 56 / 60, with 32 58 / 69; where
-    // tiles take rows straight to LDS 64 of 1408 x 2048 with 24 59 / 45).
-    if (rows > 12 * experts && rows <= 32 * experts && touched * ceil_div(m, 64) >= 256 && n >= (direct ? 4096 : 2000))
+    // Thirty-two rows of X a workgroup: the weights once.  Where tiles go through registers
+    // from three quads of columns on (64 experts of 1030 x 1100 with 24 rows each 50 / 46,
+    // 1030 x 1300 53 / 54, 1030 x 1540 54 / 60, 1030 x 1999 63 / 72, 1408 x 4096 123 / 151),
+    // where they take rows straight to LDS from eight (1408 x 2304 72 / 55, 1030 x 2560 56 /
+    // 55, 1030 x 4096 73 / 84; 8 of 11008 x 4096 with 32 101 / 115).
+    if (rows > 12 * experts && rows <= 32 * experts && touched * ceil_div(m, 64) >= 256 && n >= (direct ? 8 : 3) * 512)
       return Plan{kRows4x2, 1};
   } else if (rows <= 16 || (direct ? ceil_div(m, 32) * ceil_div(rows, 16) * (n + 700) <= 4000000 && outputs <= 400 * n
                                    : products <= 400000000)) {
     return Plan{outputs <= 65536 && m < 8192 ? kRows1 : kRows2, 1};
   }
-  // Experts with fewer rows than a tile take a whole one each.
-  const int64_t e = grouped ? experts : 0, least = grouped ? std::min(experts, rows) : 0;
+  // A quarter more than the geometric distribution's, as the fit has it.  Over 190 measured
+  // pairs of sizes and alignments that take tiles, rows spread twofold, the shape chosen
+  // takes 1.02 times the fastest's time in the mean, 1.4 at worst (64 experts of 1030 x 1100
+  // with 20 rows each at odd addresses 45 us on 128 x 32, 33 on 128 x 64).
+  const auto groups = [&](int64_t w_tiles, int bn) {
+    return (int64_t)std::ceil(1.25 * (double)w_tiles * expert_tiles(bn));
+  };
+  const int64_t e = grouped ? experts : 0;
   const TileChoice c =
-      !direct ? choose_tiles(kRaggedTileShapes, m, n, rows, e, kRaggedJoin, kRaggedJoinBytes, least, true)
-      : y16   ? choose_tiles(kTileShapes16, m, n, rows, e, kJoin, kJoinBytes, least, true)
-              : choose_tiles(kTileShapes, m, n, rows, e, kJoin, kJoinBytes, least, true);
+      !direct ? choose_tiles(kRaggedTileShapes, m, n, rows, e, groups, kRaggedJoin, kRaggedJoinBytes, true)
+      : y16   ? choose_tiles(kTileShapes16, m, n, rows, e, groups, kJoin, kJoinBytes, true)
+              : choose_tiles(kTileShapes, m, n, rows, e, groups, kJoin, kJoinBytes, true);
   return Plan{(Kind)c.kind, c.splits};
 }
 

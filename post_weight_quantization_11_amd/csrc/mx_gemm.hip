@@ -1250,7 +1250,11 @@ constexpr TileShape kScaledTileShapes[] = {
 constexpr TileShape kGroupedTileShapes[] = {kTileShapes[0], kTileShapes[2]};
 template <size_t N>
 Plan tile_plan(const TileShape (&shapes)[N], int64_t m, int64_t n, int64_t rows, int64_t experts = 0) {
-  const TileChoice c = choose_tiles(shapes, m, n, rows, experts, 4.3, 0.22e-6);
+  // Half a tile more for every expert that can have rows.
+  const auto groups = [&](int64_t w_tiles, int bn) {
+    return w_tiles * (ceil_div(rows, bn) + (std::min(experts, rows) + 1) / 2);
+  };
+  const TileChoice c = choose_tiles(shapes, m, n, rows, experts, groups, 4.3, 0.22e-6, false);
   return Plan{(Kind)c.kind, c.splits};
 }
 

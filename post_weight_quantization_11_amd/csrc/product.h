@@ -202,36 +202,38 @@ inline int64_t max_tiles(int64_t rows, int64_t experts, bool grouped, int tile) 
 
 // Products on tiles: the shape and the splits of the columns with the least time by
 // this model, in us: a launch, 256 columns of every round of workgroups, each
-// round with as many as the CUs hold at once, and the join with its splits' sums
-// (a launch, and the bytes that they move).  A round's time grows from `one` (a
+// round with as many as the CUs hold at once, what a round takes beside them, and
+// the join with its splits' sums (a launch, and the bytes that they move).  A round's time grows from `one` (a
 // workgroup a CU) to `full` along a square root (a few CUs with two already hold
-// the rest up), or at_once: it is `full` as soon as one CU has two.  Grouped by expert (experts > 0): half a tile more for every expert
-// that can have rows, `least_tiles` of X rows at least, and no splits.
+// the rest up), or at_once: it is `full` as soon as one CU has two.  experts: 0, or of
+// products grouped by expert, which have no splits; expert_groups(tiles of W, rows of X
+// of a tile): their workgroups.
 struct TileShape {
   int kind;                                  // of the caller
   int bm, bn, per_cu;                        // rows of W and of X, workgroups a CU holds
   double launch, one, full;
+  double round = 0;                          // what every round takes beside its columns
 };
 struct TileChoice {
   int kind, splits;
 };
 constexpr int kSplitCols = 256;              // a split is a multiple of this
-template <size_t N>
+template <size_t N, typename Groups>
 TileChoice choose_tiles(const TileShape (&shapes)[N], int64_t m, int64_t n, int64_t rows, int64_t experts,
-                        double join, double join_bytes, int64_t least_tiles = 0, bool at_once = false) {
+                        Groups expert_groups, double join, double join_bytes, bool at_once) {
   const int max_splits = experts > 0 ? 1 : 16;
   TileChoice best{shapes[0].kind, 1};
   double least = std::numeric_limits<double>::infinity();
   const double parts = (double)m * (double)rows * 8.0;       // bytes that a split's sums move
   for (const TileShape& s : shapes) {
-    const int64_t partial = (std::min(experts, rows) + 1) / 2, held = 256 * s.per_cu;
-    const int64_t tiles = ceil_div(m, s.bm) * std::max(ceil_div(rows, s.bn) + partial, least_tiles);
+    const int64_t held = 256 * s.per_cu, w_tiles = ceil_div(m, s.bm);
+    const int64_t tiles = experts > 0 ? expert_groups(w_tiles, s.bn) : w_tiles * ceil_div(rows, s.bn);
     for (int splits = 1; splits <= max_splits && (splits == 1 || n >= (int64_t)splits * kSplitCols); ++splits) {
       const int64_t groups = tiles * splits, rest = groups % held;
       double t = (double)(groups / held) * s.full;
       if (rest > 256) t += at_once ? s.full : s.one + (s.full - s.one) * std::sqrt((double)(rest - 256) * (1.0 / 256));
       else if (rest > 0) t += s.one;
-      t = s.launch + t * (double)ceil_div(ceil_div(n, splits), kSplitCols);
+      t = s.launch + s.round * (double)ceil_div(groups, held) + t * (double)ceil_div(ceil_div(n, splits), kSplitCols);
       if (splits > 1) t += join + join_bytes * splits * parts;
       if (t < least) least = t, best = TileChoice{s.kind, splits};
       if (groups > 2 * held) break;          // more splits only add sums

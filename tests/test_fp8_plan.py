@@ -3,7 +3,7 @@ recorded without a GPU."""
 import pytest
 
 from tests import launch_recorder
-from tests.test_fp8_launches import BF16, F16, F32, _gemm, _kind, _record
+from tests.test_fp8_launches import BF16, F16, F32, _gemm, _grouped, _kind, _record
 
 ROWS = "rows"
 
@@ -42,3 +42,28 @@ def test_the_plan_is_the_faster_one(recorder, rows, m, n, want, out):
         got = (*kind, max(s for s in range(1, 17) if -(-tiles * s // 8) * 8 == launches[0][1][0]))
         assert len(launches) == (1 if got[2] == 1 else 2)
     assert got == want
+
+
+# Experts, all rows of X (spread over the experts by popularities), of W, columns, bytes
+# from row to row, and the kernel that measured faster.
+GROUPED = [
+    # us on rows and on the tiles: 33.8 / 39.0, 36.4 / 37.9, 43.2 / 49.6
+    (64, 512, 1030, 1300, 1312, (ROWS, 2)), (64, 512, 1408, 1536, 1536, (ROWS, 2)), (64, 512, 1030, 1999, 2000, (ROWS, 2)),
+    # rows at odd addresses, 64 rows of W a workgroup: 49.8 / 45.6, 53.7 / 60.0, 62.8 / 72.3
+    (64, 1536, 1030, 1100, 1101, "tiles"), (64, 1536, 1030, 1540, 1541, (ROWS, 4)), (64, 1536, 1030, 1999, 1999, (ROWS, 4)),
+    # aligned: 73.1 / 83.6, 72.3 / 54.6
+    (64, 1536, 1030, 4096, 4096, (ROWS, 4)), (64, 1536, 1408, 2304, 2304, (128, 64)),
+    # 128 x 64 24.2, 128 x 32 30.5; 128 x 64 144, 128 x 128 141, 256 x 256 238; 128 x 128 767, 256 x 256 843;
+    # 128 x 128 15.0, 128 x 32 22.4
+    (64, 896, 1030, 1024, 1024, (128, 64)), (8, 3000, 4096, 4096, 4096, 128),
+    (8, 8192, 11008, 4096, 4096, (128, 128)), (100, 3200, 512, 512, 512, (128, 128)),
+]
+
+
+@pytest.mark.parametrize("experts,rows,m,n,ld,want", GROUPED)
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_the_plan_by_expert_is_the_faster_one(recorder, experts, rows, m, n, ld, want, out):
+    rc, launches = _record(recorder, [_grouped(experts, m, n, rows, out, ld)])[0]
+    kind = _kind(launches[0][0])
+    assert rc == 0 and len(launches) == 1
+    assert kind == want or kind[0] == want or (want == "tiles" and kind[0] != ROWS)
