@@ -532,8 +532,9 @@ Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped
     // 1408 x 1536 43 / 53; 64 of 2048 x 1024 with 4 40 / 32; 100 of 512 x 512 with 8 16 /
     // 11; one of 512 x 512 3.4 / 4.2).
     constexpr int64_t kColsAll = kRowWaves * kFp8Block;
-    if (rows <= 12 * experts && (rows <= 16 || n > kColsAll || touched * m * n <= ((int64_t)1 << 22)))
-      return Plan{touched * ceil_div(m, 32) < 256 ? kRows1 : kRows2, 1};
+    const double row_groups = (double)ceil_div(m, 32) * expert_tiles(16);
+    const Plan by_rows{row_groups < 128 ? kRows1 : kRows2, 1};
+    if (rows <= 12 * experts && (rows <= 16 || n > kColsAll || touched * m * n <= ((int64_t)1 << 22))) return by_rows;
     // Thirty-two rows of X a workgroup: the weights once.  Where tiles go through registers
     // from three quads of columns on (64 experts of 1030 x 1100 with 24 rows each 50 / 46,
     // 1030 x 1300 53 / 54, 1030 x 1540 54 / 60, 1030 x 1999 63 / 72, 1408 x 4096 123 / 151),
@@ -541,6 +542,11 @@ Plan make_plan(int64_t m, int64_t n, int64_t rows, int64_t experts, bool grouped
     // 55, 1030 x 4096 73 / 84; 8 of 11008 x 4096 with 32 101 / 115).
     if (rows > 12 * experts && rows <= 32 * experts && touched * ceil_div(m, 64) >= 256 && n >= (direct ? 8 : 3) * 512)
       return Plan{kRows4x2, 1};
+    // Whatever else is small, as one matrix's below, with any number of rows (2 experts of
+    // 128 x 5312 with 60 rows each 6.3 / 27, at odd addresses 7.9 / 53; 20 of 172 x 9051
+    // with 23 20 / 44; 3 of 3780 x 1062 with 49 18 / 11; on the slower side 5 of 1205 x 1929
+    // with 73, 17 / 15, and 3 of 3634 x 8944 with 55 at odd addresses, 65 / 106).
+    if (outputs <= 400 * n && row_groups * (double)(n + 700) <= 5e6) return by_rows;
   } else if (rows <= 16 || (direct ? ceil_div(m, 32) * ceil_div(rows, 16) * (n + 700) <= 4000000 && outputs <= 400 * n
                                    : products <= 400000000)) {
     return Plan{outputs <= 65536 && m < 8192 ? kRows1 : kRows2, 1};

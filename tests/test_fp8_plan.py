@@ -54,9 +54,13 @@ GROUPED = [
     # aligned: 73.1 / 83.6, 72.3 / 54.6
     (64, 1536, 1030, 4096, 4096, (ROWS, 4)), (64, 1536, 1408, 2304, 2304, (128, 64)),
     # 128 x 64 24.2, 128 x 32 30.5; 128 x 64 144, 128 x 128 141, 256 x 256 238; 128 x 128 767, 256 x 256 843;
-    # 128 x 128 15.0, 128 x 32 22.4
+    # 128 x 128 15.0, 128 x 32 22.4; many rows an expert, but small: 6.3 / 27, 19.6 / 44, 18.5 / 20, 17.5 / 11.4
     (64, 896, 1030, 1024, 1024, (128, 64)), (8, 3000, 4096, 4096, 4096, 128),
     (8, 8192, 11008, 4096, 4096, (128, 128)), (100, 3200, 512, 512, 512, (128, 128)),
+    (2, 120, 128, 5312, 5312, (ROWS, 1)), (20, 457, 172, 9051, 9056, (ROWS, 2)), (20, 683, 488, 3162, 3168, (ROWS, 2)),
+    (3, 147, 3780, 1062, 1072, "tiles"),
+    # at odd addresses: 7.9 / 53, 19.1 / 87, 24.5 / 51
+    (2, 120, 128, 5312, 5313, (ROWS, 1)), (20, 457, 172, 9051, 9051, (ROWS, 2)), (8, 1306, 256, 5376, 5377, (ROWS, 2)),
 ]
 
 
