@@ -3,7 +3,8 @@
 // with the experts and probabilities of the router, and G, U (rows of one stack)
 // and D microscaled or in block-scaled 8-bit floats.
 //
-// Slots: an expert with tokens has one for every fifteen of them.
+// Slots: an expert with tokens has one for every fifteen of them, and both launches
+// read its weights once a slot.
 //
 // First launch (moe_up_kernel): every workgroup routes all tokens itself (a wave a
 // token, the experts' tokens as 64-bit masks in LDS; more than sixteen tokens are
@@ -67,7 +68,7 @@ struct MoeArgs {
   int32_t* ids;                              // and their experts, where a launch before chose them
   bool chosen;
   int* slots;                                // their number, then the word of each
-  uint32_t* slot_pairs;                      // [slot][16]: pair, token in the upper half
+  uint32_t* slot_pairs;                      // [slot][kSlot]: pair, token in the upper half
   uint32_t* arrived;                         // a counter for each group of rows of D
   uint16_t* h;                               // [part of a slot][8 columns][token][plane][8], see h_at
   float* part;                               // [split][token][d]
@@ -582,7 +583,7 @@ __global__ __launch_bounds__(kThreads, 2) void moe_up_kernel(MoeArgs p) {
 // TAIL: f is no multiple of a unit.
 template <int WF, bool TAIL>
 __global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(MoeArgs p) {
-  constexpr int D = 1, kCols = Row<WF>::kCols, kSteps = Row<WF>::kSteps;
+  constexpr int kCols = Row<WF>::kCols, kSteps = Row<WF>::kSteps;
   constexpr int kParts = kSlot / kPart;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int pairs = p.tokens * p.k, most = max_slots(p.tokens, p.experts, p.k);
@@ -749,26 +750,20 @@ __global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(MoeArgs p) {
     int slot = lo / per_slot, u = lo - slot * per_slot, parts = parts_of(slot);
     at_slot = slot, at_unit = u, left = hi - lo;
     place(slot, at);
-    Unit ring[D];
-#pragma unroll
-    for (int i = 0; i < D; ++i) load(ring[i]);
+    Unit next;                               // a second one in flight gained nothing
+    load(next);
     clear();
-    for (int n = lo; n < hi; n += D) {
-#pragma unroll
-      for (int i = 0; i < D; ++i) {
-        if (n + i < hi) {
-          multiply(ring[i], u, parts);
-          ++u;
-          if (n + i + 1 == hi || u == per_slot) {
-            flush(slot, parts);
-            clear();
-            u = 0;
-            ++slot;
-            if (n + i + 1 < hi) parts = parts_of(slot);
-          }
-        }
-        load(ring[i]);
+    for (int n = lo; n < hi; ++n) {
+      multiply(next, u, parts);
+      ++u;
+      if (n + 1 == hi || u == per_slot) {
+        flush(slot, parts);
+        clear();
+        u = 0;
+        ++slot;
+        if (n + 1 < hi) parts = parts_of(slot);
       }
+      load(next);
     }
   }
   // Without a whole unit, a slot at a time.
