@@ -609,8 +609,9 @@ gptq_status gptq_moe_route(const void* logits, int l_dtype, int64_t tokens, int6
                            int32_t* order, void* stream);
 
 /* A layer of experts for up to GPTQ_MOE_MAX_TOKENS tokens (more take
- * gptq_moe_route and the products grouped by expert), in two launches (three with
- * more than 16 tokens):
+ * gptq_moe_route and the products grouped by expert, which are also faster where
+ * experts have more than about thirty tokens: the layer reads an expert's weights
+ * once for every fifteen), in two launches (three with more than 16 tokens):
  *   Y[t] = sum_j weights[t, j] D_e (silu(G_e X[t]) * (U_e X[t])),  e = ids[t, j],
  * with ids and weights as gptq_moe_route gives them for the logits, and
  * silu(a) = a / (1 + exp(-a)).
